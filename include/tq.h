@@ -55,7 +55,7 @@ typedef enum tq_status {
   TQ_ERR_DEVICE = 5 /* the device status word is non-zero (see tq_check_status) */
 } tq_status;
 
-typedef enum tq_dtype { TQ_BF16 = 0, TQ_F32 = 1 } tq_dtype;
+typedef enum tq_dtype { TQ_BF16 = 0, TQ_F32 = 1, TQ_F16 = 2 /* exact pools and attention only */ } tq_dtype;
 
 /* Device status word bits. */
 #define TQ_DEV_ERR_CAPACITY 0x1u /* an append would grow a sequence past max_ctx; the row was skipped */
@@ -64,6 +64,9 @@ typedef enum tq_dtype { TQ_BF16 = 0, TQ_F32 = 1 } tq_dtype;
 #define TQ_DEV_ERR_TIMEOUT 0x8u  /* a bounded wait on a bulk copy gave up; that split was dropped */
 #define TQ_DEV_ERR_BLOCK 0x10u   /* paged cache: a page that an append or decode touched has no valid block in
                                   * the block table; the append skipped it, the decode result is undefined */
+#define TQ_DEV_ERR_POOL 0x20u    /* block map: the pool has too few free blocks; the request got none */
+#define TQ_DEV_ERR_LENGTH 0x40u  /* an array of starts, lengths or counts does not fit its tensors; that request is
+                                  * taken as empty */
 
 /* Configuration. The key has key_bits bits per coordinate: a (key_bits - 1)-bit Lloyd-Max code plus 1 QJL
  * sign bit ([Guide] §二 steps 2-3; §五.1 key_bits=3). key_bits 4 is the 4-bit TurboQuant row of the
@@ -421,6 +424,121 @@ typedef enum tq_codec {
   TQ_CODEC_TQ_K3V4 = 4
 } tq_codec;
 size_t tq_codec_kv_bytes(int codec, int n_layers, int n_kv_heads, int head_dim, int64_t n_tokens);
+
+/* ---- Exact paged cache: block maps, appends and attention (stateless; no context) ----
+ * The layers that a model keeps in 16 bits beside the packed ones, the 16-bit row of every comparison, and the
+ * cross attention of encoder-decoder models. Pages hold 128 tokens, as the packed cache's do, so that one block
+ * table serves both (tq_block_table_offset, or a table of the caller's own).
+ *
+ * All arrays of ids, lengths, starts and slots are int32 on the device; the host reads none of them, and a call
+ * can be captured into a graph and replayed on new contents. d_status (may be NULL) is a caller's device word that
+ * gets TQ_DEV_ERR_* bits. Calls are ordered by the caller, as above. They are launched with programmatic dependent
+ * launch and wait for the stream's earlier work before they read or write anything.
+ *
+ * A pool's state: the block table [max_seqs][max_pages] (row stride table_stride entries; -1 = no block), a stack
+ * of free block ids d_free[n_blocks] of which the first *d_n_free are free (the last of them is the top). */
+
+/* tq_blocks_release: cuts the tables of requests back to their first d_keep[b] tokens (NULL: 0, the request ends).
+ * Every page from ceil(keep / 128) on that has a block gives it back: in the order of requests and pages, the first
+ * of them ends on top of the stack, so that a tq_blocks_map of the same requests takes the same blocks again. A
+ * stack that would pass n_blocks (a block freed twice) is left as it was, with TQ_DEV_ERR_POOL, and so are the
+ * tables. Requests with an id outside [0, max_seqs), an id that an earlier request has, or a negative keep are
+ * skipped with TQ_DEV_ERR_SEQ_ID (TQ_DEV_ERR_LENGTH for the keep). A table entry outside [-1, n_blocks) becomes -1
+ * with TQ_DEV_ERR_BLOCK. batch in [0, 4096]. One launch. */
+tq_status tq_blocks_release(int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride, int32_t* d_free,
+                            int n_blocks, int32_t* d_n_free, const int32_t* d_seq_ids, const int32_t* d_keep,
+                            int batch, uint32_t* d_status, tq_stream_t stream);
+
+/* tq_blocks_map: blocks and slots of one step's new tokens.
+ *   - d_lens[b], d_n_new[b]: the tokens that request b holds, and how many it adds. Its new tokens follow each
+ *     other at positions lens, lens + 1, ...; those of all requests are packed in request order.
+ *   - Every page in [ceil(lens / 128), ceil((lens + n_new) / 128)) without a block takes one from the top of the
+ *     stack, in the order of requests and pages. A page that has one keeps it.
+ *   - A request is served if it needs no block, or if the needs of all requests up to and with it fit the free
+ *     blocks. A refused one gets no block: its table stays, its slots are -1, its total is 0, and TQ_DEV_ERR_POOL
+ *     is set.
+ *   - d_starts[batch + 1]: the packed place of each request's first new token; d_starts[batch] is their number.
+ *   - d_totals[b]: lens + n_new (0 for a refused or skipped request): the lengths that attention takes.
+ *   - d_slots[max_tokens]: block * 128 + place in the block for each packed token; -1 for a token of a request
+ *     that is not served or whose page has no block (TQ_DEV_ERR_BLOCK), and behind the last token.
+ *   - A request with an id outside [0, max_seqs) or that an earlier request has (TQ_DEV_ERR_SEQ_ID), a negative
+ *     length or count, more than max_pages pages, or an end past max_tokens (TQ_DEV_ERR_LENGTH) is not served; its
+ *     tokens keep their places (none for a negative count), and starts never pass max_tokens.
+ * batch in [0, 4096], n_blocks <= 2^24. One launch. */
+tq_status tq_blocks_map(int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride, const int32_t* d_free,
+                        int n_blocks, int32_t* d_n_free, const int32_t* d_seq_ids, const int32_t* d_lens,
+                        const int32_t* d_n_new, int batch, int32_t* d_starts, int32_t* d_totals, int32_t* d_slots,
+                        int max_tokens, uint32_t* d_status, tq_stream_t stream);
+
+/* K and V of a cache or of an encoder's states: element (o, t, h, c) of K is at k + o * k_strides[0] +
+ * t * k_strides[1] + h * k_strides[2] + c, strides in elements. o is a block of a pool (tokens = 128), a request of
+ * padded states, or 0 for packed states (outer = 1, tokens = all rows). */
+typedef struct tq_kv {
+  void* k;
+  void* v;
+  int64_t k_strides[3];
+  int64_t v_strides[3];
+  int32_t outer;
+  int32_t tokens;
+  int32_t n_kv_heads;
+  int32_t head_dim; /* 64, 128 or 256 */
+  int32_t dtype;    /* TQ_BF16 or TQ_F16 */
+} tq_kv;
+
+/* tq_paged_append: writes n_tokens new rows of K and V into a pool: row t goes to block slots[t] / 128, place
+ * slots[t] % 128 (as tq_blocks_map gives them); -1 skips the row, any other slot outside the pool is skipped with
+ * TQ_DEV_ERR_BLOCK. k, v: [n_tokens][n_kv_heads][head_dim] of type dt (TQ_BF16, TQ_F16 or TQ_F32) at strides
+ * {row, head} in elements; each value is rounded to the pool's type once (to nearest even; a value past f16's range
+ * becomes infinite). Any alignment is served; 16-byte aligned rows are faster. Two rows with one slot leave values
+ * of either. One launch. */
+tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dtype dt, const int64_t* k_strides,
+                          const int64_t* v_strides, const int32_t* d_slots, int n_tokens, uint32_t* d_status,
+                          tq_stream_t stream);
+
+/* Queries and outputs of attention: packed rows [n_rows][n_q_heads][head_dim] of the cache's type at strides
+ * {row, head} in elements, 16-byte aligned rows. Rows [d_q_starts[b], d_q_starts[b + 1]) are request b's; rows
+ * behind the last request's are neither read nor written. Query head h attends KV head h / (n_q_heads /
+ * n_kv_heads); the quotient can be any whole number up to 1024. */
+typedef struct tq_queries {
+  const void* q;
+  void* out;
+  int64_t q_strides[2];
+  int64_t out_strides[2];
+  const int32_t* d_q_starts; /* [batch + 1] */
+  int32_t n_rows;
+  int32_t n_q_heads;
+  int32_t batch;       /* <= 65535 */
+  int32_t max_q;       /* no request has more rows (0: n_rows); one that has gets no output, TQ_DEV_ERR_SPLITS */
+  int32_t max_kv;      /* about the longest request's tokens to attend to (0: as many as fit); sizes the splits */
+  float softmax_scale; /* <= 0: 1 / sqrt(head_dim) */
+} tq_queries;
+
+/* tq_paged_attention: attention of new tokens over a paged cache that already holds them. Request b has
+ * n = starts[b + 1] - starts[b] queries and d_kv_lens[b] tokens, in the pages of table row d_seq_ids[b] (NULL: b).
+ * With causal = 1, query i sits at position kv_len - n + i and sees every token up to its own; with causal = 0 it
+ * sees all kv_len. softmax(scale q k) v in fp32 statistics; the weights are rounded to the cache's type for the
+ * product with V, the result once. A query that sees no token gets zeros. Pages may hold anything, also NaN,
+ * behind a request's tokens; a token that some query of the request sees has to be finite.
+ * A page without a block in the table reads as zeros (TQ_DEV_ERR_BLOCK); a bad id, length or start makes the
+ * request's outputs zeros or unwritten (TQ_DEV_ERR_SEQ_ID, TQ_DEV_ERR_LENGTH).
+ *   - K and V: base and strides a multiple of 16 bytes, positive (also where a size is 1, if read).
+ *   - workspace: tq_attention_workspace_bytes(q, kv, max_pages) bytes (max_pages 0 for cross attention), 256-byte
+ *     aligned, contents arbitrary. Calls that may
+ *     overlap on the GPU need workspaces of their own.
+ *   - Launches: one attention kernel, and one that joins the splits where the sequences are split. */
+size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv, int max_pages);
+tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_table, int max_seqs,
+                             int max_pages, int64_t table_stride, const int32_t* d_seq_ids, const int32_t* d_kv_lens,
+                             int causal, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
+                             tq_stream_t stream);
+
+/* tq_cross_attention: the same over an encoder's states, of another length than the queries, every state visible.
+ * Packed (kv->outer = 1, d_kv_starts[batch + 1] given): request b has rows [kv_starts[b], kv_starts[b + 1]).
+ * Padded (d_kv_starts NULL, kv->outer = batch, d_kv_lens[batch] given): request b has its first kv_lens[b] rows.
+ * No state gives zeros. States past a request's own may hold anything. */
+tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_kv_starts,
+                             const int32_t* d_kv_lens, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
+                             tq_stream_t stream);
 
 /* ---- Host-only inspection helpers (tests and tools; no device work) ---- */
 

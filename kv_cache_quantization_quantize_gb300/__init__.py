@@ -10,9 +10,9 @@ import torch
 
 from . import _abi
 from ._abi import TQConfig, TQError, check, load, TQ_BF16, TQ_F32
-from . import codecs
+from . import codecs, paged
 
-__all__ = ["TQConfig", "TQError", "TurboQuantCache", "HostTables", "load", "config", "codecs"]
+__all__ = ["TQConfig", "TQError", "TurboQuantCache", "HostTables", "load", "config", "codecs", "paged"]
 
 
 def config(head_dim=128, value_bits=2, n_layers=1, n_kv_heads=1, n_q_heads=1, max_seqs=1, max_ctx=1152, seed=0,
@@ -111,6 +111,7 @@ class TurboQuantCache(HostTables):
             self.cache_buf = torch.empty(cb, dtype=torch.uint8, device=self.device)
             check(self.lib.tq_cache_bind(self.ctx, _ptr(self.cache_buf), cb, _stream()))
         self._ws = None
+        self._pool = None
 
     # ---- hot path ----
     def append(self, layer, k, v, seq_ids, n_new, stream=None):
@@ -227,6 +228,20 @@ class TurboQuantCache(HostTables):
         max_pages = (self.cfg.max_ctx + 127) // 128
         n = self.cfg.max_seqs * max_pages
         return self.cache_buf[off:off + 4 * n].view(torch.int32).view(self.cfg.max_seqs, max_pages)
+
+    @property
+    def block_pool(self):
+        """Paged cache: the paged.BlockPool of this cache's block table, made on first use, which is refused once the caller
+        has mapped pages itself. Its map() and release() keep the table; exact layers share it through paged.PagedCache.
+        None when not paged."""
+        if self.cfg.n_blocks <= 0:
+            return None
+        if self._pool is None:
+            table = self.block_table
+            if bool((table != -1).any()):
+                raise ValueError("the block table already maps pages: a pool does not know which blocks are free")
+            self._pool = paged.BlockPool(self.cfg.n_blocks, self.cfg.max_seqs, self.cfg.max_ctx, table=table)
+        return self._pool
 
     def page(self, layer, slot, head, page):
         if self.cfg.n_blocks > 0:

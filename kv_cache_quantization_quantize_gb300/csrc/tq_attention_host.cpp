@@ -1,0 +1,270 @@
+// Entry points of the exact paged cache and of cross attention: argument checks and launches.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "tq_attention.cuh"
+
+namespace {
+
+tq_status fail(tq_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  return tq::set_error(st, buf);
+}
+
+tq_status done(cudaError_t e, const char* what) {
+  if (e != cudaSuccess) return fail(TQ_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+  return tq::set_error(TQ_OK, "");
+}
+
+// SMs of the current device (asked once per device).
+cudaError_t sm_count(int* out) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && (*out = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) known[dev].store(*out, std::memory_order_relaxed);
+  return e;
+}
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+tq_status check_map(const int32_t* table, int max_seqs, int max_pages, int64_t stride, const int32_t* free_ids,
+                    int n_blocks, const int32_t* n_free, const int32_t* ids, int batch) {
+  if (!table || !free_ids || !n_free || (!ids && batch > 0)) return fail(TQ_ERR_INVALID_ARG, "NULL array");
+  if (max_seqs < 1 || max_pages < 1 || max_pages > (1 << 20))
+    return fail(TQ_ERR_INVALID_ARG, "max_seqs %d, max_pages %d: at least 1, at most 2^20 pages", max_seqs, max_pages);
+  if (stride < max_pages) return fail(TQ_ERR_INVALID_ARG, "table_stride %lld below max_pages", (long long)stride);
+  if (n_blocks < 1 || n_blocks > (1 << 24) - 1) return fail(TQ_ERR_INVALID_ARG, "n_blocks %d: 1 to 2^24 - 1", n_blocks);
+  if (batch < 0) return fail(TQ_ERR_INVALID_ARG, "batch %d < 0", batch);
+  if (batch > 4096) return fail(TQ_ERR_UNSUPPORTED, "batch %d: at most 4096", batch);
+  return TQ_OK;
+}
+
+tq_status check_kv(const tq_kv* kv, bool map) {
+  if (!kv) return fail(TQ_ERR_INVALID_ARG, "kv is NULL");
+  if (kv->head_dim != 64 && kv->head_dim != 128 && kv->head_dim != 256)
+    return fail(TQ_ERR_UNSUPPORTED, "head_dim %d: supported 64, 128, 256", kv->head_dim);
+  if (kv->dtype != TQ_BF16 && kv->dtype != TQ_F16) return fail(TQ_ERR_UNSUPPORTED, "cache type %d: bf16 or f16", kv->dtype);
+  if (kv->n_kv_heads < 1 || kv->n_kv_heads > 65535 || kv->outer < 0 || kv->tokens < 0)
+    return fail(TQ_ERR_INVALID_ARG, "n_kv_heads %d, outer %d, tokens %d", kv->n_kv_heads, kv->outer, kv->tokens);
+  if (!kv->outer || !kv->tokens) return TQ_OK;  // no element
+  if (!kv->k || !kv->v) return fail(TQ_ERR_INVALID_ARG, "k or v is NULL");
+  if (!map) return TQ_OK;
+  if (!aligned(kv->k, 16) || !aligned(kv->v, 16)) return fail(TQ_ERR_INVALID_ARG, "k and v have to be 16-byte aligned");
+  const int size[3] = {kv->outer, kv->tokens, kv->n_kv_heads};
+  for (int i = 0; i < 3; ++i)
+    for (const int64_t st : {kv->k_strides[i], kv->v_strides[i]})
+      if (size[i] > 1 && (st < 1 || st % 8 || st >= (int64_t)1 << 38))
+        return fail(TQ_ERR_INVALID_ARG, "stride %lld of k or v: a positive multiple of 8 elements", (long long)st);
+  return TQ_OK;
+}
+
+tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
+  if (!q) return fail(TQ_ERR_INVALID_ARG, "queries are NULL");
+  if (q->batch < 0 || q->n_rows < 0 || q->max_q < 0 || q->max_kv < 0)
+    return fail(TQ_ERR_INVALID_ARG, "batch %d, n_rows %d, max_q %d, max_kv %d: none below 0", q->batch, q->n_rows,
+                q->max_q, q->max_kv);
+  if (q->batch > 65535) return fail(TQ_ERR_UNSUPPORTED, "batch %d: at most 65535", q->batch);
+  if (q->n_q_heads < 1 || q->n_q_heads % kv->n_kv_heads)
+    return fail(TQ_ERR_INVALID_ARG, "n_q_heads %d not a multiple of n_kv_heads %d", q->n_q_heads, kv->n_kv_heads);
+  if (q->n_q_heads / kv->n_kv_heads > 1024)
+    return fail(TQ_ERR_UNSUPPORTED, "%d query heads per KV head: at most 1024", q->n_q_heads / kv->n_kv_heads);
+  if ((int64_t)q->n_rows * q->n_q_heads >= (int64_t)1 << 31)
+    return fail(TQ_ERR_UNSUPPORTED, "n_rows x n_q_heads: below 2^31");
+  if (std::isnan(q->softmax_scale) || std::isinf(q->softmax_scale))
+    return fail(TQ_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (!q->batch || !q->n_rows) return TQ_OK;
+  if (!q->q || !q->out || !q->d_q_starts) return fail(TQ_ERR_INVALID_ARG, "q, out or d_q_starts is NULL");
+  if (!aligned(q->q, 16) || !aligned(q->out, 16)) return fail(TQ_ERR_INVALID_ARG, "q and out have to be 16-byte aligned");
+  for (int i = 0; i < 2; ++i)
+    if (q->q_strides[i] % 8 || q->out_strides[i] % 8)
+      return fail(TQ_ERR_INVALID_ARG, "strides of q and out: multiples of 8 elements");
+  return TQ_OK;
+}
+
+int64_t most_tokens(const tq_kv* kv, int max_pages) {
+  return max_pages > 0 ? (int64_t)max_pages * tq::kPage : kv->tokens;
+}
+
+tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, int max_pages, void* ws, size_t ws_bytes,
+                 uint32_t* status, tq_stream_t stream) {
+  if (!q->batch || !q->n_rows) return tq::set_error(TQ_OK, "");
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return done(e, "device");
+  const tq::AttnPlan p = tq::attn_plan(*q, *kv_in, most_tokens(kv_in, max_pages), sms);
+  if (p.tiles * kv_in->n_kv_heads >= ((int64_t)1 << 31) / std::max(p.n_splits, p.n_splits > 1 ? p.tile_rows : 1)) return fail(TQ_ERR_UNSUPPORTED, "batch x heads x rows: too many tiles for one launch");
+  if (p.bytes && (!ws || ws_bytes < p.bytes || !aligned(ws, 256)))
+    return fail(TQ_ERR_INVALID_ARG, "workspace: %zu bytes, 256-byte aligned, are needed (got %zu)", p.bytes, ws_bytes);
+  tq_kv kv = *kv_in;
+  if (!kv.outer || !kv.tokens) {  // nothing to read: the tensor maps need an address all the same
+    kv.k = kv.v = const_cast<void*>(q->q);
+    kv.outer = kv.tokens = 0;
+  }
+  a.q = q->q;
+  a.out = q->out;
+  a.q_row = q->q_strides[0];
+  a.q_head = q->q_strides[1];
+  a.o_row = q->out_strides[0];
+  a.o_head = q->out_strides[1];
+  a.q_starts = q->d_q_starts;
+  a.status = status;
+  a.part = static_cast<float*>(ws);
+  const double scale = q->softmax_scale > 0.f ? (double)q->softmax_scale : 1.0 / std::sqrt((double)kv.head_dim);
+  a.scale_log2 = (float)(scale * 1.4426950408889634);
+  a.n_rows = q->n_rows;
+  a.batch = q->batch;
+  a.hq = q->n_q_heads;
+  a.hkv = kv.n_kv_heads;
+  a.G = a.hq / a.hkv;
+  a.outer = kv.outer;
+  a.tokens = kv.tokens;
+  a.n_splits = p.n_splits;
+  a.max_rows = (int)p.max_rows;
+  a.tiles = p.packed ? 0 : (int)(p.tiles / q->batch);
+  return done(tq::launch_attention(a, kv, p, (cudaStream_t)stream), "attention launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+tq_status tq_blocks_release(int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride, int32_t* d_free,
+                            int n_blocks, int32_t* d_n_free, const int32_t* d_seq_ids, const int32_t* d_keep,
+                            int batch, uint32_t* d_status, tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_blocks_release");
+  const tq_status st = check_map(d_table, max_seqs, max_pages, table_stride, d_free, n_blocks, d_n_free, d_seq_ids, batch);
+  if (st != TQ_OK) return st;
+  if (!batch) return tq::set_error(TQ_OK, "");
+  tq::BlockMap m = {};
+  m.table = d_table;
+  m.stride = table_stride;
+  m.free = d_free;
+  m.n_free = d_n_free;
+  m.ids = d_seq_ids;
+  m.lens = d_keep;
+  m.status = d_status;
+  m.max_seqs = max_seqs;
+  m.max_pages = max_pages;
+  m.n_blocks = n_blocks;
+  m.batch = batch;
+  return done(tq::launch_blocks_release(m, (cudaStream_t)stream), "tq_blocks_release");
+}
+
+tq_status tq_blocks_map(int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride, const int32_t* d_free,
+                        int n_blocks, int32_t* d_n_free, const int32_t* d_seq_ids, const int32_t* d_lens,
+                        const int32_t* d_n_new, int batch, int32_t* d_starts, int32_t* d_totals, int32_t* d_slots,
+                        int max_tokens, uint32_t* d_status, tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_blocks_map");
+  const tq_status st = check_map(d_table, max_seqs, max_pages, table_stride, d_free, n_blocks, d_n_free, d_seq_ids, batch);
+  if (st != TQ_OK) return st;
+  if (!d_starts || (batch > 0 && (!d_lens || !d_n_new || !d_totals)) || (max_tokens > 0 && !d_slots))
+    return fail(TQ_ERR_INVALID_ARG, "NULL array");
+  if (max_tokens < 0 || max_tokens > (1 << 30)) return fail(TQ_ERR_INVALID_ARG, "max_tokens %d: 0 to 2^30", max_tokens);
+  tq::BlockMap m = {};
+  m.table = d_table;
+  m.stride = table_stride;
+  m.free = const_cast<int32_t*>(d_free);
+  m.n_free = d_n_free;
+  m.ids = d_seq_ids;
+  m.lens = d_lens;
+  m.n_new = d_n_new;
+  m.starts = d_starts;
+  m.totals = d_totals;
+  m.slots = d_slots;
+  m.status = d_status;
+  m.max_seqs = max_seqs;
+  m.max_pages = max_pages;
+  m.n_blocks = n_blocks;
+  m.batch = batch;
+  m.max_tokens = max_tokens;
+  return done(tq::launch_blocks_map(m, (cudaStream_t)stream), "tq_blocks_map");
+}
+
+tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dtype dt, const int64_t* k_strides,
+                          const int64_t* v_strides, const int32_t* d_slots, int n_tokens, uint32_t* d_status,
+                          tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_paged_append");
+  const tq_status st = check_kv(pool, false);
+  if (st != TQ_OK) return st;
+  if (pool->tokens != tq::kPage || pool->outer < 1 || pool->outer > (1 << 24) - 1)
+    return fail(TQ_ERR_INVALID_ARG, "a pool has 1 to 2^24 - 1 blocks of 128 tokens (got %d of %d)", pool->outer, pool->tokens);
+  if (dt != TQ_BF16 && dt != TQ_F16 && dt != TQ_F32) return fail(TQ_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (n_tokens < 0) return fail(TQ_ERR_INVALID_ARG, "n_tokens %d < 0", n_tokens);
+  if (!n_tokens) return tq::set_error(TQ_OK, "");
+  if (!k || !v || !k_strides || !v_strides || !d_slots) return fail(TQ_ERR_INVALID_ARG, "NULL array");
+  const size_t esz = dt == TQ_F32 ? 4 : 2;
+  if (!aligned(k, esz) || !aligned(v, esz) || !aligned(pool->k, 2) || !aligned(pool->v, 2))
+    return fail(TQ_ERR_INVALID_ARG, "an address is not a multiple of its element's size");
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return done(e, "device");
+  return done(tq::launch_paged_append(*pool, k, v, (int)dt, k_strides, v_strides, d_slots, n_tokens, d_status, sms,
+                                      (cudaStream_t)stream),
+              "tq_paged_append");
+}
+
+size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv, int max_pages) {
+  int sms = 0;
+  if (check_kv(kv, false) != TQ_OK || !q || q->batch < 1 || q->n_rows < 1 || q->max_q < 0 || q->max_kv < 0 ||
+      q->n_q_heads < 1 || q->n_q_heads % kv->n_kv_heads || max_pages < 0 || sm_count(&sms) != cudaSuccess)
+    return 0;
+  return tq::attn_plan(*q, *kv, most_tokens(kv, max_pages), sms).bytes;
+}
+
+tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_table, int max_seqs,
+                             int max_pages, int64_t table_stride, const int32_t* d_seq_ids, const int32_t* d_kv_lens,
+                             int causal, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
+                             tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_paged_attention");
+  tq_status st = check_kv(kv, true);
+  if (st == TQ_OK) st = check_queries(q, kv);
+  if (st != TQ_OK) return st;
+  if (kv->tokens != tq::kPage || kv->outer < 1 || kv->outer > (1 << 24) - 1)
+    return fail(TQ_ERR_INVALID_ARG, "a pool has 1 to 2^24 - 1 blocks of 128 tokens (got %d of %d)", kv->outer, kv->tokens);
+  if (max_seqs < 1 || max_pages < 1 || max_pages > (1 << 20) || table_stride < max_pages)
+    return fail(TQ_ERR_INVALID_ARG, "max_seqs %d, max_pages %d (at most 2^20), table_stride %lld", max_seqs, max_pages,
+                (long long)table_stride);
+  if (causal != 0 && causal != 1) return fail(TQ_ERR_INVALID_ARG, "causal %d: 0 or 1", causal);
+  if (q->batch && q->n_rows && (!d_table || !d_kv_lens)) return fail(TQ_ERR_INVALID_ARG, "d_table or d_kv_lens is NULL");
+  if (!d_seq_ids && q->batch > max_seqs) return fail(TQ_ERR_INVALID_ARG, "batch %d above max_seqs %d", q->batch, max_seqs);
+  tq::AttnArgs a = {};
+  a.mode = tq::kKvPaged;
+  a.causal = causal;
+  a.kv_lens = d_kv_lens;
+  a.seq_ids = d_seq_ids;
+  a.table = d_table;
+  a.table_stride = table_stride;
+  a.max_seqs = max_seqs;
+  a.max_pages = max_pages;
+  return attend(q, kv, a, max_pages, d_workspace, workspace_bytes, d_status, stream);
+}
+
+tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_kv_starts,
+                             const int32_t* d_kv_lens, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
+                             tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_cross_attention");
+  tq_status st = check_kv(kv, true);
+  if (st == TQ_OK) st = check_queries(q, kv);
+  if (st != TQ_OK) return st;
+  if ((d_kv_starts != nullptr) == (d_kv_lens != nullptr) && q->batch && q->n_rows)
+    return fail(TQ_ERR_INVALID_ARG, "d_kv_starts (packed states) or d_kv_lens (padded states), one of the two");
+  if (d_kv_starts && kv->outer != 1) return fail(TQ_ERR_INVALID_ARG, "packed states have outer 1 (got %d)", kv->outer);
+  if (d_kv_lens && kv->outer < q->batch) return fail(TQ_ERR_INVALID_ARG, "outer %d below batch %d", kv->outer, q->batch);
+  tq::AttnArgs a = {};
+  a.mode = d_kv_starts ? tq::kKvPacked : tq::kKvPadded;
+  a.kv_lens = d_kv_lens;
+  a.kv_starts = d_kv_starts;
+  return attend(q, kv, a, 0, d_workspace, workspace_bytes, d_status, stream);
+}
+
+}  // extern "C"

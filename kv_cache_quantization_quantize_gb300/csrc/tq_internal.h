@@ -266,4 +266,23 @@ cudaError_t launch_prefill_tc(const tq_ctx* ctx, int layer, const void* q, const
 bool step_follows(tq_ctx* ctx, int layer, cudaStream_t s);
 void record_step(tq_ctx* ctx, int layer, cudaStream_t s);
 
+// Block maps and appends of the exact paged cache (tq_paged.cu); the arrays of tq_blocks_map / tq_blocks_release.
+struct BlockMap {
+  int32_t* table;
+  int64_t stride;
+  int32_t* free;
+  int32_t* n_free;
+  const int32_t* ids;
+  const int32_t* lens;  // map: lengths; release: tokens to keep (NULL: 0)
+  const int32_t* n_new;
+  int32_t *starts, *totals, *slots;
+  uint32_t* status;
+  int max_seqs, max_pages, n_blocks, batch, max_tokens;
+};
+cudaError_t launch_blocks_release(const BlockMap& m, cudaStream_t s);
+cudaError_t launch_blocks_map(const BlockMap& m, cudaStream_t s);
+cudaError_t launch_paged_append(const tq_kv& pool, const void* k, const void* v, int dt, const int64_t* k_strides,
+                                const int64_t* v_strides, const int32_t* slots, int n_tokens, uint32_t* status,
+                                int sms, cudaStream_t s);
+
 }  // namespace tq

@@ -1,0 +1,538 @@
+"""GPU tests of the exact paged cache and of cross attention, against plain 64-bit references."""
+import math
+
+import pytest
+import torch
+
+import kv_cache_quantization_quantize_gb300 as tqm
+from kv_cache_quantization_quantize_gb300 import paged
+from tests import paged_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from kv_cache_quantization_quantize_gb300 import build
+    build.build()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def starts_of(n):
+    s = [0]
+    for x in n:
+        s.append(s[-1] + x)
+    return s
+
+
+# ---- block maps ----
+
+def random_state(gen, max_seqs, max_pages, n_blocks, fill):
+    """A table whose rows hold random prefixes of pages, and the stack of the other blocks."""
+    ids = torch.randperm(n_blocks, generator=gen).tolist()
+    table = [[-1] * max_pages for _ in range(max_seqs)]
+    for row in table:
+        for p in range(int(torch.randint(0, fill + 1, (1,), generator=gen))):
+            if ids:
+                row[p] = ids.pop()
+    return table, ids + [-1] * (n_blocks - len(ids)), len(ids)
+
+
+@pytest.mark.parametrize("batch,max_pages,n_blocks,hist,new", [
+    (1, 1, 4, 0, 1), (1, 4, 8, 300, 1), (3, 8, 64, 500, 200), (5, 8, 6, 300, 700), (33, 4, 200, 300, 5), (300, 6, 2000, 600, 129),
+    (1025, 3, 3200, 200, 100), (4, 300, 1300, 20000, 15000),
+])
+def test_map_and_release_follow_the_serial_form(batch, max_pages, n_blocks, hist, new):
+    gen = torch.Generator().manual_seed(batch * 1000 + max_pages)
+    r = lambda hi, n: torch.randint(0, hi + 1, (n,), generator=gen).tolist()  # noqa: E731
+    max_seqs = batch + 2
+    table, free, n_free = random_state(gen, max_seqs, max_pages, n_blocks, max(1, pages_in(n_blocks, max_seqs, max_pages)))
+    d_table, d_free, d_n = i32(table), i32(free), i32([n_free])
+    for step in range(3):
+        ids = torch.randperm(max_seqs, generator=gen)[:batch].tolist()
+        keep = [min(k, 128 * sum(e >= 0 for e in table[i])) for i, k in zip(ids, r(hist, batch))]
+        n_free = ref.release(table, free, n_free, ids, keep)
+        paged.release_blocks(d_table, d_free, d_n, i32(ids), i32(keep))
+        assert d_table.tolist() == table and d_n.tolist() == [n_free] and d_free.tolist() == free
+        count = r(new, batch)
+        total = sum(count)
+        for room in (total, max(0, total - 3), total + 7)[step:step + 1]:
+            slots, starts, totals, n_free = ref.map_(table, free, n_free, ids, keep, count, room)
+            got = paged.map_blocks(d_table, d_free, d_n, i32(ids), i32(keep), i32(count), room)
+            assert [x.tolist() for x in got] == [slots, starts, totals]
+            assert d_table.tolist() == table and d_n.tolist() == [n_free] and d_free.tolist() == free
+
+
+def pages_in(n_blocks, max_seqs, max_pages):
+    return min(max_pages, n_blocks // max_seqs)
+
+
+def test_map_takes_the_same_blocks_again_after_a_release():
+    pool = paged.BlockPool(50, 4, 1024)
+    ids, lens, new = i32([2, 0]), i32([0, 0]), i32([300, 129])
+    first = [x.tolist() for x in pool.map(ids, lens, new, 429)]
+    assert first[0][:3] == [0, 1, 2] and pool.n_free.tolist() == [45]
+    pool.release(ids, keep=i32([128, 0]))
+    assert pool.n_free.tolist() == [49]
+    again = [x.tolist() for x in pool.map(ids, i32([128, 0]), i32([172, 129]), 301)]
+    assert again[0] == first[0][128:] and again[2] == [300, 129]
+    pool.release(ids)
+    assert pool.n_free.tolist() == [50] and bool((pool.table == -1).all())
+    assert sorted(pool.free.tolist()) == list(range(50)) and pool.check_status() == 0
+
+
+def test_map_reports_what_it_does_not_serve():
+    pool = paged.BlockPool(10, 4, 512)
+    # an id out of range, the same id twice, a negative length, a negative count, too many pages
+    ids, lens, new = [9, 1, 1, 2, 3, 0], [0, 0, 0, -5, 0, 400], [2, 3, 4, 1, -1, 200]
+    slots, starts, totals = pool.map(i32(ids), i32(lens), i32(new), 215)
+    table, free = [[-1] * 4 for _ in range(4)], list(range(9, -1, -1))
+    want = ref.map_(table, free, 10, ids, lens, new, 215)
+    assert [slots.tolist(), starts.tolist(), totals.tolist(), pool.n_free.item()] == list(want)
+    assert pool.check_status() == paged.TQ_DEV_ERR_SEQ_ID | paged.TQ_DEV_ERR_LENGTH and pool.check_status() == 0
+    # a partial page without a block: no slot, and the next page's tokens have theirs
+    slots, _, totals = pool.map(i32([2]), i32([100]), i32([60]), 60)
+    assert slots.tolist()[:28] == [-1] * 28 and slots[28].item() % 128 == 0 and totals.tolist() == [160]
+    assert pool.check_status() == paged.TQ_DEV_ERR_BLOCK
+    # more blocks than are free: the request is refused, one that needs none is served
+    pool = paged.BlockPool(2, 4, 512)
+    pool.map(i32([0]), i32([0]), i32([5]), 5)
+    slots, starts, totals = pool.map(i32([1, 0, 2]), i32([0, 5, 0]), i32([256, 3, 1]), 260)
+    assert totals.tolist() == [0, 8, 0] and slots[:256].unique().tolist() == [-1] and slots[256:].tolist() == [5, 6, 7, -1]
+    assert pool.check_status() == paged.TQ_DEV_ERR_POOL and pool.n_free.tolist() == [1]
+    # a block freed twice: nothing changes
+    pool.table[3] = pool.table[0]
+    pool.free[:] = 1
+    pool.table[3, 1] = 0
+    before = pool.table.clone()
+    pool.release(i32([3, 0]))
+    assert torch.equal(pool.table, before) and pool.n_free.tolist() == [1] and pool.check_status() == paged.TQ_DEV_ERR_POOL
+    # entries that are no block ids are dropped; the same id twice counts once
+    pool = paged.BlockPool(4, 2, 512)
+    pool.table[1] = i32([3, 99, -7, -1])
+    pool.n_free.fill_(2)
+    pool.release(i32([1, 1, -1]))
+    assert pool.table[1].tolist() == [-1] * 4 and pool.n_free.tolist() == [3] and pool.free[2].item() == 3
+    assert pool.check_status() == paged.TQ_DEV_ERR_BLOCK | paged.TQ_DEV_ERR_SEQ_ID
+
+
+def test_map_of_nothing():
+    pool = paged.BlockPool(4, 4, 512)
+    slots, starts, totals = pool.map(i32([]), i32([]), i32([]), 6)
+    assert slots.tolist() == [-1] * 6 and starts.tolist() == [0] and totals.tolist() == []
+    slots, starts, totals = pool.map(i32([1, 2]), i32([0, 0]), i32([0, 0]), 0)
+    assert slots.tolist() == [] and starts.tolist() == [0, 0, 0] and totals.tolist() == [0, 0]
+    pool.release(i32([]))
+    assert pool.check_status() == 0 and pool.n_free.tolist() == [4]
+
+
+def test_map_with_a_strided_table_and_given_outputs():
+    wide = torch.full((5, 20), -1, dtype=torch.int32, device=DEV)
+    table = wide[:, 4:10]
+    free, n_free = i32([0, 1, 2, 3, 4, 5, 6, 7]), i32([8])
+    buf = torch.full((64,), 77, dtype=torch.int32, device=DEV)
+    out = (buf[1:12], buf[20:23], buf[30:32])  # slots at an odd address: no wide stores
+    paged.map_blocks(table, free, n_free, i32([4, 1]), i32([0, 0]), i32([3, 7]), 11, out=out)
+    assert out[0].tolist() == [7 * 128, 7 * 128 + 1, 7 * 128 + 2] + [6 * 128 + i for i in range(7)] + [-1]
+    assert out[1].tolist() == [0, 3, 10] and out[2].tolist() == [3, 7]
+    rest = buf.tolist()
+    assert rest[0] == 77 and rest[12:20] == [77] * 8 and rest[23:30] == [77] * 7 and rest[32:] == [77] * 32
+    assert int((wide != -1).sum()) == 2 and table[4, 0].item() == 7 and table[1, 0].item() == 6
+
+
+# ---- append ----
+
+@pytest.mark.parametrize("src", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("dst", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("tokens,heads,d", [(1, 1, 64), (7, 3, 128), (300, 2, 256), (1000, 8, 128)])
+@pytest.mark.parametrize("layout", ["plain", "fused", "odd"])
+def test_append_rounds_once_and_touches_nothing_else(src, dst, tokens, heads, d, layout):
+    gen = torch.Generator(device=DEV).manual_seed(tokens + heads)
+    blocks = ref.pages(tokens) + 2
+    big = torch.randn((tokens, 3 * heads, d + (3 if layout == "odd" else 0)), generator=gen, device=DEV) * 4
+    big[0, :, 0] = 70000.0  # past f16's range
+    big = big.to(src)
+    k, v = big[:, heads:2 * heads], big[:, 2 * heads:]
+    if layout == "plain":
+        k, v = k.contiguous(), v.contiguous()
+    if layout == "odd":  # rows that start at odd addresses, on both sides
+        k, v = k[..., 1:d + 1], v[..., 2:d + 2]
+        base = torch.full((2, blocks, 128, heads, d + 1), 3.0, dtype=dst, device=DEV)
+        pools = base[..., 1:]
+    else:
+        base = pools = torch.full((2, blocks, heads, 128, d), 3.0, dtype=dst, device=DEV)
+        pools = pools.transpose(2, 3)
+    slots = (torch.randperm(blocks * 128, generator=gen, device=DEV)[:tokens]).to(torch.int32)
+    if tokens > 3:
+        slots[2] = -1
+    want = base.clone()
+    view = want[..., 1:] if layout == "odd" else want.transpose(2, 3)
+    at = slots[slots >= 0].long()
+    view[0, at // 128, at % 128] = k[slots >= 0].to(dst)
+    view[1, at // 128, at % 128] = v[slots >= 0].to(dst)
+    status = i32([0])
+    paged.append(k, v, pools[0], pools[1], slots, status=status)
+    assert torch.equal(base, want) and status.item() == 0
+
+
+def test_append_skips_slots_outside_the_pool():
+    pool = torch.zeros((2, 3, 128, 2, 64), dtype=torch.bfloat16, device=DEV)
+    x = torch.ones((5, 2, 64), dtype=torch.bfloat16, device=DEV)
+    status = i32([0])
+    paged.append(x, x, pool[0], pool[1], i32([3 * 128, -2, 2 ** 31 - 1, -2 ** 31, 3 * 128 - 1]), status=status)
+    assert status.item() == paged.TQ_DEV_ERR_BLOCK
+    assert float(pool.float().sum()) == 2 * 2 * 64 and bool((pool[:, 2, 127] == 1).all())
+    paged.append(x[:0], x[:0], pool[0], pool[1], i32([]))
+
+
+# ---- attention ----
+
+def paged_inputs(nq, kv, hq, hkv, d, dtype, heads_first, seed, tail=0):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    batch = len(nq)
+    blocks = sum(ref.pages(x) for x in kv) + 2
+    shape = (2, blocks, hkv, 128, d) if heads_first else (2, blocks, 128, hkv, d)
+    pool = torch.full(shape, float("nan"), dtype=dtype, device=DEV)
+    if heads_first:
+        pool = pool.transpose(2, 3)
+    table = torch.full((batch + 2, max(1, max(ref.pages(x) for x in kv)) + 1), -1, dtype=torch.int32)
+    rows = torch.randperm(batch + 2, generator=torch.Generator().manual_seed(seed))[:batch]
+    ids = torch.randperm(blocks, generator=torch.Generator().manual_seed(seed + 1)).tolist()
+    ks, vs = [], []
+    for b, n in enumerate(kv):
+        k = torch.randn((n, hkv, d), generator=gen, device=DEV) * torch.where(torch.arange(d, device=DEV) % 31 == 5, 4.0, 1.0)
+        v = torch.randn((n, hkv, d), generator=gen, device=DEV) + 0.5
+        ks.append(k.to(dtype))
+        vs.append(v.to(dtype))
+        for p in range(ref.pages(n)):
+            blk = ids.pop()
+            table[rows[b], p] = blk
+            m = min(128, n - 128 * p)
+            pool[0, blk, :m] = ks[-1][128 * p:128 * p + m]
+            pool[1, blk, :m] = vs[-1][128 * p:128 * p + m]
+    q = torch.randn((sum(nq) + tail, hq + 2, d), generator=gen, device=DEV).to(dtype)[:, :hq]
+    return q, pool, table.to(DEV), rows.to(torch.int32).to(DEV), ks, vs
+
+
+def visible_of(n, m, causal):
+    return [max(0, m - n + i + 1) if causal else m for i in range(n)]
+
+
+def check_rows(out, q, ks, vs, nq, kv, causal, scale, starts=None):
+    starts = starts or starts_of(nq)
+    for b, (n, m) in enumerate(zip(nq, kv)):
+        sl = slice(starts[b], starts[b] + n)
+        want, bound = ref.attention(q[sl], ks[b][:m], vs[b][:m], visible_of(n, m, causal), scale)
+        err = (out[sl].double() - want).abs()
+        assert torch.isfinite(out[sl]).all(), f"request {b}"
+        worst = (err - bound).max().item() if n else 0.0
+        assert worst <= 0, f"request {b} ({n} queries, {m} tokens): {worst} past the bound, error {err.max().item()}"
+
+
+HEADS = [(4, 4), (8, 2), (6, 2), (5, 1), (16, 1), (40, 2)]
+LENGTHS = [
+    ([1], [1]), ([1], [128]), ([1, 1, 1, 1], [1, 127, 129, 1000]), ([1, 0, 1], [63, 0, 65]), ([0, 1, 1], [50, 0, 3]),
+    ([4, 1, 3], [4, 700, 258]), ([5, 2], [3, 2]), ([17, 1], [400, 300]), ([130, 3, 40], [130, 200, 513]), ([300], [700]),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("case", range(len(LENGTHS)))
+def test_paged_attention(dtype, d, heads, case):
+    nq, kv = LENGTHS[case]
+    hq, hkv = heads
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, hq, hkv, d, dtype, case % 2 == 1, 100 * case + d, tail=2)
+    status = i32([0])
+    out = torch.full(q.shape, 9.0, dtype=dtype, device=DEV)
+    paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=max(nq), max_kv=max(kv), out=out, status=status)
+    assert status.item() == 0
+    check_rows(out, q, ks, vs, nq, kv, True, 1 / math.sqrt(d))
+    assert bool((out[sum(nq):] == 9).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq,kv", [([1, 1], [9000, 1]), ([3], [20000]), ([1, 2, 1], [5000, 4999, 130]), ([100], [9000]), ([40, 1], [6000, 7000])])
+def test_paged_attention_over_split_sequences(d, nq, kv):
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, d, torch.bfloat16, False, 7 + d, tail=1)
+    assert paged.attention_workspace_bytes(q, pool[0], max(nq), max(kv), len(nq), table.shape[1]) > 0
+    out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+    paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=max(nq), max_kv=max(kv), out=out)
+    check_rows(out, q, ks, vs, nq, kv, True, 1 / math.sqrt(d))
+    assert bool((out[sum(nq):] == 9).all())
+    # without the hints the plan is another one, the result the same up to its own bound
+    out2 = paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv))
+    check_rows(out2, q, ks, vs, nq, kv, True, 1 / math.sqrt(d))
+
+
+def test_paged_attention_options():
+    """No ids (row b of the table), a scale of its own, all tokens visible, a strided output, scores far apart."""
+    nq, kv, d = [2, 3], [150, 40], 128
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 4, 2, d, torch.bfloat16, False, 3)
+    table = table[rows.long()].contiguous()
+    big = torch.full((5, 8, d), 9.0, dtype=q.dtype, device=DEV)
+    out = paged.attention(q * 8, pool[0], pool[1], table, None, i32(starts_of(nq)), i32(kv), causal=False, softmax_scale=0.5, out=big[:, ::2])
+    check_rows(out, q * 8, ks, vs, nq, kv, False, 0.5)
+    assert bool((big[:, 1::2] == 9).all())
+
+
+def test_paged_attention_reports_bad_arrays():
+    nq, kv = [1, 2, 1, 1], [100, 200, 50, 60]
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 4, 2, 128, torch.bfloat16, False, 5)
+    status = i32([0])
+
+    def run(starts=None, lens=None, ids=None, tab=None, max_q=2):
+        status.zero_()
+        out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+        paged.attention(q, pool[0], pool[1], table if tab is None else tab, rows if ids is None else i32(ids), i32(starts or starts_of(nq)),
+                        i32(lens or kv), max_q=max_q, out=out, status=status)
+        return out, status.item()
+
+    good, word = run()
+    assert word == 0
+    out, word = run(lens=[100, -1, 50, 10 ** 6])
+    assert word == paged.TQ_DEV_ERR_LENGTH and not out[1:3].any() and not out[4].any()
+    assert torch.equal(out[[0, 3]], good[[0, 3]])
+    r = rows.tolist()
+    out, word = run(ids=[r[0], 77, r[2], -3])
+    assert word == paged.TQ_DEV_ERR_SEQ_ID and torch.equal(out[[0, 3]], good[[0, 3]]) and not out[1:3].any() and not out[4].any()
+    out, word = run(starts=[0, 1, 3, 2, 9])
+    assert word & paged.TQ_DEV_ERR_LENGTH and torch.equal(out[:3], good[:3]) and bool((out[3:] == 9).all())
+    broken = table.clone()
+    broken[rows[1].long(), 1] = 5000
+    out, word = run(tab=broken)
+    assert word == paged.TQ_DEV_ERR_BLOCK and torch.equal(out[[0, 3, 4]], good[[0, 3, 4]])
+    out, word = run(max_q=1)
+    assert word == paged.TQ_DEV_ERR_SPLITS and torch.equal(out[[0, 3, 4]], good[[0, 3, 4]]) and bool((out[1:3] == 9).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(4, 4), (12, 4), (8, 1)])
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("nq,kv", [([1, 1, 1], [1, 200, 65]), ([1, 3, 0, 2], [0, 129, 70, 128]), ([50, 7], [300, 1]), ([200, 1], [77, 500])])
+def test_cross_attention(dtype, d, heads, padded, nq, kv):
+    hq, hkv = heads
+    gen = torch.Generator(device=DEV).manual_seed(d + hq + sum(kv))
+    q = torch.randn((sum(nq), hq, d), generator=gen, device=DEV).to(dtype)
+    both = torch.randn((sum(kv) + 3, 2, hkv, d), generator=gen, device=DEV).to(dtype)
+    both[sum(kv):] = float("nan")
+    s = starts_of(kv)
+    ks, vs = ([both[s[b]:s[b + 1], w] for b in range(len(kv))] for w in (0, 1))
+    status = i32([0])
+    if padded:
+        rows = torch.full((len(kv), max(kv) + 5, 2, hkv, d), float("nan"), dtype=dtype, device=DEV)
+        for b, n in enumerate(kv):
+            rows[b, :n] = both[s[b]:s[b + 1]]
+        out = paged.cross_attention(q, rows[:, :, 0], rows[:, :, 1], i32(starts_of(nq)), kv_lens=i32(kv), max_q=max(nq), status=status)
+    else:
+        out = paged.cross_attention(q, both[:, 0], both[:, 1], i32(starts_of(nq)), kv_starts=i32(s), max_q=max(nq), max_kv=max(kv), status=status)
+    assert status.item() == 0
+    check_rows(out, q, ks, vs, nq, kv, False, 1 / math.sqrt(d))
+
+
+def test_cross_attention_over_long_states():
+    nq, kv, d = [1, 1], [6000, 5000], 64
+    q = torch.randn((2, 4, d), device=DEV).half()
+    both = torch.randn((sum(kv), 2, 2, d), device=DEV).half()
+    out = paged.cross_attention(q, both[:, 0], both[:, 1], i32([0, 1, 2]), kv_starts=i32([0, 6000, 11000]), max_q=1, max_kv=6000)
+    check_rows(out, q, [both[:6000, 0], both[6000:, 0]], [both[:6000, 1], both[6000:, 1]], nq, kv, False, 1 / math.sqrt(d))
+
+
+def test_cross_attention_without_any_state():
+    q = torch.randn((3, 4, 64), device=DEV).half()
+    none = torch.empty((0, 2, 64), dtype=torch.float16, device=DEV)
+    out = paged.cross_attention(q, none, none, i32([0, 1, 3]), kv_starts=i32([0, 0, 0]))
+    assert not out.any()
+    none = torch.empty((2, 0, 2, 64), dtype=torch.float16, device=DEV)
+    out = paged.cross_attention(q, none, none, i32([0, 1, 3]), kv_lens=i32([0, 0]))
+    assert not out.any()
+    assert paged.cross_attention(q[:0], none, none, i32([0, 0, 0]), kv_lens=i32([0, 0])).shape == (0, 4, 64)
+
+
+def test_cross_attention_reports_bad_arrays():
+    q = torch.randn((2, 2, 64), device=DEV).half()
+    x = torch.randn((10, 2, 64), device=DEV).half()
+    status = i32([0])
+    for starts in ([0, 4, 11], [-1, 4, 10], [5, 4, 10]):
+        status.zero_()
+        paged.cross_attention(q, x, x, i32([0, 1, 2]), kv_starts=i32(starts), status=status)
+        assert status.item() == paged.TQ_DEV_ERR_LENGTH
+
+
+# ---- streams, graphs, and the operators together ----
+
+def test_a_captured_step_replays_on_new_lengths():
+    """map, append and attention of one step in a graph; two graphs that share one workspace replay in turn."""
+    d, hkv, hq, room = 128, 2, 8, 6
+    pool = paged.BlockPool(40, 4, 2048)
+    cache = paged.PagedCache(1, pool, hkv, d)
+    ids, lens, new = i32([3, 1]), i32([0, 0]), i32([0, 0])
+    k = torch.zeros((room, hkv, d), dtype=torch.bfloat16, device=DEV)
+    v, q = torch.zeros_like(k), torch.zeros((room, hq, d), dtype=torch.bfloat16, device=DEV)
+    out = torch.zeros_like(q)
+    need = paged.attention_workspace_bytes(q, cache.kv[0, 0], room, 2048, 2, pool.table.shape[1])
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
+
+    def step():
+        slots, starts, totals = pool.map(ids, lens, new, room)
+        cache.append(0, k, v, slots)
+        cache.attention(0, q, ids, starts, totals, max_q=room, max_kv=2048, out=out, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    seen = [[[], []], [[], []]]
+    have = [0, 0]
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    for i, count in enumerate([(4, 2), (1, 1), (0, 5), (6, 0), (2, 3), (1, 1)]):
+        for x in (k, v, q):
+            x.copy_(torch.randn(x.shape, generator=gen, device=DEV))
+        lens.copy_(i32(have))
+        new.copy_(i32(list(count)))
+        graphs[i % 2].replay()
+        s = 0
+        for b, n in enumerate(count):
+            seen[b][0].append(k[s:s + n].clone())
+            seen[b][1].append(v[s:s + n].clone())
+            s += n
+        have = [h + n for h, n in zip(have, count)]
+        check_rows(out, q, [torch.cat(x[0]) for x in seen], [torch.cat(x[1]) for x in seen], list(count), have, True, 1 / math.sqrt(d))
+    assert pool.check_status() == 0
+
+
+def test_calls_on_another_stream():
+    nq, kv = [1, 2], [3000, 700]
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, 128, torch.bfloat16, False, 9)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = [paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=2, max_kv=3000, stream=s)
+            for s in (side, None, side, None)]
+    torch.cuda.current_stream().wait_stream(side)
+    for out in outs:
+        check_rows(out, q, ks, vs, nq, kv, True, 1 / math.sqrt(128))
+
+
+def test_packed_and_exact_layers_share_one_block_table():
+    """A serving loop: prompts, decode steps, a rollback and a release. The packed cache's layer and the exact layer use the
+    same table; the exact layer's attention is checked against 64 bits, the packed one's against a cache of its own blocks."""
+    d, hkv, hq, seqs = 128, 2, 8, 3
+    cfg = tqm.config(head_dim=d, n_layers=1, n_kv_heads=hkv, n_q_heads=hq, max_seqs=seqs, max_ctx=1024, n_blocks=20, seed=4)
+    flat = tqm.config(head_dim=d, n_layers=1, n_kv_heads=hkv, n_q_heads=hq, max_seqs=seqs, max_ctx=1024, seed=4)
+    packed, plain = tqm.TurboQuantCache(cfg), tqm.TurboQuantCache(flat)
+    pool = packed.block_pool
+    exact = paged.PagedCache(1, pool, hkv, d)
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    have, ks, vs = [0] * seqs, [[] for _ in range(seqs)], [[] for _ in range(seqs)]
+    for count in ([200, 130, 1], [1, 1, 1], [1, 1, 127], [60, 1, 1]):
+        total, most = sum(count), max(count)
+        k, v = (torch.randn((total, hkv, d), generator=gen, device=DEV).bfloat16() for _ in range(2))
+        q = torch.randn((total, hq, d), generator=gen, device=DEV).bfloat16()
+        ids = i32([2, 0, 1])
+        slots, starts, totals = pool.map(ids, i32(have), i32(count), total)
+        exact.append(0, k, v, slots)
+        out = exact.attention(0, q, ids, starts, totals, max_q=most, max_kv=1024)
+        padded = [torch.zeros((seqs, most, hkv, d), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        s = starts_of(count)
+        for b in range(seqs):
+            for x, p, keep in ((k, padded[0], ks), (v, padded[1], vs)):
+                p[b, :count[b]] = x[s[b]:s[b + 1]]
+                keep[b].append(x[s[b]:s[b + 1]])
+        have = [h + n for h, n in zip(have, count)]
+        check_rows(out, q, [torch.cat(x) for x in ks], [torch.cat(x) for x in vs], count, have, True, 1 / math.sqrt(d))
+        last = q[torch.tensor([x - 1 for x in s[1:]], device=DEV)].contiguous()
+        for cache in (packed, plain):
+            cache.append(0, padded[0], padded[1], ids, i32(count))
+        assert torch.equal(packed.decode(0, last, ids), plain.decode(0, last, ids))
+    assert pool.check_status() == 0 and packed.check_status() == 0
+    assert pool.n_free.item() == 20 - sum(ref.pages(h) for h in have)
+    pool.release(i32([0, 1, 2]))
+    assert pool.n_free.item() == 20
+    assert packed.block_pool is pool and plain.block_pool is None
+
+
+def test_a_pool_needs_an_untouched_table():
+    cache = tqm.TurboQuantCache(tqm.config(n_blocks=4, max_ctx=256))
+    cache.block_table[0, 0] = 2
+    with pytest.raises(ValueError):
+        cache.block_pool
+
+
+def test_offsets_past_32_bits():
+    """Blocks whose elements lie past 2^31 elements (and 4 GB) of the pool."""
+    d, hkv, blocks = 128, 8, 20000  # 2.6 G elements per pool
+    pool = torch.empty((blocks, 128, hkv, d), dtype=torch.bfloat16, device=DEV)
+    vpool = torch.empty_like(pool)
+    n = 200
+    table = i32([[blocks - 1, blocks - 3]])
+    k, v = (torch.randn((n, hkv, d), device=DEV).bfloat16() for _ in range(2))
+    slots = torch.cat([(blocks - 1) * 128 + torch.arange(128), (blocks - 3) * 128 + torch.arange(72)]).to(torch.int32).to(DEV)
+    paged.append(k, v, pool, vpool, slots)
+    assert torch.equal(pool[blocks - 1], k[:128]) and torch.equal(vpool[blocks - 3, :72], v[128:])
+    q = torch.randn((40, hkv, d), device=DEV).bfloat16()
+    for rows in (1, 40):
+        out = paged.attention(q[:rows], pool, vpool, table, None, i32([0, rows]), i32([n]), max_q=rows)
+        check_rows(out, q[:rows], [k], [v], [rows], [n], True, 1 / math.sqrt(d))
+
+
+def test_refusals():
+    pool = torch.zeros((3, 128, 2, 64), dtype=torch.bfloat16, device=DEV)
+    table, one = i32([[0, 1, 2]]), i32([1])
+    q = torch.zeros((1, 4, 64), dtype=torch.bfloat16, device=DEV)
+
+    def bad(exc, **over):
+        args = {"q": q, "k_pool": pool, "v_pool": pool, "table": table, "seq_ids": None, "q_starts": i32([0, 1]), "kv_lens": one, **over}
+        with pytest.raises(exc):
+            paged.attention(**args)
+
+    bad(ValueError, q=q.half())
+    bad(ValueError, q=q[:, :3])
+    bad(ValueError, q=q.cpu())
+    bad(ValueError, v_pool=pool[:2])
+    bad(ValueError, k_pool=pool.float(), v_pool=pool.float())
+    bad(ValueError, k_pool=pool[:, :64], v_pool=pool[:, :64])
+    bad(ValueError, table=table.long())
+    bad(ValueError, q_starts=torch.tensor([0, 1], device=DEV))
+    bad(ValueError, kv_lens=i32([]))
+    bad(ValueError, seq_ids=i32([]))
+    bad(ValueError, out=torch.zeros_like(q)[:, :2])
+    bad(ValueError, status=torch.zeros(1, dtype=torch.int32))
+    bad(tqm.TQError, q_starts=i32([0, 1, 1]), kv_lens=i32([1, 1]))  # two requests, one table row, no ids
+    bad(tqm.TQError, max_q=-1)
+    bad(tqm.TQError, softmax_scale=float("nan"))
+    odd = torch.zeros((3, 128, 2, 68), dtype=torch.bfloat16, device=DEV)
+    bad(tqm.TQError, k_pool=odd[..., 4:], v_pool=odd[..., 4:])  # rows not 16-byte aligned
+    wide = torch.zeros((3, 128, 1, 64), dtype=torch.bfloat16, device=DEV).expand(3, 128, 2, 64)
+    bad(tqm.TQError, k_pool=wide, v_pool=wide)  # one head's memory for two
+    bad(tqm.TQError, q=torch.zeros((1, 4, 65), dtype=torch.bfloat16, device=DEV)[..., 1:])
+    d96 = torch.zeros((3, 128, 2, 96), dtype=torch.bfloat16, device=DEV)
+    bad(tqm.TQError, q=torch.zeros((1, 4, 96), dtype=torch.bfloat16, device=DEV), k_pool=d96, v_pool=d96)
+    long = torch.zeros((100, 128, 2, 64), dtype=torch.bfloat16, device=DEV)
+    bad(tqm.TQError, k_pool=long, v_pool=long, table=torch.zeros((1, 90), dtype=torch.int32, device=DEV),
+        workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    x = torch.zeros((2, 2, 64), dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError):
+        paged.cross_attention(q, x, x, i32([0, 1]))
+    with pytest.raises(ValueError):
+        paged.cross_attention(q, x, x, i32([0, 1]), kv_lens=one)
+    with pytest.raises(ValueError):
+        paged.append(x, x[:, :1], pool, pool, i32([0, 1]))
+    with pytest.raises(ValueError):
+        paged.append(x, x, pool, pool, i32([0]))
+    with pytest.raises(ValueError):
+        paged.map_blocks(table, i32([0]), one, one, one, i32([]), 1)
+    with pytest.raises(tqm.TQError):
+        paged.map_blocks(table, i32([0]), one, one, one, one, -1)
