@@ -185,10 +185,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D>::kCtas)
   bool ok = true;
   for (int u = u0; u < u1; ++u) {
     const int k = u - u0, st = k % ST;
-    if (!mbar_wait(&full[st], (k / ST) & 1)) {
-      ok = false;
-      break;
-    }
+    ok = __all_sync(0xffffffffu, mbar_wait(&full[st], (k / ST) & 1));
+    if (!ok) break;
     const int t0 = u * kUnit + warp * 16;
     if (t0 < kv) {
       const uint32_t kt = base + st * 2 * kTile, vt = kt + kTile;
@@ -463,17 +461,25 @@ cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtens
 
 AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int sms) {
   AttnPlan p;
-  const int G = q.n_q_heads / kv.n_kv_heads;
+  const int G = q.n_q_heads / kv.n_kv_heads, d = kv.head_dim;
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * G;
-  p.tile_rows = rows <= 16 || kv.head_dim == 256 ? 16 : 32;
-  p.unit = kUnit;
+  p.max_rows = rows;
+  p.tc = rows > (d == 256 ? 16 : 32);
+  if (p.tc) {
+    p.tile_rows = attn_tc_tile_rows(d);
+    p.unit = attn_tc_unit(d);
+    // packed tiles (find_tile): the last request's last tile is below floor(n_rows G / tile_rows) + batch
+    p.tiles = (int64_t)q.n_rows * G / p.tile_rows + q.batch;
+  } else {
+    p.tile_rows = rows <= 16 ? 16 : 32;
+    p.unit = kUnit;
+    p.tiles = q.batch;
+  }
   int64_t tokens = max_tokens;
   if (q.max_kv > 0) tokens = std::min<int64_t>(tokens, q.max_kv);
   const int64_t units = std::max<int64_t>(1, (tokens + p.unit - 1) / p.unit);
-  p.packed = false;
-  p.tiles = std::max<int64_t>(1, (int64_t)q.batch * ((rows + p.tile_rows - 1) / p.tile_rows));
   const int64_t base = p.tiles * kv.n_kv_heads;
-  const int64_t slots = (int64_t)sms * (kv.head_dim == 256 ? 1 : 2);
+  const int64_t slots = (int64_t)sms * (p.tc || d == 256 ? 1 : 2);
   // the fewest splits within 3 % of the least cost: waves of CTAs x (units of a CTA + about 4 for its start and end)
   const int most = (int)std::min<int64_t>(units, kMaxAttnSplits);
   auto cost = [&](int n) {
@@ -484,7 +490,6 @@ AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int
   for (int n = 2; n <= most; ++n) best = std::min(best, cost(n));
   p.n_splits = 1;
   while (cost(p.n_splits) > 1.03 * best) ++p.n_splits;
-  p.max_rows = rows;
   p.bytes = 0;
   if (p.n_splits > 1) {
     const size_t slots_n = (size_t)q.n_rows * q.n_q_heads * p.n_splits;
@@ -498,7 +503,8 @@ cudaError_t launch_attention(const AttnArgs& a, const tq_kv& kv, const AttnPlan&
   cudaError_t e = attn_tensor_map(kv, false, p.unit, &m.k);
   if (e == cudaSuccess) e = attn_tensor_map(kv, true, p.unit, &m.v);
   if (e != cudaSuccess) return e;
-  e = kv.dtype == TQ_BF16 ? launch_rows<true>(a, m, kv.head_dim, p.tile_rows, s)
+  e = p.tc                  ? launch_attn_tc(a, m, p, kv.head_dim, kv.dtype, s)
+      : kv.dtype == TQ_BF16 ? launch_rows<true>(a, m, kv.head_dim, p.tile_rows, s)
                           : launch_rows<false>(a, m, kv.head_dim, p.tile_rows, s);
   if (e != cudaSuccess || p.n_splits == 1) return e;
   return kv.head_dim == 64    ? launch_join<64>(a, p, kv.dtype, s)

@@ -181,9 +181,13 @@ struct AttnPlan {
   int n_splits;
   int64_t max_rows;  // rows (query, head of the group) of a request and KV head at most
   int64_t tiles;     // tiles of one KV head over all requests
-  bool packed;       // tiles are packed (find_tile)
+  bool tc;           // tensor-core kernel, packed tiles (find_tile)
   size_t bytes;
 };
+// Tensor-core kernel (tq_attention_tc.cu): its tiles and units, and the launch.
+int attn_tc_tile_rows(int d);
+int attn_tc_unit(int d);
+cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int sms);
 cudaError_t launch_attention(const AttnArgs& a, const tq_kv& kv, const AttnPlan& p, cudaStream_t s);
 

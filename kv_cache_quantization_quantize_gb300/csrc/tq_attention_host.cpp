@@ -130,7 +130,7 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, int m
   a.tokens = kv.tokens;
   a.n_splits = p.n_splits;
   a.max_rows = (int)p.max_rows;
-  a.tiles = p.packed ? 0 : (int)(p.tiles / q->batch);
+  a.tiles = p.tc ? 0 : (int)(p.tiles / q->batch);
   return done(tq::launch_attention(a, kv, p, (cudaStream_t)stream), "attention launch");
 }
 
