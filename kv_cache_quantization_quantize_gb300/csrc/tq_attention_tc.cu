@@ -36,6 +36,27 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
+// Registers per thread from here on (executed by every warp of a warpgroup).
+template <int N>
+__device__ __forceinline__ void set_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+// A value that all lanes of the warp hold, told to the compiler as such (the MMA operands sit in uniform registers).
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
 // 32 columns of this thread's TMEM lane, without the wait.
 __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* r) {
   asm volatile(
@@ -88,13 +109,13 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(skv + ST * kTile);
   uint64_t* empty = full + ST;
   uint64_t* s_full = empty + ST;  // per tile: scores are in TMEM
-  uint64_t* p_full = s_full + NT;  // per tile: weights are in TMEM, O is rescaled
-  uint64_t* o_full = p_full + NT;  // per tile: the product with V is done
+  uint64_t* p_full = s_full + NT;  // per tile and half of the unit: weights are in TMEM, O is rescaled
+  uint64_t* o_full = p_full + 2 * NT;  // per tile: the product with V is done
   uint64_t* drained = o_full + NT;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drained + 1);
   __shared__ int gave_up;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   constexpr int kMmaWarp = NT * 4, kTmaWarp = NT * 4 + 1;
   if (threadIdx.x == 0) {
     gave_up = 0;
@@ -104,7 +125,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     }
     for (int i = 0; i < NT; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[2 * i], 4);
+      mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
     }
     mbar_init(drained, 1);
@@ -159,123 +181,138 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_base;
-
-  if (warp == kTmaWarp) {
-    // ---- K and V tiles: ring entry 2 k holds K of unit u0 + k, entry 2 k + 1 its V ----
-    int2 place = make_int2(0, 0);
-    bool ok = true;
-    int issued = 0;
-    for (int k = 0; k < n_all && ok; ++k) {
-      if ((k & 31) == 0 && k + lane < n_all) {
-        const int tok = (u0 + k + lane) * BN;
-        place = page_place(a, r, tok / kPage, err);
-        place.y += tok % kPage;
+  const uint32_t tmem = uniform(*tmem_base);
+  // The softmax threads hold a row of scores: they take registers from the other warps (8 x 32 x 216 + 4 x 32 x 72 =
+  // 384 x 168, what the block was launched with). One tile's warps have enough as it is.
+  constexpr bool kSplitRegs = NT == 2;
+  if (warp >= kMmaWarp) {
+    if constexpr (kSplitRegs) set_regs_dec<72>();
+    if (warp == kTmaWarp) {
+      // ---- K and V tiles: ring entry 2 k holds K of unit u0 + k, entry 2 k + 1 its V ----
+      int2 place = make_int2(0, 0);
+      bool ok = true;
+      int issued = 0;
+      for (int k = 0; k < n_all && ok; ++k) {
+        if ((k & 31) == 0 && k + lane < n_all) {
+          const int tok = (u0 + k + lane) * BN;
+          place = page_place(a, r, tok / kPage, err);
+          place.y += tok % kPage;
+        }
+        const int w = __shfl_sync(0xffffffffu, place.x, k & 31), y = __shfl_sync(0xffffffffu, place.y, k & 31);
+        if (lane == 0) {
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            const int e = 2 * k + which, st = e % ST;
+            if (ok && e >= ST) ok = mbar_wait(&empty[st], ((e / ST) - 1) & 1);
+            if (!ok) break;
+            uint8_t* dst = skv + st * kTile;
+            mbar_expect_tx(&full[st], kTile);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_4d(dst + c * (BN * 128), which ? &map_v : &map_k, c * 64, y, h, w, &full[st]);
+            issued = e + 1;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      const int w = __shfl_sync(0xffffffffu, place.x, k & 31), y = __shfl_sync(0xffffffffu, place.y, k & 31);
       if (lane == 0) {
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-          const int e = 2 * k + which, st = e % ST;
-          if (ok && e >= ST) ok = mbar_wait(&empty[st], ((e / ST) - 1) & 1);
-          if (!ok) break;
-          uint8_t* dst = skv + st * kTile;
-          mbar_expect_tx(&full[st], kTile);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            tma_load_4d(dst + c * (BN * 128), which ? &map_v : &map_k, c * 64, y, h, w, &full[st]);
-          issued = e + 1;
+        // leave only when every copy has landed (they have, unless a wait gave up)
+        for (int e = max(0, issued - ST); e < issued; ++e) ok &= mbar_wait(&full[e % ST], (e / ST) & 1);
+        if (!ok) {
+          err |= TQ_DEV_ERR_TIMEOUT;
+          atomicExch(&gave_up, 1);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-    if (lane == 0) {
-      // leave only when every copy has landed (they have, unless a wait gave up)
-      for (int e = max(0, issued - ST); e < issued; ++e) ok &= mbar_wait(&full[e % ST], (e / ST) & 1);
-      if (!ok) {
-        err |= TQ_DEV_ERR_TIMEOUT;
-        atomicExch(&gave_up, 1);
-      }
-    }
-    if (err && a.status) atomicOr(a.status, err);
-  } else if (warp == kMmaWarp) {
-    // ---- products: S_t(0), S_1(0), then per unit and tile O_t += P_t V and the next S_t ----
-    bool ok = true;
-    const uint32_t q_lo = umma_desc_sw128_lo(smem_u32(smem)), kv_lo = smem_u32(skv) >> 4;
-    auto scores = [&](int t, int k) {  // S_t = Q_t K(k)^T
-      if (lane == 0) {
-        const uint32_t ka = kv_lo + ((2 * k) % ST) * (kTile >> 4) + (1u << 16);
+      if (err && a.status) atomicOr(a.status, err);
+    } else if (warp == kMmaWarp) {
+      // ---- products: S_t(0), S_1(0), then per unit and tile O_t += P_t V and the next S_t ----
+      bool ok = true;
+      const bool leader = elect_one();
+      n_all = uniform(n_all);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t step = (i & 3) * 2;
-          umma_bf16_lo(tmem + Sh::kS + t * 128, q_lo + t * (Sh::kQ >> 4) + (i >> 2) * 1024 + step,
-                       ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
+      for (int t = 0; t < NT; ++t) n_of[t] = uniform(n_of[t]);
+      const uint32_t q_lo = umma_desc_sw128_lo(smem_u32(smem)), kv_lo = smem_u32(skv) >> 4;
+      auto scores = [&](int t, int k) {  // S_t = Q_t K(k)^T
+        if (leader) {
+          const uint32_t ka = kv_lo + ((2 * k) % ST) * (kTile >> 4) + (1u << 16);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t step = (i & 3) * 2;
+            umma_bf16_lo(tmem + Sh::kS + t * 128, q_lo + t * (Sh::kQ >> 4) + (i >> 2) * 1024 + step,
+                         ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
+          }
+          umma_commit(&s_full[t]);
         }
-        umma_commit(&s_full[t]);
-      }
-    };
-    if (n_all > 0) ok = warp_wait(&full[0], 0);
-    if (ok && n_all > 0) {
-      tc_fence_after();
+      };
+      if (n_all > 0) ok = warp_wait(&full[0], 0);
+      if (ok && n_all > 0) {
+        tc_fence_after();
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        if (n_of[t] > 0) scores(t, 0);
-      if (lane == 0) umma_commit(&empty[0]);
-    }
-    for (int k = 0; k < n_all && ok; ++k) {
-      const int ve = 2 * k + 1, vs = ve % ST;
-      ok = warp_wait(&full[vs], (ve / ST) & 1);
-      if (!ok) break;
-      // the unit that the sequence ends in: V rows behind it are zeroed up to the next step of 16 (0 x NaN is NaN),
-      // and the steps behind them are left out
-      const int valid = min(BN, kv - (u0 + k) * BN), steps = (valid + 15) / 16;
-      if (valid & 15) {
-        const int n = (16 - (valid & 15)) * (D / 8);
-        for (int i = lane; i < n; i += 32) {
-          const int c = i % (D / 8), row = valid + i / (D / 8);
-          *reinterpret_cast<uint4*>(skv + vs * kTile + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
-              make_uint4(0, 0, 0, 0);
+        for (int t = 0; t < NT; ++t)
+          if (n_of[t] > 0) scores(t, 0);
+        if (leader) umma_commit(&empty[0]);
+      }
+      for (int k = 0; k < n_all && ok; ++k) {
+        const int ve = 2 * k + 1, vs = ve % ST;
+        ok = warp_wait(&full[vs], (ve / ST) & 1);
+        if (!ok) break;
+        // the unit that the sequence ends in: V rows behind it are zeroed up to the next step of 16 (0 x NaN is NaN),
+        // and the steps behind them are left out
+        const int valid = uniform(min(BN, kv - (u0 + k) * BN)), steps = (valid + 15) / 16;
+        if (valid & 15) {
+          const int n = (16 - (valid & 15)) * (D / 8);
+          for (int i = lane; i < n; i += 32) {
+            const int c = i % (D / 8), row = valid + i / (D / 8);
+            *reinterpret_cast<uint4*>(skv + vs * kTile + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_async_smem();
+          __syncwarp();
         }
-        fence_async_smem();
-        __syncwarp();
-      }
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (k < n_of[t] && ok) {
-          ok = warp_wait(&p_full[t], k & 1);
-          if (!ok) break;
-          tc_fence_after();
-          if (lane == 0) {
+        for (int t = 0; t < NT; ++t) {
+          if (k < n_of[t] && ok) {
             // MN-major operand: 64-channel blocks BN x 128 bytes apart, 8-token groups 1024 bytes apart
             const uint32_t va = kv_lo + vs * (kTile >> 4) + ((uint32_t)(BN * 128 >> 4) << 16);
-            for (int i = 0; i < steps; ++i)
-              umma_ts_lo(tmem + Sh::kO + t * D, tmem + Sh::kS + t * 128 + i * 8, va + i * (2048 >> 4), kIdescO,
-                         (k > 0 || i > 0));
-            umma_commit(&o_full[t]);
-          }
-        }
-        if (t == NT - 1 && lane == 0) umma_commit(&empty[vs]);
-        if (k + 1 < n_all && ok) {
-          const int ke = 2 * (k + 1), ks = ke % ST;
-          if (t == 0) ok = warp_wait(&full[ks], (ke / ST) & 1);
-          if (k + 1 < n_of[t] && ok) {
-            ok = warp_wait(&o_full[t], k & 1);  // S_t(k + 1) goes over P_t(k)
+            const uint32_t od = tmem + Sh::kO + t * D, pa = tmem + Sh::kS + t * 128;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && warp_wait(&p_full[2 * t + half], k & 1);
+              if (!ok) break;
+              tc_fence_after();
+              if (leader) {
+#pragma unroll
+                for (int i = half * (BN / 32); i < (half + 1) * (BN / 32); ++i)
+                  if (i < steps) umma_ts_lo(od, pa + i * 8, va + i * (2048 >> 4), kIdescO, k > 0 || i > 0);
+              }
+            }
             if (!ok) break;
-            tc_fence_after();
-            scores(t, k + 1);
+            if (leader) umma_commit(&o_full[t]);
           }
-          if (t == NT - 1 && lane == 0) umma_commit(&empty[ks]);
+          if (t == NT - 1 && leader) umma_commit(&empty[vs]);
+          if (k + 1 < n_all && ok) {
+            const int ke = 2 * (k + 1), ks = ke % ST;
+            if (t == 0) ok = warp_wait(&full[ks], (ke / ST) & 1);
+            if (k + 1 < n_of[t] && ok) {
+              ok = warp_wait(&o_full[t], k & 1);  // S_t(k + 1) goes over P_t(k)
+              if (!ok) break;
+              tc_fence_after();
+              scores(t, k + 1);
+            }
+            if (t == NT - 1 && leader) umma_commit(&empty[ks]);
+          }
         }
       }
+      // leave only when every product is done
+      if (leader) umma_commit(drained);
+      const bool done = warp_wait(drained, 0);
+      if ((!ok || !done) && leader) {
+        atomicExch(&gave_up, 1);
+        if (a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
+      }
     }
-    // leave only when every product is done
-    if (lane == 0) umma_commit(drained);
-    const bool done = warp_wait(drained, 0);
-    if ((!ok || !done) && lane == 0) {
-      atomicExch(&gave_up, 1);
-      if (a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
-    }
-  } else if (warp < kMmaWarp) {
+  } else {
+    if constexpr (kSplitRegs) set_regs_inc<216>();
     // ---- softmax of tile t: a thread per row ----
     const int t = warp >> 2;
     const int n = t == 0 ? n_of[0] : n_of[NT - 1];
@@ -334,24 +371,27 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const float2 sc = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-mu, -mu);
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int c = 0; c < BN; c += 32) {
-        uint32_t p[16];
+      for (int half = 0; half < 2; ++half) {  // the product with the first half of V starts while the second is made
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 y = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), sc, off);
-          y.x = exp2_fast(y.x);
-          y.y = exp2_fast(y.y);
-          sum[i & 1] = add2(sum[i & 1], y);
-          p[i] = pack2<BF16>(y.x, y.y);
+        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 y = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), sc, off);
+            y.x = exp2_fast(y.x);
+            y.y = exp2_fast(y.y);
+            sum[i & 1] = add2(sum[i & 1], y);
+            p[i] = pack2<BF16>(y.x, y.y);
+          }
+          tmem_st16(ts + c / 2, p);
         }
-        tmem_st16(ts + c / 2, p);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
       }
       const float2 both = add2(sum[0], sum[1]);
       l += both.x + both.y;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[t]);
     }
     if (ok && n > 0) ok = warp_wait(&o_full[t], (n - 1) & 1);
     if (!ok) {
