@@ -359,13 +359,13 @@ __global__ void __launch_bounds__(128)
   const int in_tile = x % rows;
   x /= rows;
   const int h = x % a.hkv;
-  const int2 t = find_tile(a, x / a.hkv, tile_rows);
+  const int b = x / a.hkv / a.tiles, tile = x / a.hkv % a.tiles;
   uint32_t err = 0;
-  const Request r = find_request(a, t.x, err);
-  const int f = t.y * tile_rows + in_tile;
+  const Request r = find_request(a, b, err);
+  const int f = tile * tile_rows + in_tile;
   if (f >= r.n_q * (int64_t)a.G || r.n_q * (int64_t)a.G > a.max_rows) return;
   const int row = r.q0 + f / a.G, head = h * a.G + f % a.G;
-  const int kv = tile_kv(a, r, t.y, tile_rows);
+  const int kv = tile_kv(a, r, tile, tile_rows);
   const int units = (kv + unit - 1) / unit, per = units_per_split(units, a.n_splits);
   if (units <= per) return;  // its kernel has written the result
   const int live = (units + per - 1) / per;
@@ -465,21 +465,22 @@ AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * G;
   p.max_rows = rows;
   p.tc = rows > (d == 256 ? 16 : 32);
+  p.ctas = sms;
+  p.tiles = 1;
+  p.tile_rows = p.n_splits = 1;
   if (p.tc) {
-    p.tile_rows = attn_tc_tile_rows(d);
     p.unit = attn_tc_unit(d);
-    // packed tiles (find_tile): the last request's last tile is below floor(n_rows G / tile_rows) + batch
-    p.tiles = (int64_t)q.n_rows * G / p.tile_rows + q.batch;
-  } else {
-    p.tile_rows = rows <= 16 ? 16 : 32;
-    p.unit = kUnit;
-    p.tiles = q.batch;
+    p.bytes = attn_tc_bytes(d, sms);
+    return p;
   }
+  p.tile_rows = rows <= 16 ? 16 : 32;
+  p.unit = kUnit;
+  p.tiles = q.batch;
   int64_t tokens = max_tokens;
   if (q.max_kv > 0) tokens = std::min<int64_t>(tokens, q.max_kv);
   const int64_t units = std::max<int64_t>(1, (tokens + p.unit - 1) / p.unit);
   const int64_t base = p.tiles * kv.n_kv_heads;
-  const int64_t slots = (int64_t)sms * (p.tc || d == 256 ? 1 : 2);
+  const int64_t slots = (int64_t)sms * (d == 256 ? 1 : 2);
   // the fewest splits within 3 % of the least cost: waves of CTAs x (units of a CTA + about 4 for its start and end)
   const int most = (int)std::min<int64_t>(units, kMaxAttnSplits);
   auto cost = [&](int n) {
@@ -506,7 +507,7 @@ cudaError_t launch_attention(const AttnArgs& a, const tq_kv& kv, const AttnPlan&
   e = p.tc                  ? launch_attn_tc(a, m, p, kv.head_dim, kv.dtype, s)
       : kv.dtype == TQ_BF16 ? launch_rows<true>(a, m, kv.head_dim, p.tile_rows, s)
                           : launch_rows<false>(a, m, kv.head_dim, p.tile_rows, s);
-  if (e != cudaSuccess || p.n_splits == 1) return e;
+  if (e != cudaSuccess || p.tc || p.n_splits == 1) return e;
   return kv.head_dim == 64    ? launch_join<64>(a, p, kv.dtype, s)
          : kv.head_dim == 128 ? launch_join<128>(a, p, kv.dtype, s)
                               : launch_join<256>(a, p, kv.dtype, s);

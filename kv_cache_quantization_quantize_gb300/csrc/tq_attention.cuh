@@ -11,6 +11,18 @@ constexpr int kMaxAttnSplits = 128;
 
 enum KvMode { kKvPaged = 0, kKvPadded = 1, kKvPacked = 2 };
 
+// x / d for 0 <= x < 2^31 and a d that does not change in a launch: (mulhi(x, m) + x) >> s (Granlund and Montgomery,
+// Division by invariant integers using multiplication, 1994).
+struct FastDiv {
+  uint32_t m, s;
+  void set(uint32_t d) {
+    s = 0;
+    while ((1ull << s) < d) ++s;
+    m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+  }
+  __device__ __forceinline__ int operator()(int x) const { return (int)((__umulhi((uint32_t)x, m) + (uint32_t)x) >> s); }
+};
+
 struct AttnArgs {
   const void* q;
   void* out;
@@ -25,10 +37,11 @@ struct AttnArgs {
   float* part;               // partials of the splits (see part_slot)
   float scale_log2;          // softmax scale * log2(e)
   int n_rows, batch, hq, hkv, G;
+  FastDiv div_g;             // by G
   int max_seqs, max_pages, outer, tokens;
   int mode, causal;
   int n_splits, max_rows;    // max_rows: rows (query, head of the group) of a request and KV head at most
-  int tiles;                 // tiles of every request; 0: packed tiles (find_tile)
+  int tiles;                 // rows kernel: tiles of every request
 };
 
 // One request as its CTA sees it. Bad arrays give an empty request and status bits.
@@ -105,32 +118,6 @@ __device__ __forceinline__ int tile_kv(const AttnArgs& a, const Request& r, int 
 // Splits of a range of `units`: split s takes units [s * per, min(units, (s + 1) * per)).
 __device__ __forceinline__ int units_per_split(int units, int n_splits) { return (units + n_splits - 1) / n_splits; }
 
-// The last b in [0, n) whose key(b) is <= x, for keys that do not fall and key(0) <= x (else 0). All 32 lanes of a
-// warp call it with the same x; each round reads 32 keys at once, so a batch of 1024 takes two rounds of loads.
-template <typename Key>
-__device__ __forceinline__ int find_last(int n, int x, Key key) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0;
-  while (n > 1) {
-    const int step = (n + 31) / 32, at = lane * step;
-    const uint32_t m = __ballot_sync(0xffffffffu, at < n && key(lo + at) <= x);
-    const int k = m ? 31 - __clz(m) : 0;
-    lo += k * step;
-    n = min(step, n - k * step);
-  }
-  return lo;
-}
-
-// The tile with index x of the launch: its request and its place there. A fixed number of tiles per request where
-// all have few rows; else request b's tiles start at index floor(q_starts[b] * G / tile_rows) + b, which leaves each
-// request as many as it needs and at most one more. Attention kernel and join find the same tile.
-__device__ __forceinline__ int2 find_tile(const AttnArgs& a, int x, int tile_rows) {
-  if (a.tiles > 0) return make_int2(x / a.tiles, x % a.tiles);
-  auto key = [&](int i) { return (int)(((int64_t)a.q_starts[i] * a.G) / tile_rows) + i; };
-  const int b = find_last(a.batch, x, key);
-  return make_int2(b, max(0, x - key(b)));
-}
-
 // Partial of (row of q, query head) and split s: {m, l} and D floats of the weighted sum; weights are
 // exp2(score * scale_log2 - m) and l their sum. All {m, l} come first.
 __device__ __forceinline__ size_t part_slot(const AttnArgs& a, int row, int head, int s) {
@@ -176,16 +163,17 @@ struct AttnMaps {
 cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m);
 // One launch plan: which kernel, its tiles and splits, and the bytes of partials it needs.
 struct AttnPlan {
-  int tile_rows;  // rows (query, head of the group) of a tile
-  int unit;       // tokens of a unit: splits take whole units
-  int n_splits;
+  int unit;          // tokens of a unit: splits take whole units
+  int tile_rows;     // rows kernel: rows (query, head of the group) of a tile
+  int n_splits;      // rows kernel
   int64_t max_rows;  // rows (query, head of the group) of a request and KV head at most
-  int64_t tiles;     // tiles of one KV head over all requests
-  bool tc;           // tensor-core kernel, packed tiles (find_tile)
+  int64_t tiles;     // rows kernel: tiles of one KV head over all requests
+  bool tc;           // tensor-core kernel
+  int ctas;          // its CTAs
   size_t bytes;
 };
-// Tensor-core kernel (tq_attention_tc.cu): its tiles and units, and the launch.
-int attn_tc_tile_rows(int d);
+// Tensor-core kernel (tq_attention_tc.cu): its workspace, its unit of tokens, and the launch.
+size_t attn_tc_bytes(int d, int ctas);
 int attn_tc_unit(int d);
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int sms);

@@ -126,11 +126,12 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, int m
   a.hq = q->n_q_heads;
   a.hkv = kv.n_kv_heads;
   a.G = a.hq / a.hkv;
+  a.div_g.set((uint32_t)a.G);
   a.outer = kv.outer;
   a.tokens = kv.tokens;
   a.n_splits = p.n_splits;
   a.max_rows = (int)p.max_rows;
-  a.tiles = p.tc ? 0 : (int)(p.tiles / q->batch);
+  a.tiles = (int)std::max<int64_t>(1, p.tiles / q->batch);
   return done(tq::launch_attention(a, kv, p, (cudaStream_t)stream), "attention launch");
 }
 

@@ -11,8 +11,9 @@ namespace {
 // k_attn_tc: one CTA takes NT tiles of 128 rows (query, head of the group) of one request and KV head, and one
 // split of its tokens. The rows of a group share K and V, so a tile is full at any group size.
 //   - a TMA warp keeps a ring of K and V tiles (BN tokens) in flight, in the 128-byte swizzle;
-//   - an MMA warp issues S_t = Q_t K^T into TMEM, and O_t += P_t V with P_t read from TMEM and V taken as it lies
-//     (tokens x channels, the MN-major operand form);
+//   - an MMA warp per tile issues S_t = Q_t K^T into TMEM, and O_t += P_t V with P_t read from TMEM and V taken as it
+//     lies (tokens x channels, the MN-major operand form); with a warp per tile, neither tile's waits hold up the
+//     other's products;
 //   - a warpgroup per tile reads S_t (a thread per row, so row sums need no exchange), writes P_t = 2^(s - m) in 16
 //     bits over it, and rescales O_t only where a row's maximum grew by more than 2^8: the weights stay below
 //     2^8, far inside fp32 and f16, and the final division takes the factor out.
@@ -27,8 +28,12 @@ struct TcShape {
   static constexpr int kThreads = kNT * 128 + 128;
   static constexpr int kQ = 128 * D * 2;           // bytes of a tile's queries
   static constexpr int kSmem = 1024 + kNT * kQ + kStages * kTile + 512;
-  static constexpr uint32_t kS = 0;                // TMEM columns: S_t (P_t over it) at kS + t * 128, O_t at kO + t * D
-  static constexpr uint32_t kO = 256;
+  // TMEM columns: S_t at t * 128, P_t at kP + t * kPStep, O_t at kO + t * D. At D = 128 they fill all 512 columns
+  // with P_t over S_t, so that the next S_t waits for P_t's product; else P_t has a place of its own, and the next
+  // S_t is made while the softmax works on this one.
+  static constexpr bool kOwnP = D != 128;
+  static constexpr uint32_t kP = kOwnP ? (D == 64 ? 256 : 128) : 0, kPStep = kOwnP ? 64 : 128;
+  static constexpr uint32_t kO = D == 64 ? 384 : 256;
 };
 
 // A warp's wait on an mbarrier: every lane waits, all go on together, and all give up if one does.
@@ -89,15 +94,107 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
+// ---------------------------------------------------------------------------------------------
+// The split of the work. All tiles of all requests and KV heads lie on one line, in the order (request, head, tile);
+// each takes as much of it as it is estimated to cost, in 64ths of a unit: its tokens and kTileCost. CTA c takes
+// [c Q, (c + 1) Q); a tile that is cut there has its units divided in proportion, and the parts are joined by
+// k_attn_tc_join. So every SM gets the same amount of work whatever the lengths are, at most two cut tiles per CTA go
+// through memory, and the host needs no lengths. Costs have closed sums, so finding a place takes one pass over the
+// requests.
+// ---------------------------------------------------------------------------------------------
+constexpr int kTileCost = 96;   // start and end of a tile, as 1.5 units
+constexpr int kMinPart = 320;   // no CTA gets less than this (5 units): short work takes fewer CTAs
+
+// A tile that begins in this CTA and ends in a later one.
+struct CutTile {
+  int64_t s, e, q;  // its place on the line, and Q
+  int32_t valid, b, h, t;
+  int64_t pad;
+};
+
+template <int T, int BN>
+struct Walk {
+  int64_t p0, p1;  // this CTA's part of the line
+  int64_t s, e;    // the current tile's place
+  int64_t fixed, slope;
+  Request r;
+  int b, h, t, nt, rows;
+
+  __device__ __forceinline__ void load(const AttnArgs& a, int request, uint32_t& err) {
+    b = request;
+    r = find_request(a, b, err);
+    rows = 0;
+    if (r.n_q * (int64_t)a.G > a.max_rows) err |= TQ_DEV_ERR_SPLITS;
+    else rows = r.n_q * a.G;
+    nt = (rows + T - 1) / T;
+    const int base = a.causal ? max(0, r.kv - r.n_q) : r.kv;
+    fixed = (int64_t)base * 64 / BN + kTileCost;
+    slope = a.causal ? max(1, T * 64 / (a.G * BN)) : 0;
+  }
+  __device__ __forceinline__ int64_t before(int tile) const {
+    return tile * fixed + slope * ((int64_t)tile * (tile + 1) / 2);
+  }
+  // The tile in hand: its place, or the first one of a later request.
+  __device__ __forceinline__ void settle(const AttnArgs& a) {
+    uint32_t err = 0;
+    while (t >= nt && b < a.batch) {
+      t = 0;
+      if (nt > 0 && ++h < a.hkv) break;
+      h = 0;
+      if (b + 1 >= a.batch) {
+        b = a.batch;
+        break;
+      }
+      load(a, b + 1, err);
+    }
+    e = s + fixed + slope * (t + 1);
+  }
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    s = e;
+    ++t;
+    settle(a);
+  }
+};
+
+// First unit of the part of a tile [s, e) that begins at place p of the line.
+__device__ __forceinline__ int cut_at(int64_t p, int64_t s, int64_t e, int units) {
+  return p <= s ? 0 : p >= e ? units : (int)((p - s) * units / (e - s));
+}
+
+// What a CTA does of one tile, as its warps read it from a ring in shared memory that one thread fills. n_all < 0: no
+// more.
+struct Part {
+  int f0, rows;      // first row of the tile, rows of the request
+  int kv;            // tokens that any row of the tile sees
+  int u0, n_all;     // first unit, units
+  int n_of[2];       // units of each tile of 128 rows: up to the last token that its last row sees
+  int h, q0, n_q, r_kv, row, base;  // KV head and request
+  int direct, slot;  // all of the tile: results go to out; else which part of the workspace takes them
+};
+constexpr int kParts = 4;
+
+// Workspace: the cut tiles [CTAs], then {m, l} [CTAs][2][T] and the sums [CTAs][2][T][D] of the parts of cut tiles;
+// part 0 of a CTA is of a tile that an earlier CTA began, part 1 of one that it began itself.
+__device__ __forceinline__ CutTile* cut_tiles(const AttnArgs& a) { return reinterpret_cast<CutTile*>(a.part); }
+template <int T>
+__device__ __forceinline__ float2* cut_ml(const AttnArgs& a, int ctas, int cta, int part) {
+  return reinterpret_cast<float2*>(cut_tiles(a) + ctas) + ((size_t)cta * 2 + part) * T;
+}
+template <int T, int D>
+__device__ __forceinline__ float* cut_o(const AttnArgs& a, int ctas, int cta, int part) {
+  return reinterpret_cast<float*>(reinterpret_cast<float2*>(cut_tiles(a) + ctas) + (size_t)ctas * 2 * T) +
+         ((size_t)cta * 2 + part) * T * D;
+}
+
 // Rescale O when a maximum grows by more than this (in powers of two).
 constexpr float kLazy = 8.0f;
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
-              const __grid_constant__ CUtensorMap map_v, int n_tiles) {
+              const __grid_constant__ CUtensorMap map_v) {
   using Sh = TcShape<D>;
-  constexpr int NT = Sh::kNT, BN = Sh::kBN, ST = Sh::kStages;
+  constexpr int NT = Sh::kNT, BN = Sh::kBN, ST = Sh::kStages, T = 128 * NT;
   constexpr uint32_t kTile = Sh::kTile;
   constexpr uint32_t kType = BF16 ? 1u : 0u;
   constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
@@ -108,176 +205,245 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint8_t* skv = smem + NT * Sh::kQ;
   uint64_t* full = reinterpret_cast<uint64_t*>(skv + ST * kTile);
   uint64_t* empty = full + ST;
-  uint64_t* s_full = empty + ST;  // per tile: scores are in TMEM
-  uint64_t* p_full = s_full + NT;  // per tile and half of the unit: weights are in TMEM, O is rescaled
+  uint64_t* q_full = empty + ST;       // per tile: queries are in shared memory
+  uint64_t* s_full = q_full + NT;      // per tile: scores are in TMEM
+  uint64_t* p_full = s_full + NT;      // per tile and half of the unit: weights are in TMEM, O is rescaled
   uint64_t* o_full = p_full + 2 * NT;  // per tile: the product with V is done
-  uint64_t* drained = o_full + NT;
+  uint64_t* s_free = o_full + NT;      // per tile: the softmax has read the scores (kOwnP)
+  uint64_t* v_clean = s_free + NT;     // per ring entry: V rows behind the sequence are zeroed
+  uint64_t* part_full = v_clean + ST;  // ring of parts
+  uint64_t* part_empty = part_full + kParts;
+  uint64_t* drained = part_empty + kParts;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drained + 1);
-  __shared__ int gave_up;
+  __shared__ int64_t warp_sums[Sh::kThreads / 32];
+  __shared__ Part parts[kParts];
+  __shared__ int64_t line[3];  // this CTA's part of the line, and where the tile that holds its start begins
+  __shared__ int first[3];     // that tile: request, head, tile
 
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-  constexpr int kMmaWarp = NT * 4, kTmaWarp = NT * 4 + 1;
+  constexpr int kMmaWarp = NT * 4, kTmaWarp = NT * 4 + 1, kWalkWarp = NT * 4 + 2, kMmaWarp1 = NT * 4 + 3;
   if (threadIdx.x == 0) {
-    gave_up = 0;
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], NT);
+      mbar_init(&v_clean[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
+      mbar_init(&q_full[i], 4);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[2 * i], 4);
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
+      mbar_init(&s_free[i], 4);
     }
-    mbar_init(drained, 1);
+    for (int i = 0; i < kParts; ++i) {
+      mbar_init(&part_full[i], 1);
+      mbar_init(&part_empty[i], NT * 4 + 1 + NT);
+    }
+    mbar_init(drained, NT);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  pdl_wait();
-  if (a.n_splits > 1) pdl_launch();  // the join may be scheduled; it waits for this kernel's end
-  uint32_t err = 0;
-  int x = blockIdx.x;
-  const int split = x % a.n_splits;
-  x /= a.n_splits;
-  const int h = x % a.hkv;
-  // the last tiles first: with causal masks they are the longest, and a short tail ends the launch
-  const int2 where = find_tile(a, n_tiles - 1 - x / a.hkv, 128 * NT);
-  const Request r = find_request(a, where.x, err);
-  if (r.n_q * (int64_t)a.G > a.max_rows) err |= TQ_DEV_ERR_SPLITS;
-  const int rows = err & TQ_DEV_ERR_SPLITS ? 0 : r.n_q * a.G;
-  const int f0 = where.y * (128 * NT);
-  const int kv = tile_kv(a, r, where.y, 128 * NT);
-  const int units = (kv + BN - 1) / BN, per = units_per_split(units, a.n_splits);
-  const int u0 = split * per, u1 = min(units, u0 + per);
-  const bool direct = units <= per;
-  if (threadIdx.x == 0 && err && a.status) atomicOr(a.status, err);
-  if (where.y > (rows - 1) / (128 * NT) || f0 >= rows || (u0 >= u1 && split > 0)) return;
-  // units of each tile: up to the last token that its last row sees
-  int n_of[NT];
-  int n_all = 0;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int kv_t = f0 + t * 128 < rows ? tile_kv(a, r, where.y * NT + t, 128) : 0;
-    n_of[t] = max(0, min(u1, (kv_t + BN - 1) / BN) - u0);
-    n_all = max(n_all, n_of[t]);
-  }
-
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(tmem_base)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
-  // queries into shared memory, as K-major operands; rows past the last are zero
-  for (int i = threadIdx.x; i < NT * 128 * (D / 8); i += Sh::kThreads) {
-    const int row = i / (D / 8), c = i % (D / 8), f = f0 + row;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (f < rows) {
-      const int qi = f / a.G, g = f - qi * a.G;
-      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + (int64_t)(r.q0 + qi) * a.q_row +
-                                          (int64_t)(h * a.G + g) * a.q_head + c * 8);
+  pdl_wait();
+  pdl_launch();  // the join may be scheduled; it waits for this kernel's end
+  uint32_t err = 0;
+
+  // ---- this CTA's part of the line: prefix sums of the requests' costs over the block ----
+  {
+    Walk<T, BN> w;
+    const int per = (a.batch + Sh::kThreads - 1) / Sh::kThreads;
+    const int lo = min(a.batch, (int)threadIdx.x * per), hi = min(a.batch, lo + per);
+    int64_t sum = 0;
+    for (int b = lo; b < hi; ++b) {
+      w.load(a, b, err);
+      sum += a.hkv * w.before(w.nt);
     }
-    const int rr = row & 127;
-    *reinterpret_cast<uint4*>(smem + (row >> 7) * Sh::kQ + (c >> 3) * 16384 + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = v;
+    if (blockIdx.x == 0 && err && a.status) atomicOr(a.status, err);
+    err = 0;
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sums[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    int64_t start = inc - sum, total = 0;
+#pragma unroll
+    for (int i = 0; i < Sh::kThreads / 32; ++i) {
+      if (i < warp) start += warp_sums[i];
+      total += warp_sums[i];
+    }
+    const int64_t q = max((int64_t)kMinPart, (total + gridDim.x - 1) / gridDim.x);
+    const int64_t p0 = q * blockIdx.x, p1 = min(total, p0 + q);
+    if (p0 >= start && p0 < start + sum) {  // one thread's requests hold p0
+      for (int b = lo; b < hi; ++b) {
+        w.load(a, b, err);
+        const int64_t one = w.before(w.nt);
+        if (p0 >= start + a.hkv * one) {
+          start += a.hkv * one;
+          continue;
+        }
+        const int head = (int)((p0 - start) / one);
+        start += head * one;
+        int at = 0, n = w.nt;  // the last tile that begins at p0 or before
+        while (n > 1) {
+          const int half = n / 2;
+          if (start + w.before(at + half) <= p0) {
+            at += half;
+            n -= half;
+          } else {
+            n = half;
+          }
+        }
+        first[0] = b;
+        first[1] = head;
+        first[2] = at;
+        line[2] = start + w.before(at);
+        break;
+      }
+    }
+    if (threadIdx.x == 0) {
+      line[0] = p0;
+      line[1] = p1;
+    }
+    __syncthreads();
   }
-  fence_async_smem();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
   const uint32_t tmem = uniform(*tmem_base);
+  bool ok = true;
+  int at = 0;  // parts taken from the ring
+  // the next part of the ring into registers; false: no more (or a wait gave up)
+  auto take = [&](Part& g) {
+    const int i = at % kParts;
+    ok = ok && warp_wait(&part_full[i], (at / kParts) & 1);
+    if (!ok) return false;
+    g = parts[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&part_empty[i]);
+    ++at;
+    return g.n_all >= 0;
+  };
   // The softmax threads hold a row of scores: they take registers from the other warps (8 x 32 x 216 + 4 x 32 x 72 =
   // 384 x 168, what the block was launched with). One tile's warps have enough as it is.
   constexpr bool kSplitRegs = NT == 2;
   if (warp >= kMmaWarp) {
     if constexpr (kSplitRegs) set_regs_dec<72>();
     if (warp == kTmaWarp) {
-      // ---- K and V tiles: ring entry 2 k holds K of unit u0 + k, entry 2 k + 1 its V ----
-      int2 place = make_int2(0, 0);
-      bool ok = true;
-      int issued = 0;
-      for (int k = 0; k < n_all && ok; ++k) {
-        if ((k & 31) == 0 && k + lane < n_all) {
-          const int tok = (u0 + k + lane) * BN;
-          place = page_place(a, r, tok / kPage, err);
-          place.y += tok % kPage;
-        }
-        const int w = __shfl_sync(0xffffffffu, place.x, k & 31), y = __shfl_sync(0xffffffffu, place.y, k & 31);
-        if (lane == 0) {
-#pragma unroll
-          for (int which = 0; which < 2; ++which) {
-            const int e = 2 * k + which, st = e % ST;
-            if (ok && e >= ST) ok = mbar_wait(&empty[st], ((e / ST) - 1) & 1);
-            if (!ok) break;
-            uint8_t* dst = skv + st * kTile;
-            mbar_expect_tx(&full[st], kTile);
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(dst + c * (BN * 128), which ? &map_v : &map_k, c * 64, y, h, w, &full[st]);
-            issued = e + 1;
+      // ---- K and V tiles: for every unit, ring entry e holds K and entry e + 1 its V ----
+      int e = 0, issued = 0;
+      Part g;
+      while (ok && take(g)) {
+        Request r;
+        r.row = g.row;
+        r.base = g.base;
+        int2 place = make_int2(0, 0);
+        for (int k = 0; k < g.n_all && ok; ++k, e += 2) {
+          if ((k & 31) == 0 && k + lane < g.n_all) {
+            const int tok = (g.u0 + k + lane) * BN;
+            place = page_place(a, r, tok / kPage, err);
+            place.y += tok % kPage;
           }
+          const int pw = __shfl_sync(0xffffffffu, place.x, k & 31), py = __shfl_sync(0xffffffffu, place.y, k & 31);
+          if (lane == 0) {
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+              const int st = (e + which) % ST;
+              if (ok && e + which >= ST) ok = mbar_wait(&empty[st], ((e + which) / ST - 1) & 1);
+              if (!ok) break;
+              uint8_t* dst = skv + st * kTile;
+              mbar_expect_tx(&full[st], kTile);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_4d(dst + c * (BN * 128), which ? &map_v : &map_k, c * 64, py, g.h, pw, &full[st]);
+              issued = e + which + 1;
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
+      // leave only when every copy has landed (they have, unless a wait gave up)
       if (lane == 0) {
-        // leave only when every copy has landed (they have, unless a wait gave up)
-        for (int e = max(0, issued - ST); e < issued; ++e) ok &= mbar_wait(&full[e % ST], (e / ST) & 1);
-        if (!ok) {
-          err |= TQ_DEV_ERR_TIMEOUT;
-          atomicExch(&gave_up, 1);
-        }
+        for (int i = max(0, issued - ST); i < issued; ++i) ok &= mbar_wait(&full[i % ST], (i / ST) & 1);
+        if (!ok) err |= TQ_DEV_ERR_TIMEOUT;
       }
       if (err && a.status) atomicOr(a.status, err);
-    } else if (warp == kMmaWarp) {
-      // ---- products: S_t(0), S_1(0), then per unit and tile O_t += P_t V and the next S_t ----
-      bool ok = true;
+    } else if (warp == kMmaWarp || (NT == 2 && warp == kMmaWarp1)) {
+      // ---- products of tile t ----
+      const int t = warp == kMmaWarp ? 0 : 1;
       const bool leader = elect_one();
-      n_all = uniform(n_all);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) n_of[t] = uniform(n_of[t]);
-      const uint32_t q_lo = umma_desc_sw128_lo(smem_u32(smem)), kv_lo = smem_u32(skv) >> 4;
-      auto scores = [&](int t, int k) {  // S_t = Q_t K(k)^T
+      const uint32_t q_lo = umma_desc_sw128_lo(smem_u32(smem)) + t * (Sh::kQ >> 4), kv_lo = smem_u32(skv) >> 4;
+      const uint32_t sd = tmem + t * 128, pa = tmem + Sh::kP + t * Sh::kPStep, od = tmem + Sh::kO + t * D;
+      int e = 0;       // ring entry of the unit's K
+      int made = 0;    // units whose products are issued
+      int loaded = 0;  // query tiles taken
+      uint32_t cleaned = 0;  // parities of v_clean: an entry is cleaned again only after this warp gave it back
+      // S_t = Q_t K^T of ring entry `entry`, or nothing; the entry is given back either way, once it has been filled
+      auto scores = [&](int entry, bool wanted, uint64_t* after, int parity) {
+        const int st = entry % ST;
+        ok = ok && warp_wait(&full[st], (entry / ST) & 1);
+        if (wanted && after) ok = ok && warp_wait(after, parity & 1);
+        if (!ok) return;
+        tc_fence_after();
         if (leader) {
-          const uint32_t ka = kv_lo + ((2 * k) % ST) * (kTile >> 4) + (1u << 16);
+          if (wanted) {
+            const uint32_t ka = kv_lo + st * (kTile >> 4) + (1u << 16);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t step = (i & 3) * 2;
-            umma_bf16_lo(tmem + Sh::kS + t * 128, q_lo + t * (Sh::kQ >> 4) + (i >> 2) * 1024 + step,
-                         ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
+            for (int i = 0; i < D / 16; ++i) {
+              const uint32_t step = (i & 3) * 2;
+              umma_bf16_lo(sd, q_lo + (i >> 2) * 1024 + step, ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
+            }
+            umma_commit(&s_full[t]);
           }
-          umma_commit(&s_full[t]);
+          umma_commit(&empty[st]);
         }
       };
-      if (n_all > 0) ok = warp_wait(&full[0], 0);
-      if (ok && n_all > 0) {
-        tc_fence_after();
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          if (n_of[t] > 0) scores(t, 0);
-        if (leader) umma_commit(&empty[0]);
-      }
-      for (int k = 0; k < n_all && ok; ++k) {
-        const int ve = 2 * k + 1, vs = ve % ST;
-        ok = warp_wait(&full[vs], (ve / ST) & 1);
-        if (!ok) break;
-        // the unit that the sequence ends in: V rows behind it are zeroed up to the next step of 16 (0 x NaN is NaN),
-        // and the steps behind them are left out
-        const int valid = uniform(min(BN, kv - (u0 + k) * BN)), steps = (valid + 15) / 16;
-        if (valid & 15) {
-          const int n = (16 - (valid & 15)) * (D / 8);
-          for (int i = lane; i < n; i += 32) {
-            const int c = i % (D / 8), row = valid + i / (D / 8);
-            *reinterpret_cast<uint4*>(skv + vs * kTile + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-          fence_async_smem();
-          __syncwarp();
+      Part g;
+      while (ok && take(g)) {
+        const int n_all = uniform(g.n_all), n = uniform(t == 0 ? g.n_of[0] : g.n_of[NT - 1]);
+        const int kv = uniform(g.kv), u0 = uniform(g.u0);
+        if (n_all == 0) continue;
+        if (n > 0) {
+          ok = warp_wait(&q_full[t], loaded & 1);
+          ++loaded;
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          if (k < n_of[t] && ok) {
+        // where S_t goes: the last unit's scores have been read, and with P_t over them, its product is done
+        uint64_t* const s_ready = Sh::kOwnP ? &s_free[t] : &o_full[t];
+        scores(e, n > 0, made > 0 ? s_ready : nullptr, made - 1);
+        for (int k = 0; k < n_all && ok; ++k, e += 2) {
+          if (Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, s_ready, made);
+          const int vs = (e + 1) % ST;
+          ok = ok && warp_wait(&full[vs], ((e + 1) / ST) & 1);
+          if (!ok) break;
+          // the unit that the sequence ends in: V rows behind it are zeroed up to the next step of 16 (0 x NaN is
+          // NaN), and the steps behind them are left out
+          const int valid = min(BN, kv - (u0 + k) * BN), steps = (valid + 15) / 16;
+          if (valid & 15) {
+            if (t == 0) {
+              const int rows16 = (16 - (valid & 15)) * (D / 8);
+              for (int i = lane; i < rows16; i += 32) {
+                const int c = i % (D / 8), row = valid + i / (D / 8);
+                *reinterpret_cast<uint4*>(skv + vs * kTile + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (NT == 2 && lane == 0) mbar_arrive(&v_clean[vs]);
+            } else {
+              ok = warp_wait(&v_clean[vs], (cleaned >> vs) & 1);
+              cleaned ^= 1u << vs;
+            }
+          }
+          if (k < n) {
             // MN-major operand: 64-channel blocks BN x 128 bytes apart, 8-token groups 1024 bytes apart
             const uint32_t va = kv_lo + vs * (kTile >> 4) + ((uint32_t)(BN * 128 >> 4) << 16);
-            const uint32_t od = tmem + Sh::kO + t * D, pa = tmem + Sh::kS + t * 128;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && warp_wait(&p_full[2 * t + half], k & 1);
+              ok = ok && warp_wait(&p_full[2 * t + half], made & 1);
               if (!ok) break;
               tc_fence_after();
               if (leader) {
@@ -288,124 +454,220 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
             }
             if (!ok) break;
             if (leader) umma_commit(&o_full[t]);
+            ++made;
           }
-          if (t == NT - 1 && leader) umma_commit(&empty[vs]);
-          if (k + 1 < n_all && ok) {
-            const int ke = 2 * (k + 1), ks = ke % ST;
-            if (t == 0) ok = warp_wait(&full[ks], (ke / ST) & 1);
-            if (k + 1 < n_of[t] && ok) {
-              ok = warp_wait(&o_full[t], k & 1);  // S_t(k + 1) goes over P_t(k)
-              if (!ok) break;
-              tc_fence_after();
-              scores(t, k + 1);
-            }
-            if (t == NT - 1 && leader) umma_commit(&empty[ks]);
-          }
+          if (leader) umma_commit(&empty[vs]);
+          if (!Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, s_ready, made - 1);
         }
       }
       // leave only when every product is done
       if (leader) umma_commit(drained);
       const bool done = warp_wait(drained, 0);
-      if ((!ok || !done) && leader) {
-        atomicExch(&gave_up, 1);
-        if (a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
+      if ((!ok || !done) && lane == 0 && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
+    } else if (warp == kWalkWarp && lane == 0) {
+      // ---- the parts of this CTA, in order ----
+      Walk<T, BN> w;
+      w.p0 = line[0];
+      w.p1 = line[1];
+      CutTile cut = {};
+      w.b = a.batch;
+      if (w.p0 < w.p1) {
+        w.load(a, first[0], err);
+        w.h = first[1];
+        w.t = first[2];
+        w.s = line[2];
+        w.settle(a);
       }
+      for (bool more = true; more;) {
+        Part g = {};
+        g.n_all = -1;
+        more = w.b < a.batch && w.s < w.p1;
+        if (more) {
+          g.f0 = w.t * T;
+          g.rows = w.rows;
+          g.kv = tile_kv(a, w.r, w.t, T);
+          const int units = (g.kv + BN - 1) / BN;
+          g.u0 = cut_at(w.p0, w.s, w.e, units);
+          const int u1 = cut_at(w.p1, w.s, w.e, units);
+          g.n_all = u1 - g.u0;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const int kv_t = g.f0 + t * 128 < w.rows ? tile_kv(a, w.r, w.t * NT + t, 128) : 0;
+            g.n_of[t] = max(0, min(u1, (kv_t + BN - 1) / BN) - g.u0);
+          }
+          g.h = w.h;
+          g.q0 = w.r.q0;
+          g.n_q = w.r.n_q;
+          g.r_kv = w.r.kv;
+          g.row = w.r.row;
+          g.base = w.r.base;
+          g.direct = g.n_all == units;
+          g.slot = w.s >= w.p0;
+          if (g.slot && w.e > w.p1) {
+            cut.valid = 1;
+            cut.s = w.s;
+            cut.e = w.e;
+            cut.q = w.p1 - w.p0;  // a whole part: the tile goes on behind it
+            cut.b = w.b;
+            cut.h = w.h;
+            cut.t = w.t;
+          }
+          w.next(a);
+          if (g.n_all == 0 && (units > 0 || !g.slot)) continue;  // nothing of it falls to this CTA
+        }
+        const int i = at % kParts;
+        if (at >= kParts) ok = mbar_wait(&part_empty[i], (at / kParts - 1) & 1);
+        if (!ok) break;
+        parts[i] = g;
+        mbar_arrive(&part_full[i]);
+        ++at;
+      }
+      cut_tiles(a)[blockIdx.x] = cut;
+      if (!ok && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
     }
   } else {
     if constexpr (kSplitRegs) set_regs_inc<216>();
     // ---- softmax of tile t: a thread per row ----
-    const int t = warp >> 2;
-    const int n = t == 0 ? n_of[0] : n_of[NT - 1];
+    const int t = warp >> 2, row_t = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
-    const uint32_t ts = tmem + Sh::kS + t * 128 + lanes, to = tmem + Sh::kO + t * D + lanes;
-    const int f = f0 + t * 128 + (threadIdx.x & 127);
-    const bool mine = f < rows;
-    const int qi = mine ? f / a.G : 0;
-    const int lim = mine ? seen(a, r, qi) : 0;
-    // what every row of the tile sees needs no mask; rows past the last may hold anything
-    const int f_first = min(f0 + t * 128, rows - 1);
-    const int lim_all = seen(a, r, f_first / a.G);
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    for (int k = 0; k < n; ++k) {
-      ok = warp_wait(&s_full[t], k & 1);
-      if (!ok) break;
-      tc_fence_after();
-      float s[BN];
+    const uint32_t ts = tmem + t * 128 + lanes, tp = tmem + Sh::kP + t * Sh::kPStep + lanes;
+    const uint32_t to = tmem + Sh::kO + t * D + lanes;
+    int made = 0;
+    Part g = {};
+    // a part's queries into shared memory, as a K-major operand; rows past the last are zero
+    auto load_q = [&] {
+      if ((t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
+      constexpr int kChunks = D / 8, kRowsStep = 128 / kChunks;  // 16-byte chunks of a row; rows of one step
+      const int c = row_t % kChunks;
+      for (int r0 = row_t / kChunks; r0 < 128; r0 += 8 * kRowsStep) {
+        uint4 v[8];  // eight loads in flight
 #pragma unroll
-      for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + c, s + c);
-      tmem_wait_ld();
-      const int base = (u0 + k) * BN;
-      if (base + BN > lim_all) {
-        const int left = lim - base;
+        for (int j = 0; j < 8; ++j) {
+          const int f = g.f0 + t * 128 + r0 + j * kRowsStep;
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (f < g.rows) {
+            const int qi = a.div_g(f), head = g.h * a.G + f - qi * a.G;
+            v[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                        (int64_t)(g.q0 + qi) * a.q_row + (int64_t)head * a.q_head + c * 8));
+          }
+        }
 #pragma unroll
-        for (int c = 0; c < BN; ++c) s[c] = c < left ? s[c] : -INFINITY;
+        for (int j = 0; j < 8; ++j) {
+          const int row = r0 + j * kRowsStep;
+          *reinterpret_cast<uint4*>(smem + t * Sh::kQ + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[j];
+        }
       }
-      float top[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < BN; c += 8) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], c + 4 + i < BN ? fmaxf(s[c + i], s[c + 4 + i]) : s[c + i]);
-      }
-      const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
-      float mn = m;
-      if (mx > m + kLazy || m == -INFINITY) mn = fmaxf(m, mx);
-      const bool grew = mn != m && m != -INFINITY;
-      if (__any_sync(0xffffffffu, grew)) {
-        const float alpha = grew ? exp2_fast(m - mn) : 1.f;
-        l *= alpha;
-        ok = warp_wait(&o_full[t], (k - 1) & 1);  // a maximum that grew has seen a unit, so k > 0
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[t]);
+    };
+    bool have = take(g);
+    if (have) load_q();
+    while (have) {
+      const int n = t == 0 ? g.n_of[0] : g.n_of[NT - 1];
+      const int f = g.f0 + t * 128 + row_t;
+      const bool mine = f < g.rows;
+      const int qi = mine ? f / a.G : 0;
+      Request r;
+      r.n_q = g.n_q;
+      r.kv = g.r_kv;
+      const int lim = mine ? seen(a, r, qi) : 0;
+      // what every row of the tile sees needs no mask; rows past the last may hold anything
+      const int lim_all = seen(a, r, min(g.f0 + t * 128, g.rows - 1) / a.G);
+      const int u0 = g.u0;
+      float m = -INFINITY, l = 0.f;
+      for (int k = 0; k < n; ++k) {
+        ok = warp_wait(&s_full[t], made & 1);
         if (!ok) break;
         tc_fence_after();
+        float s[BN];
+#pragma unroll
+        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + c, s + c);
+        tmem_wait_ld();
+        if constexpr (Sh::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[t]);
+        }
+        const int base = (u0 + k) * BN;
+        if (base + BN > lim_all) {
+          const int left = lim - base;
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = c < left ? s[c] : -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < BN; c += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], c + 4 + i < BN ? fmaxf(s[c + i], s[c + 4 + i]) : s[c + i]);
+        }
+        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+        float mn = m;
+        if (mx > m + kLazy || m == -INFINITY) mn = fmaxf(m, mx);
+        const bool grew = mn != m && m != -INFINITY;
+        const bool rescale = __any_sync(0xffffffffu, grew);
+        if (rescale || (Sh::kOwnP && made > 0)) {  // O_t is whole, and P_t has been used
+          ok = warp_wait(&o_full[t], (made - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (rescale) {
+          const float alpha = grew ? exp2_fast(m - mn) : 1.f;
+          l *= alpha;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(to + c, o);
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + c, o);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-          tmem_st32(to + c, o);
-        }
-      }
-      m = mn;
-      const float mu = m == -INFINITY ? 0.f : m;
-      const float2 sc = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-mu, -mu);
-      float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {  // the product with the first half of V starts while the second is made
-#pragma unroll
-        for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 y = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), sc, off);
-            y.x = exp2_fast(y.x);
-            y.y = exp2_fast(y.y);
-            sum[i & 1] = add2(sum[i & 1], y);
-            p[i] = pack2<BF16>(y.x, y.y);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(to + c, o);
           }
-          tmem_st16(ts + c / 2, p);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+        m = mn;
+        const float mu = m == -INFINITY ? 0.f : m;
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-mu, -mu);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {  // the product with the first half of V starts while the second is made
+#pragma unroll
+          for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
+            uint32_t p[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 y = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), sc, off);
+              y.x = exp2_fast(y.x);
+              y.y = exp2_fast(y.y);
+              sum[i & 1] = add2(sum[i & 1], y);
+              p[i] = pack2<BF16>(y.x, y.y);
+            }
+            tmem_st16(tp + c / 2, p);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+        }
+        const float2 both = add2(sum[0], sum[1]);
+        l += both.x + both.y;
+        ++made;
       }
-      const float2 both = add2(sum[0], sum[1]);
-      l += both.x + both.y;
-    }
-    if (ok && n > 0) ok = warp_wait(&o_full[t], (n - 1) & 1);
-    if (!ok) {
-      if (lane == 0) {
-        atomicExch(&gave_up, 1);
-        if (a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
-      }
-    } else {
-      tc_fence_after();
-      const int head = h * a.G + f - qi * a.G;
+      if (!ok) break;
+      // where this part's result goes; then the next tile's queries, so that its scores are made under the end of
+      // this one
+      const bool direct = g.direct;
       const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-      const size_t slot = mine && !direct ? part_slot(a, r.q0 + qi, head, split) : 0;
-      uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + qi) * a.o_row + (int64_t)head * a.o_head;
-      float* po = part_o(a) + slot * D;
+      uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(g.q0 + qi) * a.o_row +
+                      (int64_t)(g.h * a.G + (mine ? f - qi * a.G : 0)) * a.o_head;
+      float* po = cut_o<T, D>(a, gridDim.x, blockIdx.x, g.slot) + (size_t)(t * 128 + row_t) * D;
+      if (!direct) cut_ml<T>(a, gridDim.x, blockIdx.x, g.slot)[t * 128 + row_t] = make_float2(m, l);
+      have = take(g);
+      if (!ok) break;
+      if (have) load_q();
+      if (n > 0) {
+        ok = warp_wait(&o_full[t], (made - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -416,21 +678,21 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * inv : 0.f;
-        if (mine && direct) {
+        if (!direct) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+        } else if (mine) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
             *reinterpret_cast<uint4*>(dst + c + i) =
                 make_uint4(pack2<BF16>(o[i], o[i + 1]), pack2<BF16>(o[i + 2], o[i + 3]),
                            pack2<BF16>(o[i + 4], o[i + 5]), pack2<BF16>(o[i + 6], o[i + 7]));
-        } else if (mine) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
         }
       }
-      if (mine && !direct) part_ml(a)[slot] = make_float2(m, l);
       tc_fence_before();
     }
+    if (!ok && lane == 0 && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
   }
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -439,19 +701,75 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   }
 }
 
+// k_attn_tc_join: the parts of the tile that CTA blockIdx.x began and did not end, joined with their maxima and sums.
+// A warp per row.
+constexpr int kJoinRows = 16;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(128) k_attn_tc_join(const __grid_constant__ AttnArgs a, int ctas) {
+  constexpr int T = 128 * TcShape<D>::kNT, BN = TcShape<D>::kBN, V = D / 32;
+  pdl_wait();
+  const CutTile c = cut_tiles(a)[blockIdx.x];
+  if (!c.valid) return;
+  uint32_t err = 0;
+  const Request r = find_request(a, c.b, err);
+  const int rows = r.n_q * a.G;
+  const int kv = tile_kv(a, r, c.t, T), units = (kv + BN - 1) / BN;
+  const int i0 = blockIdx.x, i1 = (int)((c.e - 1) / c.q);
+  int live = 0;
+  for (int i = i0; i <= i1; ++i) live += cut_at((i + 1) * c.q, c.s, c.e, units) > cut_at(i * c.q, c.s, c.e, units);
+  if (live < 2) return;  // one CTA had all of it
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int row = blockIdx.y * kJoinRows + warp; row < (int)(blockIdx.y + 1) * kJoinRows; row += 4) {
+    const int f = c.t * T + row;
+    if (f >= rows) break;
+    float top = -INFINITY, sum = 0.f, acc[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    for (int i = i0; i <= i1; ++i) {
+      if (cut_at((i + 1) * c.q, c.s, c.e, units) <= cut_at(i * c.q, c.s, c.e, units)) continue;
+      const float2 ml = cut_ml<T>(a, ctas, i, i == i0)[row];
+      const float* po = cut_o<T, D>(a, ctas, i, i == i0) + (size_t)row * D + lane * V;
+      float v[V];
+      if constexpr (V == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po);
+      else
+#pragma unroll
+        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(v + j) = *reinterpret_cast<const float4*>(po + j);
+      if (ml.x == -INFINITY) continue;  // saw no token
+      const float mn = fmaxf(top, ml.x);
+      const float wa = exp2_fast(top - mn), wb = exp2_fast(ml.x - mn);
+      top = mn;
+      sum = sum * wa + ml.y * wb;
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = acc[j] * wa + v[j] * wb;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const int qi = f / a.G, head = c.h * a.G + f - qi * a.G;
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + qi) * a.o_row + (int64_t)head * a.o_head + lane * V;
+    uint32_t out[V / 2];
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) out[j] = pack2<BF16>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+    if constexpr (V == 2) *reinterpret_cast<uint32_t*>(dst) = out[0];
+    else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+  }
+}
+
 template <int D, bool BF16>
 cudaError_t launch_tc_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, cudaStream_t s) {
   using Sh = TcShape<D>;
   cudaError_t e = cudaFuncSetAttribute(k_attn_tc<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (e == cudaSuccess)
+    e = launch_pdl(k_attn_tc<D, BF16>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_attn_tc<D, BF16>, dim3((unsigned)p.tiles * a.hkv * a.n_splits), dim3(Sh::kThreads), Sh::kSmem, s,
-                    a, m.k, m.v, (int)p.tiles);
+  return launch_pdl(k_attn_tc_join<D, BF16>, dim3(p.ctas, Sh::kNT * 128 / kJoinRows), dim3(128), 0, s, a, p.ctas);
 }
 
 }  // namespace
 
-int attn_tc_tile_rows(int d) { return d == 256 ? TcShape<256>::kNT * 128 : TcShape<128>::kNT * 128; }
-int attn_tc_unit(int d) { return d == 256 ? TcShape<256>::kBN : TcShape<128>::kBN; }
+size_t attn_tc_bytes(int d, int ctas) {
+  const size_t rows = (size_t)ctas * 2 * 128 * (d == 256 ? TcShape<256>::kNT : TcShape<128>::kNT);
+  return ctas * sizeof(CutTile) + rows * (sizeof(float2) + d * sizeof(float));
+}
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {
   if (dtype == TQ_BF16)
@@ -462,5 +780,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan&
          : d == 128 ? launch_tc_as<128, false>(a, m, p, s)
                     : launch_tc_as<256, false>(a, m, p, s);
 }
+
+int attn_tc_unit(int d) { return d == 256 ? TcShape<256>::kBN : TcShape<128>::kBN; }
 
 }  // namespace tq
