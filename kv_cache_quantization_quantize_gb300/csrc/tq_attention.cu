@@ -465,12 +465,12 @@ AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * G;
   p.max_rows = rows;
   p.tc = rows > (d == 256 ? 16 : 32);
-  p.ctas = sms;
+  p.ctas = std::min(sms, 1024);  // one per SM
   p.tiles = 1;
   p.tile_rows = p.n_splits = 1;
   if (p.tc) {
     p.unit = attn_tc_unit(d);
-    p.bytes = attn_tc_bytes(d, sms);
+    p.bytes = attn_tc_bytes(d, p.ctas);
     return p;
   }
   p.tile_rows = rows <= 16 ? 16 : 32;

@@ -77,6 +77,11 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 // Shared-memory writes of this thread become visible to the async proxy (TMA, MMA operands).
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 // x * y + z and x + y on pairs of floats.
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 r;
@@ -108,8 +113,8 @@ constexpr int kMinPart = 320;   // no CTA gets less than this (5 units): short w
 // A tile that begins in this CTA and ends in a later one.
 struct CutTile {
   int64_t s, e, q;  // its place on the line, and Q
-  int32_t valid, b, h, t;
-  int64_t pad;
+  int32_t units;    // 0: there is no such tile
+  int32_t f0, rows, h, q0, pad;
 };
 
 template <int T, int BN>
@@ -122,7 +127,10 @@ struct Walk {
 
   __device__ __forceinline__ void load(const AttnArgs& a, int request, uint32_t& err) {
     b = request;
-    r = find_request(a, b, err);
+    take(a, find_request(a, b, err), err);
+  }
+  __device__ __forceinline__ void take(const AttnArgs& a, const Request& request, uint32_t& err) {
+    r = request;
     rows = 0;
     if (r.n_q * (int64_t)a.G > a.max_rows) err |= TQ_DEV_ERR_SPLITS;
     else rows = r.n_q * a.G;
@@ -218,7 +226,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   __shared__ int64_t warp_sums[Sh::kThreads / 32];
   __shared__ Part parts[kParts];
   __shared__ int64_t line[3];  // this CTA's part of the line, and where the tile that holds its start begins
-  __shared__ int first[3];     // that tile: request, head, tile
+  __shared__ int first[6];     // that tile: request, head, tile; the request's first row, queries, tokens
+  __shared__ int first_kv[2];  // and where its K and V are
 
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   constexpr int kMmaWarp = NT * 4, kTmaWarp = NT * 4 + 1, kWalkWarp = NT * 4 + 2, kMmaWarp1 = NT * 4 + 3;
@@ -304,6 +313,11 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         first[0] = b;
         first[1] = head;
         first[2] = at;
+        first[3] = w.r.q0;
+        first[4] = w.r.n_q;
+        first[5] = w.r.kv;
+        first_kv[0] = w.r.row;
+        first_kv[1] = w.r.base;
         line[2] = start + w.before(at);
         break;
       }
@@ -472,7 +486,14 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       CutTile cut = {};
       w.b = a.batch;
       if (w.p0 < w.p1) {
-        w.load(a, first[0], err);
+        Request r;
+        r.q0 = first[3];
+        r.n_q = first[4];
+        r.kv = first[5];
+        r.row = first_kv[0];
+        r.base = first_kv[1];
+        w.b = first[0];
+        w.take(a, r, err);
         w.h = first[1];
         w.t = first[2];
         w.s = line[2];
@@ -504,13 +525,14 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           g.direct = g.n_all == units;
           g.slot = w.s >= w.p0;
           if (g.slot && w.e > w.p1) {
-            cut.valid = 1;
+            cut.units = units;
+            cut.f0 = g.f0;
+            cut.rows = w.rows;
+            cut.q0 = w.r.q0;
+            cut.h = w.h;
             cut.s = w.s;
             cut.e = w.e;
             cut.q = w.p1 - w.p0;  // a whole part: the tile goes on behind it
-            cut.b = w.b;
-            cut.h = w.h;
-            cut.t = w.t;
           }
           w.next(a);
           if (g.n_all == 0 && (units > 0 || !g.slot)) continue;  // nothing of it falls to this CTA
@@ -537,12 +559,13 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     // a part's queries into shared memory, as a K-major operand; rows past the last are zero
     auto load_q = [&] {
       if ((t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
+      constexpr int kBatch = D == 64 ? 8 : 16;
       constexpr int kChunks = D / 8, kRowsStep = 128 / kChunks;  // 16-byte chunks of a row; rows of one step
       const int c = row_t % kChunks;
-      for (int r0 = row_t / kChunks; r0 < 128; r0 += 8 * kRowsStep) {
-        uint4 v[8];  // eight loads in flight
+      for (int r0 = row_t / kChunks; r0 < 128; r0 += kBatch * kRowsStep) {
+        uint4 v[kBatch];  // loads in flight
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
           const int f = g.f0 + t * 128 + r0 + j * kRowsStep;
           v[j] = make_uint4(0, 0, 0, 0);
           if (f < g.rows) {
@@ -552,7 +575,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < kBatch; ++j) {
           const int row = r0 + j * kRowsStep;
           *reinterpret_cast<uint4*>(smem + t * Sh::kQ + (c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[j];
         }
@@ -567,7 +590,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const int n = t == 0 ? g.n_of[0] : g.n_of[NT - 1];
       const int f = g.f0 + t * 128 + row_t;
       const bool mine = f < g.rows;
-      const int qi = mine ? f / a.G : 0;
+      const int qi = mine ? a.div_g(f) : 0;
       Request r;
       r.n_q = g.n_q;
       r.kv = g.r_kv;
@@ -597,11 +620,13 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int c = 4; c < BN; c += 8) {
+        for (int c = 4; c < BN - 4; c += 8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], c + 4 + i < BN ? fmaxf(s[c + i], s[c + 4 + i]) : s[c + i]);
+          for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[c + i], s[c + 4 + i]);
         }
-        const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[BN - 4 + i]);
+        const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
         float mn = m;
         if (mx > m + kLazy || m == -INFINITY) mn = fmaxf(m, mx);
         const bool grew = mn != m && m != -INFINITY;
@@ -702,52 +727,77 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
 }
 
 // k_attn_tc_join: the parts of the tile that CTA blockIdx.x began and did not end, joined with their maxima and sums.
-// A warp per row.
+// Each warp takes kJoinRows / 4 rows at once, so that their loads overlap; latency bounds the kernel.
 constexpr int kJoinRows = 16;
+constexpr int kJoinMost = 1024;  // CTAs of a launch at most
 template <int D, bool BF16>
 __global__ void __launch_bounds__(128) k_attn_tc_join(const __grid_constant__ AttnArgs a, int ctas) {
-  constexpr int T = 128 * TcShape<D>::kNT, BN = TcShape<D>::kBN, V = D / 32;
+  constexpr int T = 128 * TcShape<D>::kNT, V = D / 32, R = kJoinRows / 4;
+  __shared__ int16_t part[kJoinMost];
+  __shared__ int parts;
   pdl_wait();
   const CutTile c = cut_tiles(a)[blockIdx.x];
-  if (!c.valid) return;
-  uint32_t err = 0;
-  const Request r = find_request(a, c.b, err);
-  const int rows = r.n_q * a.G;
-  const int kv = tile_kv(a, r, c.t, T), units = (kv + BN - 1) / BN;
-  const int i0 = blockIdx.x, i1 = (int)((c.e - 1) / c.q);
-  int live = 0;
-  for (int i = i0; i <= i1; ++i) live += cut_at((i + 1) * c.q, c.s, c.e, units) > cut_at(i * c.q, c.s, c.e, units);
-  if (live < 2) return;  // one CTA had all of it
+  const int row0 = blockIdx.y * kJoinRows;
+  if (!c.units || c.f0 + row0 >= c.rows) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int row = blockIdx.y * kJoinRows + warp; row < (int)(blockIdx.y + 1) * kJoinRows; row += 4) {
-    const int f = c.t * T + row;
-    if (f >= rows) break;
-    float top = -INFINITY, sum = 0.f, acc[V];
+  const int i0 = blockIdx.x, i1 = (int)((c.e - 1) / c.q);
+  if (warp == 0) {  // the CTAs that had units of it
+    int n = 0;
+    for (int base = i0; base <= i1; base += 32) {
+      const int i = base + lane;
+      const bool live = i <= i1 && cut_at((i + 1) * c.q, c.s, c.e, c.units) > cut_at(i * c.q, c.s, c.e, c.units);
+      const uint32_t m = __ballot_sync(0xffffffffu, live);
+      if (live) part[n + __popc(m & ((1u << lane) - 1))] = (int16_t)i;
+      n += __popc(m);
+    }
+    if (lane == 0) parts = n;
+  }
+  __syncthreads();
+  if (parts < 2) return;  // one CTA had all of it
+  float top[R], sum[R], acc[R][V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    for (int i = i0; i <= i1; ++i) {
-      if (cut_at((i + 1) * c.q, c.s, c.e, units) <= cut_at(i * c.q, c.s, c.e, units)) continue;
-      const float2 ml = cut_ml<T>(a, ctas, i, i == i0)[row];
-      const float* po = cut_o<T, D>(a, ctas, i, i == i0) + (size_t)row * D + lane * V;
-      float v[V];
-      if constexpr (V == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(po);
+  for (int j = 0; j < R; ++j) {
+    top[j] = -INFINITY;
+    sum[j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
+  }
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+    const int i = part[k];
+    const float2* pml = cut_ml<T>(a, ctas, i, i == i0) + row0 + warp;
+    const float* po = cut_o<T, D>(a, ctas, i, i == i0) + (size_t)(row0 + warp) * D + lane * V;
+    float2 ml[R];
+    float v[R][V];
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      ml[j] = pml[4 * j];
+      if constexpr (V == 2) *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(po + 4 * j * D);
       else
 #pragma unroll
-        for (int j = 0; j < V; j += 4) *reinterpret_cast<float4*>(v + j) = *reinterpret_cast<const float4*>(po + j);
-      if (ml.x == -INFINITY) continue;  // saw no token
-      const float mn = fmaxf(top, ml.x);
-      const float wa = exp2_fast(top - mn), wb = exp2_fast(ml.x - mn);
-      top = mn;
-      sum = sum * wa + ml.y * wb;
-#pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = acc[j] * wa + v[j] * wb;
+        for (int q = 0; q < V; q += 4)
+          *reinterpret_cast<float4*>(v[j] + q) = *reinterpret_cast<const float4*>(po + 4 * j * D + q);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const int qi = f / a.G, head = c.h * a.G + f - qi * a.G;
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(r.q0 + qi) * a.o_row + (int64_t)head * a.o_head + lane * V;
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      const float mn = fmaxf(top[j], ml[j].x), mu = mn == -INFINITY ? 0.f : mn;
+      const float wa = exp2_fast(top[j] - mu), wb = exp2_fast(ml[j].x - mu);  // 0 for a part that saw no token
+      top[j] = mn;
+      sum[j] = sum[j] * wa + ml[j].y * wb;
+#pragma unroll
+      for (int i2 = 0; i2 < V; ++i2) acc[j][i2] = acc[j][i2] * wa + v[j][i2] * wb;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const int f = c.f0 + row0 + warp + 4 * j;
+    if (f >= c.rows) continue;
+    const float inv = sum[j] > 0.f ? 1.f / sum[j] : 0.f;
+    const int qi = a.div_g(f), head = c.h * a.G + f - qi * a.G;
+    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(c.q0 + qi) * a.o_row + (int64_t)head * a.o_head + lane * V;
     uint32_t out[V / 2];
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) out[j] = pack2<BF16>(acc[2 * j] * inv, acc[2 * j + 1] * inv);
+    for (int i = 0; i < V / 2; ++i) out[i] = pack2<BF16>(acc[j][2 * i] * inv, acc[j][2 * i + 1] * inv);
     if constexpr (V == 2) *reinterpret_cast<uint32_t*>(dst) = out[0];
     else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
