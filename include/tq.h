@@ -509,7 +509,7 @@ typedef struct tq_queries {
   int32_t n_q_heads;
   int32_t batch;       /* <= 65535 */
   int32_t max_q;       /* no request has more rows (0: n_rows); one that has gets no output, TQ_DEV_ERR_SPLITS */
-  int32_t max_kv;      /* about the longest request's tokens to attend to (0: as many as fit); sizes the splits */
+  int32_t max_kv;      /* no request has more tokens to attend to (0: unknown); bounds the CTAs of short calls */
   float softmax_scale; /* <= 0: 1 / sqrt(head_dim) */
 } tq_queries;
 
@@ -522,11 +522,12 @@ typedef struct tq_queries {
  * A page without a block in the table reads as zeros (TQ_DEV_ERR_BLOCK); a bad id, length or start makes the
  * request's outputs zeros or unwritten (TQ_DEV_ERR_SEQ_ID, TQ_DEV_ERR_LENGTH).
  *   - K and V: base and strides a multiple of 16 bytes, positive (also where a size is 1, if read).
- *   - workspace: tq_attention_workspace_bytes(q, kv, max_pages) bytes (max_pages 0 for cross attention), 256-byte
- *     aligned, contents arbitrary. Calls that may
+ *   - workspace: tq_attention_workspace_bytes(q, kv) bytes, 256-byte aligned, contents arbitrary. Calls that may
  *     overlap on the GPU need workspaces of their own.
- *   - Launches: one attention kernel, and one that joins the splits where the sequences are split. */
-size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv, int max_pages);
+ *   - Launches: one attention kernel whose CTAs get equal parts of all requests' work, and one that joins the
+ *     results of tiles that were cut between CTAs. max_q chooses the attention kernel: up to 32 rows (queries of a
+ *     request x query heads per KV head) one for few rows, else one on the tensor cores. */
+size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv);
 tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_table, int max_seqs,
                              int max_pages, int64_t table_stride, const int32_t* d_seq_ids, const int32_t* d_kv_lens,
                              int causal, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,

@@ -74,7 +74,7 @@ _SIGS = {
     "tq_blocks_map": (c_int, [c_void_p, c_int, c_int, ctypes.c_int64, c_void_p, c_int] + [c_void_p] * 4 + [c_int] + [c_void_p] * 3
                       + [c_int, c_void_p, c_void_p]),
     "tq_paged_append": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p]),
-    "tq_attention_workspace_bytes": (c_size_t, [c_void_p, c_void_p, c_int]),
+    "tq_attention_workspace_bytes": (c_size_t, [c_void_p, c_void_p]),
     "tq_paged_attention": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, ctypes.c_int64, c_void_p, c_void_p, c_int, c_void_p,
                                    c_size_t, c_void_p, c_void_p]),
     "tq_cross_attention": (c_int, [c_void_p] * 5 + [c_size_t, c_void_p, c_void_p]),

@@ -7,7 +7,7 @@
 
 namespace tq {
 
-constexpr int kMaxAttnSplits = 128;
+constexpr int kMaxAttnCtas = 1024;  // of a launch
 
 enum KvMode { kKvPaged = 0, kKvPadded = 1, kKvPacked = 2 };
 
@@ -34,14 +34,15 @@ struct AttnArgs {
   const int32_t* table;      // paged
   int64_t table_stride;
   uint32_t* status;
-  float* part;               // partials of the splits (see part_slot)
+  void* part;                // workspace (tq_attention_line.cuh)
   float scale_log2;          // softmax scale * log2(e)
   int n_rows, batch, hq, hkv, G;
   FastDiv div_g;             // by G
-  int max_seqs, max_pages, outer, tokens;
+  int max_seqs, outer, tokens;   // max_seqs: padded: the outer size
+  int most_kv;               // paged, padded: tokens of a request at most
+  int slope;                 // cost that each tile of a causal request has over the one before (tq_attention_line.cuh)
   int mode, causal;
-  int n_splits, max_rows;    // max_rows: rows (query, head of the group) of a request and KV head at most
-  int tiles;                 // rows kernel: tiles of every request
+  int max_rows;              // rows (query, head of the group) of a request and KV head at most
 };
 
 // One request as its CTA sees it. Bad arrays give an empty request and status bits.
@@ -51,41 +52,30 @@ struct Request {
 };
 
 __device__ __forceinline__ Request find_request(const AttnArgs& a, int b, uint32_t& err) {
+  // the loads first, so that they overlap
+  const bool packed = a.mode == kKvPacked;
+  const int32_t* lens = packed ? a.kv_starts : a.kv_lens;
+  const int q0 = a.q_starts[b], q1 = a.q_starts[b + 1], x = lens[b];
+  const int y = packed ? a.kv_starts[b + 1] : a.seq_ids ? a.seq_ids[b] : b;
+  const bool bad_q = q0 < 0 || q1 < q0 || q1 > a.n_rows;
   Request r;
-  r.q0 = a.q_starts[b];
-  const int q1 = a.q_starts[b + 1];
-  r.n_q = q1 - r.q0;
-  if (r.q0 < 0 || q1 < r.q0 || q1 > a.n_rows) {
-    err |= TQ_DEV_ERR_LENGTH;
-    r.q0 = r.n_q = 0;
-  }
-  r.row = b;
-  r.base = 0;
-  if (a.mode == kKvPacked) {
-    r.base = a.kv_starts[b];
-    const int k1 = a.kv_starts[b + 1];
-    r.kv = k1 - r.base;
+  r.q0 = bad_q ? 0 : q0;
+  r.n_q = bad_q ? 0 : q1 - q0;
+  bool bad_kv, bad_id = false;
+  if (packed) {
+    bad_kv = x < 0 || y < x || y > a.tokens;
+    r.kv = y - x;
+    r.base = x;
     r.row = 0;
-    if (r.base < 0 || k1 < r.base || k1 > a.tokens) {
-      err |= TQ_DEV_ERR_LENGTH;
-      r.kv = 0;
-    }
   } else {
-    r.kv = a.kv_lens[b];
-    const int64_t most = a.mode == kKvPaged ? (int64_t)a.max_pages * kPage : a.tokens;
-    if (r.kv < 0 || r.kv > most) {
-      err |= TQ_DEV_ERR_LENGTH;
-      r.kv = 0;
-    }
-    if (a.mode == kKvPaged) {
-      if (a.seq_ids) r.row = a.seq_ids[b];
-      if (r.row < 0 || r.row >= a.max_seqs) {
-        err |= TQ_DEV_ERR_SEQ_ID;
-        r.row = 0;
-        r.kv = 0;
-      }
-    }
+    bad_kv = x < 0 || x > a.most_kv;
+    bad_id = y < 0 || y >= a.max_seqs;
+    r.kv = x;
+    r.base = 0;
+    r.row = bad_id ? 0 : y;
   }
+  if (bad_kv || bad_id) r.kv = 0;
+  err |= (bad_q || bad_kv ? TQ_DEV_ERR_LENGTH : 0u) | (bad_id ? TQ_DEV_ERR_SEQ_ID : 0u);
   return r;
 }
 
@@ -112,21 +102,7 @@ __device__ __forceinline__ int2 page_place(const AttnArgs& a, const Request& r, 
 // Tokens that any row of a tile sees.
 __device__ __forceinline__ int tile_kv(const AttnArgs& a, const Request& r, int tile, int tile_rows) {
   const int last = min((tile + 1) * tile_rows, r.n_q * a.G) - 1;
-  return last < 0 ? 0 : seen(a, r, last / a.G);
-}
-
-// Splits of a range of `units`: split s takes units [s * per, min(units, (s + 1) * per)).
-__device__ __forceinline__ int units_per_split(int units, int n_splits) { return (units + n_splits - 1) / n_splits; }
-
-// Partial of (row of q, query head) and split s: {m, l} and D floats of the weighted sum; weights are
-// exp2(score * scale_log2 - m) and l their sum. All {m, l} come first.
-__device__ __forceinline__ size_t part_slot(const AttnArgs& a, int row, int head, int s) {
-  return ((size_t)row * a.hq + head) * a.n_splits + s;
-}
-__device__ __forceinline__ float2* part_ml(const AttnArgs& a) { return reinterpret_cast<float2*>(a.part); }
-__device__ __forceinline__ float* part_o(const AttnArgs& a) {
-  // n_rows * hq * n_splits pairs, rounded up to 16 bytes
-  return a.part + (((size_t)a.n_rows * a.hq * a.n_splits * 2 + 3) & ~(size_t)3);
+  return last < 0 ? 0 : seen(a, r, a.div_g(last));
 }
 
 // 2^x as the special function unit gives it (relative error about 2^-22, 0 for -inf).
@@ -161,22 +137,21 @@ struct AttnMaps {
 // Tensor map of K or V for boxes of 64 channels x box_tokens tokens of one head, 128-byte swizzle: dimensions
 // {head_dim, tokens, heads, outer}.
 cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m);
-// One launch plan: which kernel, its tiles and splits, and the bytes of partials it needs.
-struct AttnPlan {
-  int unit;          // tokens of a unit: splits take whole units
-  int tile_rows;     // rows kernel: rows (query, head of the group) of a tile
-  int n_splits;      // rows kernel
-  int64_t max_rows;  // rows (query, head of the group) of a request and KV head at most
-  int64_t tiles;     // rows kernel: tiles of one KV head over all requests
-  bool tc;           // tensor-core kernel
-  int ctas;          // its CTAs
-  size_t bytes;
+// A kernel's tiles and launch: rows (query, head of the group) of a tile, tokens of a unit, CTAs at most, bytes of
+// workspace per CTA; a tile's fixed cost and the least work of a CTA (tq_attention_line.cuh).
+struct AttnShape {
+  int tile_rows, unit, ctas;
+  size_t cta_bytes;
+  int cost, least;
 };
-// Tensor-core kernel (tq_attention_tc.cu): its workspace, its unit of tokens, and the launch.
-size_t attn_tc_bytes(int d, int ctas);
-int attn_tc_unit(int d);
+struct AttnPlan : AttnShape {
+  bool tc;           // tensor-core kernel (tq_attention_tc.cu), else the rows kernel (tq_attention_rows.cu)
+  int64_t max_rows;  // rows of a request and KV head at most
+  size_t bytes;      // of workspace
+};
+AttnShape attn_rows_shape(int d, int64_t rows, int sms);
+AttnShape attn_tc_shape(int d, int sms);
+cudaError_t launch_attn_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
-AttnPlan attn_plan(const tq_queries& q, const tq_kv& kv, int64_t max_tokens, int sms);
-cudaError_t launch_attention(const AttnArgs& a, const tq_kv& kv, const AttnPlan& p, cudaStream_t s);
 
 }  // namespace tq

@@ -5,7 +5,38 @@
 #include <cstdarg>
 #include <cstdio>
 
+#include <cudaTypedefs.h>
+
 #include "tq_attention.cuh"
+
+namespace tq {
+
+cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+    return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
+                                                                : nullptr;
+  }();
+  if (!encode) return cudaErrorNotSupported;
+  const int64_t* st = values ? kv.v_strides : kv.k_strides;
+  void* base = values ? kv.v : kv.k;
+  const cuuint64_t d = (cuuint64_t)kv.head_dim;
+  // an empty dimension is given as one (no request has tokens there), a stride that is never taken as any valid one
+  const cuuint64_t tokens = (cuuint64_t)std::max(kv.tokens, 1), outer = (cuuint64_t)std::max(kv.outer, 1);
+  const cuuint64_t dims[4] = {d, tokens, (cuuint64_t)kv.n_kv_heads, outer};
+  auto bytes = [&](cuuint64_t n, int64_t stride) { return n > 1 ? (cuuint64_t)stride * 2 : d * 2; };
+  const cuuint64_t strides[3] = {bytes(tokens, st[1]), bytes(dims[2], st[2]), bytes(outer, st[0])};
+  const cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(m, kv.dtype == TQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                            base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace tq
 
 namespace {
 
@@ -91,19 +122,32 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
   return TQ_OK;
 }
 
-int64_t most_tokens(const tq_kv* kv, int max_pages) {
-  return max_pages > 0 ? (int64_t)max_pages * tq::kPage : kv->tokens;
+// Requests of few rows take the rows kernel, others the tensor cores.
+tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
+  tq::AttnPlan p;
+  const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * (q.n_q_heads / kv.n_kv_heads);
+  const bool tc = rows > 32;
+  static_cast<tq::AttnShape&>(p) = tc ? tq::attn_tc_shape(kv.head_dim, sms) : tq::attn_rows_shape(kv.head_dim, rows, sms);
+  p.tc = tc;
+  p.max_rows = rows;
+  p.ctas = std::min(p.ctas, tq::kMaxAttnCtas);
+  if (q.max_kv > 0) {  // no more CTAs than the most work there can be feeds
+    const double tiles = (double)q.batch * kv.n_kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows);
+    const double most = tiles * ((double)q.max_kv * 64 / p.unit + 64 + p.cost);
+    if (most < (double)p.ctas * p.least) p.ctas = std::max(1, (int)std::ceil(most / p.least));
+  }
+  p.bytes = p.ctas * p.cta_bytes;
+  return p;
 }
 
-tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, int max_pages, void* ws, size_t ws_bytes,
+tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void* ws, size_t ws_bytes,
                  uint32_t* status, tq_stream_t stream) {
   if (!q->batch || !q->n_rows) return tq::set_error(TQ_OK, "");
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return done(e, "device");
-  const tq::AttnPlan p = tq::attn_plan(*q, *kv_in, most_tokens(kv_in, max_pages), sms);
-  if (p.tiles * kv_in->n_kv_heads >= ((int64_t)1 << 31) / std::max(p.n_splits, p.n_splits > 1 ? p.tile_rows : 1)) return fail(TQ_ERR_UNSUPPORTED, "batch x heads x rows: too many tiles for one launch");
-  if (p.bytes && (!ws || ws_bytes < p.bytes || !aligned(ws, 256)))
+  const tq::AttnPlan p = plan_of(*q, *kv_in, sms);
+  if (!ws || ws_bytes < p.bytes || !aligned(ws, 256))
     return fail(TQ_ERR_INVALID_ARG, "workspace: %zu bytes, 256-byte aligned, are needed (got %zu)", p.bytes, ws_bytes);
   tq_kv kv = *kv_in;
   if (!kv.outer || !kv.tokens) {  // nothing to read: the tensor maps need an address all the same
@@ -118,7 +162,7 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, int m
   a.o_head = q->out_strides[1];
   a.q_starts = q->d_q_starts;
   a.status = status;
-  a.part = static_cast<float*>(ws);
+  a.part = ws;
   const double scale = q->softmax_scale > 0.f ? (double)q->softmax_scale : 1.0 / std::sqrt((double)kv.head_dim);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
   a.n_rows = q->n_rows;
@@ -129,10 +173,15 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, int m
   a.div_g.set((uint32_t)a.G);
   a.outer = kv.outer;
   a.tokens = kv.tokens;
-  a.n_splits = p.n_splits;
   a.max_rows = (int)p.max_rows;
-  a.tiles = (int)std::max<int64_t>(1, p.tiles / q->batch);
-  return done(tq::launch_attention(a, kv, p, (cudaStream_t)stream), "attention launch");
+  a.slope = a.causal ? std::max(1, p.tile_rows * 64 / (a.G * p.unit)) : 0;
+  tq::AttnMaps m;
+  e = tq::attn_tensor_map(kv, false, p.unit, &m.k);
+  if (e == cudaSuccess) e = tq::attn_tensor_map(kv, true, p.unit, &m.v);
+  if (e == cudaSuccess)
+    e = p.tc ? tq::launch_attn_tc(a, m, p, kv.head_dim, kv.dtype, (cudaStream_t)stream)
+             : tq::launch_attn_rows(a, m, p, kv.head_dim, kv.dtype, (cudaStream_t)stream);
+  return done(e, "attention launch");
 }
 
 }  // namespace
@@ -214,12 +263,12 @@ tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dt
               "tq_paged_append");
 }
 
-size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv, int max_pages) {
+size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv) {
   int sms = 0;
-  if (check_kv(kv, false) != TQ_OK || !q || q->batch < 1 || q->n_rows < 1 || q->max_q < 0 || q->max_kv < 0 ||
-      q->n_q_heads < 1 || q->n_q_heads % kv->n_kv_heads || max_pages < 0 || sm_count(&sms) != cudaSuccess)
+  if (check_kv(kv, false) != TQ_OK || !q || q->batch < 1 || q->n_rows < 1 || q->max_q < 0 || q->n_q_heads < 1 ||
+      q->n_q_heads % kv->n_kv_heads || sm_count(&sms) != cudaSuccess)
     return 0;
-  return tq::attn_plan(*q, *kv, most_tokens(kv, max_pages), sms).bytes;
+  return plan_of(*q, *kv, sms).bytes;
 }
 
 tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_table, int max_seqs,
@@ -246,8 +295,8 @@ tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t
   a.table = d_table;
   a.table_stride = table_stride;
   a.max_seqs = max_seqs;
-  a.max_pages = max_pages;
-  return attend(q, kv, a, max_pages, d_workspace, workspace_bytes, d_status, stream);
+  a.most_kv = max_pages * tq::kPage;
+  return attend(q, kv, a, d_workspace, workspace_bytes, d_status, stream);
 }
 
 tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_kv_starts,
@@ -265,7 +314,9 @@ tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t
   a.mode = d_kv_starts ? tq::kKvPacked : tq::kKvPadded;
   a.kv_lens = d_kv_lens;
   a.kv_starts = d_kv_starts;
-  return attend(q, kv, a, 0, d_workspace, workspace_bytes, d_status, stream);
+  a.max_seqs = kv->outer;
+  a.most_kv = kv->tokens;
+  return attend(q, kv, a, d_workspace, workspace_bytes, d_status, stream);
 }
 
 }  // extern "C"

@@ -1,7 +1,5 @@
 // Attention of chunks of new tokens over an exact cache or an encoder's states, on the tensor cores (tcgen05).
-#include <algorithm>
-
-#include "tq_attention.cuh"
+#include "tq_attention_line.cuh"
 #include "tq_tcgen05.cuh"
 
 namespace tq {
@@ -39,11 +37,6 @@ struct TcShape {
   // the special function units are the bound and turns only add waits (1670 against 2290 cycles per unit).
   static constexpr bool kTurns = D == 128;
 };
-
-// A warp's wait on an mbarrier: every lane waits, all go on together, and all give up if one does.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
-}
 
 // Registers per thread from here on (executed by every warp of a warpgroup).
 template <int N>
@@ -103,103 +96,8 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-// ---------------------------------------------------------------------------------------------
-// The split of the work. All tiles of all requests and KV heads lie on one line, in the order (request, head, tile);
-// each takes as much of it as it is estimated to cost, in 64ths of a unit: its tokens and kTileCost. CTA c takes
-// [c Q, (c + 1) Q); a tile that is cut there has its units divided in proportion, and the parts are joined by
-// k_attn_tc_join. So every SM gets the same amount of work whatever the lengths are, at most two cut tiles per CTA go
-// through memory, and the host needs no lengths. Costs have closed sums, so finding a place takes one pass over the
-// requests.
-// ---------------------------------------------------------------------------------------------
-constexpr int kTileCost = 96;   // start and end of a tile, as 1.5 units
-constexpr int kMinPart = 320;   // no CTA gets less than this (5 units): short work takes fewer CTAs
-
-// A tile that begins in this CTA and ends in a later one.
-struct CutTile {
-  int64_t s, e, q;  // its place on the line, and Q
-  int32_t units;    // 0: there is no such tile
-  int32_t f0, rows, h, q0, pad;
-};
-
-template <int T, int BN>
-struct Walk {
-  int64_t p0, p1;  // this CTA's part of the line
-  int64_t s, e;    // the current tile's place
-  int64_t fixed, slope;
-  Request r;
-  int b, h, t, nt, rows;
-
-  __device__ __forceinline__ void load(const AttnArgs& a, int request, uint32_t& err) {
-    b = request;
-    take(a, find_request(a, b, err), err);
-  }
-  __device__ __forceinline__ void take(const AttnArgs& a, const Request& request, uint32_t& err) {
-    r = request;
-    rows = 0;
-    if (r.n_q * (int64_t)a.G > a.max_rows) err |= TQ_DEV_ERR_SPLITS;
-    else rows = r.n_q * a.G;
-    nt = (rows + T - 1) / T;
-    const int base = a.causal ? max(0, r.kv - r.n_q) : r.kv;
-    fixed = (int64_t)base * 64 / BN + kTileCost;
-    slope = a.causal ? max(1, T * 64 / (a.G * BN)) : 0;
-  }
-  __device__ __forceinline__ int64_t before(int tile) const {
-    return tile * fixed + slope * ((int64_t)tile * (tile + 1) / 2);
-  }
-  // The tile in hand: its place, or the first one of a later request.
-  __device__ __forceinline__ void settle(const AttnArgs& a) {
-    uint32_t err = 0;
-    while (t >= nt && b < a.batch) {
-      t = 0;
-      if (nt > 0 && ++h < a.hkv) break;
-      h = 0;
-      if (b + 1 >= a.batch) {
-        b = a.batch;
-        break;
-      }
-      load(a, b + 1, err);
-    }
-    e = s + fixed + slope * (t + 1);
-  }
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    s = e;
-    ++t;
-    settle(a);
-  }
-};
-
-// First unit of the part of a tile [s, e) that begins at place p of the line.
-__device__ __forceinline__ int cut_at(int64_t p, int64_t s, int64_t e, int units) {
-  return p <= s ? 0 : p >= e ? units : (int)((p - s) * units / (e - s));
-}
-
-// What a CTA does of one tile, as its warps read it from a ring in shared memory that one thread fills. n_all < 0: no
-// more.
-struct Part {
-  int f0, rows;      // first row of the tile, rows of the request
-  int kv;            // tokens that any row of the tile sees
-  int u0, n_all;     // first unit, units
-  int n_of[2];       // units of each tile of 128 rows: up to the last token that its last row sees
-  int h, q0, n_q, r_kv, row, base;  // KV head and request
-  int direct, slot;  // all of the tile: results go to out; else which part of the workspace takes them
-};
-constexpr int kParts = 4;
-
-// Workspace: the cut tiles [CTAs], then {m, l} [CTAs][2][T] and the sums [CTAs][2][T][D] of the parts of cut tiles;
-// part 0 of a CTA is of a tile that an earlier CTA began, part 1 of one that it began itself.
-__device__ __forceinline__ CutTile* cut_tiles(const AttnArgs& a) { return reinterpret_cast<CutTile*>(a.part); }
-template <int T>
-__device__ __forceinline__ float2* cut_ml(const AttnArgs& a, int ctas, int cta, int part) {
-  return reinterpret_cast<float2*>(cut_tiles(a) + ctas) + ((size_t)cta * 2 + part) * T;
-}
-template <int T, int D>
-__device__ __forceinline__ float* cut_o(const AttnArgs& a, int ctas, int cta, int part) {
-  return reinterpret_cast<float*>(reinterpret_cast<float2*>(cut_tiles(a) + ctas) + (size_t)ctas * 2 * T) +
-         ((size_t)cta * 2 + part) * T * D;
-}
-
-// Rescale O when a maximum grows by more than this (in powers of two).
-constexpr float kLazy = 8.0f;
+constexpr int kTileCost = 96;  // start and end of a tile, as 1.5 units
+constexpr int kMinPart = 320;  // no CTA gets less than this (5 units): short work takes fewer CTAs
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
@@ -207,6 +105,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               const __grid_constant__ CUtensorMap map_v) {
   using Sh = TcShape<D>;
   constexpr int NT = Sh::kNT, BN = Sh::kBN, ST = Sh::kStages, T = 128 * NT;
+  using W = Walk<T, BN, kTileCost, NT>;
   constexpr uint32_t kTile = Sh::kTile;
   constexpr uint32_t kType = BF16 ? 1u : 0u;
   constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
@@ -230,12 +129,14 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drained + 1);
   __shared__ int64_t warp_sums[Sh::kThreads / 32];
   __shared__ Part parts[kParts];
-  __shared__ int64_t line[3];  // this CTA's part of the line, and where the tile that holds its start begins
-  __shared__ int first[6];     // that tile: request, head, tile; the request's first row, queries, tokens
-  __shared__ int first_kv[2];  // and where its K and V are
+  __shared__ LineStart first;
 
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
   constexpr int kMmaWarp = NT * 4, kTmaWarp = NT * 4 + 1, kWalkWarp = NT * 4 + 2, kMmaWarp1 = NT * 4 + 3;
+  if (threadIdx.x == 32) {
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
@@ -266,74 +167,9 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   pdl_launch();  // the join may be scheduled; it waits for this kernel's end
   uint32_t err = 0;
 
-  // ---- this CTA's part of the line: prefix sums of the requests' costs over the block ----
-  {
-    Walk<T, BN> w;
-    const int per = (a.batch + Sh::kThreads - 1) / Sh::kThreads;
-    const int lo = min(a.batch, (int)threadIdx.x * per), hi = min(a.batch, lo + per);
-    int64_t sum = 0;
-    for (int b = lo; b < hi; ++b) {
-      w.load(a, b, err);
-      sum += a.hkv * w.before(w.nt);
-    }
-    if (blockIdx.x == 0 && err && a.status) atomicOr(a.status, err);
-    err = 0;
-    int64_t inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) warp_sums[warp] = inc;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    int64_t start = inc - sum, total = 0;
-#pragma unroll
-    for (int i = 0; i < Sh::kThreads / 32; ++i) {
-      if (i < warp) start += warp_sums[i];
-      total += warp_sums[i];
-    }
-    const int64_t q = max((int64_t)kMinPart, (total + gridDim.x - 1) / gridDim.x);
-    const int64_t p0 = q * blockIdx.x, p1 = min(total, p0 + q);
-    if (p0 >= start && p0 < start + sum) {  // one thread's requests hold p0
-      for (int b = lo; b < hi; ++b) {
-        w.load(a, b, err);
-        const int64_t one = w.before(w.nt);
-        if (p0 >= start + a.hkv * one) {
-          start += a.hkv * one;
-          continue;
-        }
-        const int head = (int)((p0 - start) / one);
-        start += head * one;
-        int at = 0, n = w.nt;  // the last tile that begins at p0 or before
-        while (n > 1) {
-          const int half = n / 2;
-          if (start + w.before(at + half) <= p0) {
-            at += half;
-            n -= half;
-          } else {
-            n = half;
-          }
-        }
-        first[0] = b;
-        first[1] = head;
-        first[2] = at;
-        first[3] = w.r.q0;
-        first[4] = w.r.n_q;
-        first[5] = w.r.kv;
-        first_kv[0] = w.r.row;
-        first_kv[1] = w.r.base;
-        line[2] = start + w.before(at);
-        break;
-      }
-    }
-    if (threadIdx.x == 0) {
-      line[0] = p0;
-      line[1] = p1;
-    }
-    __syncthreads();
-  }
+  tc_fence_before();
+  find_start<W, Sh::kThreads>(a, kMinPart, first, warp_sums);
+  tc_fence_after();
   const uint32_t tmem = uniform(*tmem_base);
   bool ok = true;
   int at = 0;  // parts taken from the ring
@@ -486,63 +322,12 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       if ((!ok || !done) && lane == 0 && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
     } else if (warp == kWalkWarp && lane == 0) {
       // ---- the parts of this CTA, in order ----
-      Walk<T, BN> w;
-      w.p0 = line[0];
-      w.p1 = line[1];
+      W w;
+      w.start(a, first);
       CutTile cut = {};
-      w.b = a.batch;
-      if (w.p0 < w.p1) {
-        Request r;
-        r.q0 = first[3];
-        r.n_q = first[4];
-        r.kv = first[5];
-        r.row = first_kv[0];
-        r.base = first_kv[1];
-        w.b = first[0];
-        w.take(a, r, err);
-        w.h = first[1];
-        w.t = first[2];
-        w.s = line[2];
-        w.settle(a);
-      }
       for (bool more = true; more;) {
         Part g = {};
-        g.n_all = -1;
-        more = w.b < a.batch && w.s < w.p1;
-        if (more) {
-          g.f0 = w.t * T;
-          g.rows = w.rows;
-          g.kv = tile_kv(a, w.r, w.t, T);
-          const int units = (g.kv + BN - 1) / BN;
-          g.u0 = cut_at(w.p0, w.s, w.e, units);
-          const int u1 = cut_at(w.p1, w.s, w.e, units);
-          g.n_all = u1 - g.u0;
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            const int kv_t = g.f0 + t * 128 < w.rows ? tile_kv(a, w.r, w.t * NT + t, 128) : 0;
-            g.n_of[t] = max(0, min(u1, (kv_t + BN - 1) / BN) - g.u0);
-          }
-          g.h = w.h;
-          g.q0 = w.r.q0;
-          g.n_q = w.r.n_q;
-          g.r_kv = w.r.kv;
-          g.row = w.r.row;
-          g.base = w.r.base;
-          g.direct = g.n_all == units;
-          g.slot = w.s >= w.p0;
-          if (g.slot && w.e > w.p1) {
-            cut.units = units;
-            cut.f0 = g.f0;
-            cut.rows = w.rows;
-            cut.q0 = w.r.q0;
-            cut.h = w.h;
-            cut.s = w.s;
-            cut.e = w.e;
-            cut.q = w.p1 - w.p0;  // a whole part: the tile goes on behind it
-          }
-          w.next(a);
-          if (g.n_all == 0 && (units > 0 || !g.slot)) continue;  // nothing of it falls to this CTA
-        }
+        more = w.next(a, g, cut);
         const int i = at % kParts;
         if (at >= kParts) ok = mbar_wait(&part_empty[i], (at / kParts - 1) & 1);
         if (!ok) break;
@@ -603,7 +388,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       r.kv = g.r_kv;
       const int lim = mine ? seen(a, r, qi) : 0;
       // what every row of the tile sees needs no mask; rows past the last may hold anything
-      const int lim_all = seen(a, r, min(g.f0 + t * 128, g.rows - 1) / a.G);
+      const int lim_all = seen(a, r, a.div_g(min(g.f0 + t * 128, g.rows - 1)));
       const int u0 = g.u0;
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
       float m = -INFINITY, l = 0.f;
@@ -743,84 +528,6 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   }
 }
 
-// k_attn_tc_join: the parts of the tile that CTA blockIdx.x began and did not end, joined with their maxima and sums.
-// Each warp takes kJoinRows / 4 rows at once, so that their loads overlap; latency bounds the kernel.
-constexpr int kJoinRows = 16;
-constexpr int kJoinMost = 1024;  // CTAs of a launch at most
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) k_attn_tc_join(const __grid_constant__ AttnArgs a, int ctas) {
-  constexpr int T = 128 * TcShape<D>::kNT, V = D / 32, R = kJoinRows / 4;
-  __shared__ int16_t part[kJoinMost];
-  __shared__ int parts;
-  pdl_wait();
-  const CutTile c = cut_tiles(a)[blockIdx.x];
-  const int row0 = blockIdx.y * kJoinRows;
-  if (!c.units || c.f0 + row0 >= c.rows) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i0 = blockIdx.x, i1 = (int)((c.e - 1) / c.q);
-  if (warp == 0) {  // the CTAs that had units of it
-    int n = 0;
-    for (int base = i0; base <= i1; base += 32) {
-      const int i = base + lane;
-      const bool live = i <= i1 && cut_at((i + 1) * c.q, c.s, c.e, c.units) > cut_at(i * c.q, c.s, c.e, c.units);
-      const uint32_t m = __ballot_sync(0xffffffffu, live);
-      if (live) part[n + __popc(m & ((1u << lane) - 1))] = (int16_t)i;
-      n += __popc(m);
-    }
-    if (lane == 0) parts = n;
-  }
-  __syncthreads();
-  if (parts < 2) return;  // one CTA had all of it
-  float top[R], sum[R], acc[R][V];
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    top[j] = -INFINITY;
-    sum[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
-  }
-#pragma unroll 2
-  for (int k = 0; k < parts; ++k) {
-    const int i = part[k];
-    const float2* pml = cut_ml<T>(a, ctas, i, i == i0) + row0 + warp;
-    const float* po = cut_o<T, D>(a, ctas, i, i == i0) + (size_t)(row0 + warp) * D + lane * V;
-    float2 ml[R];
-    float v[R][V];
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      ml[j] = pml[4 * j];
-      if constexpr (V == 2) *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(po + 4 * j * D);
-      else
-#pragma unroll
-        for (int q = 0; q < V; q += 4)
-          *reinterpret_cast<float4*>(v[j] + q) = *reinterpret_cast<const float4*>(po + 4 * j * D + q);
-    }
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-      const float mn = fmaxf(top[j], ml[j].x), mu = mn == -INFINITY ? 0.f : mn;
-      const float wa = exp2_fast(top[j] - mu), wb = exp2_fast(ml[j].x - mu);  // 0 for a part that saw no token
-      top[j] = mn;
-      sum[j] = sum[j] * wa + ml[j].y * wb;
-#pragma unroll
-      for (int i2 = 0; i2 < V; ++i2) acc[j][i2] = acc[j][i2] * wa + v[j][i2] * wb;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < R; ++j) {
-    const int f = c.f0 + row0 + warp + 4 * j;
-    if (f >= c.rows) continue;
-    const float inv = sum[j] > 0.f ? 1.f / sum[j] : 0.f;
-    const int qi = a.div_g(f), head = c.h * a.G + f - qi * a.G;
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(c.q0 + qi) * a.o_row + (int64_t)head * a.o_head + lane * V;
-    uint32_t out[V / 2];
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) out[i] = pack2<BF16>(acc[j][2 * i] * inv, acc[j][2 * i + 1] * inv);
-    if constexpr (V == 2) *reinterpret_cast<uint32_t*>(dst) = out[0];
-    else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
-  }
-}
-
 template <int D, bool BF16>
 cudaError_t launch_tc_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, cudaStream_t s) {
   using Sh = TcShape<D>;
@@ -828,14 +535,15 @@ cudaError_t launch_tc_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p
   if (e == cudaSuccess)
     e = launch_pdl(k_attn_tc<D, BF16>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_attn_tc_join<D, BF16>, dim3(p.ctas, Sh::kNT * 128 / kJoinRows), dim3(128), 0, s, a, p.ctas);
+  return launch_join<D, 128 * Sh::kNT, BF16>(a, p.ctas, p.max_rows, s);
 }
 
 }  // namespace
 
-size_t attn_tc_bytes(int d, int ctas) {
-  const size_t rows = (size_t)ctas * 2 * 128 * (d == 256 ? TcShape<256>::kNT : TcShape<128>::kNT);
-  return ctas * sizeof(CutTile) + rows * (sizeof(float2) + d * sizeof(float));
+AttnShape attn_tc_shape(int d, int sms) {
+  const int tile = d == 256 ? 128 * TcShape<256>::kNT : 128 * TcShape<128>::kNT;
+  return {tile, d == 256 ? TcShape<256>::kBN : TcShape<128>::kBN, sms,
+          cta_bytes(tile, d), kTileCost, kMinPart};
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {
@@ -847,7 +555,5 @@ cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan&
          : d == 128 ? launch_tc_as<128, false>(a, m, p, s)
                     : launch_tc_as<256, false>(a, m, p, s);
 }
-
-int attn_tc_unit(int d) { return d == 256 ? TcShape<256>::kBN : TcShape<128>::kBN; }
 
 }  // namespace tq

@@ -164,7 +164,7 @@ def append(k, v, k_pool, v_pool, slots, status=None, stream=None):
                                      _optional("status", status, device, 1), on.raw))
 
 
-def _attend(q, dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv, max_pages, call):
+def _attend(q, dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv, call):
     if q.dim() != 3 or q.dtype is not dtype or q.device != device or q.shape[2] != d or q.shape[1] % heads or not q.shape[1]:
         raise ValueError(f"q: expected a {dtype} tensor [rows, a multiple of {heads} heads, {d}] on {device}")
     if out is None:
@@ -181,7 +181,7 @@ def _attend(q, dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, 
     queries = _QUERIES.pack(q.data_ptr(), out.data_ptr(), qs[0], qs[1], os[0], os[1], _ints("q_starts", q_starts, device), q.shape[0],
                             q.shape[1], batch, max_q, max_kv, softmax_scale)
     if workspace is None:
-        n = load().tq_attention_workspace_bytes(queries, kv, max_pages)
+        n = load().tq_attention_workspace_bytes(queries, kv)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
@@ -191,15 +191,15 @@ def _attend(q, dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, 
     return out
 
 
-def attention_workspace_bytes(q, k, max_q=0, max_kv=0, batch=1, max_pages=0):
-    """Bytes of workspace that attention (max_pages: the table's width) or cross_attention (0) needs for q [rows, heads,
-    d] against k (a pool, or an encoder's states) in `batch` requests; 0: none."""
+def attention_workspace_bytes(q, k, max_q=0, max_kv=0, batch=1):
+    """Bytes of workspace that attention or cross_attention needs for q [rows, heads, d] against k (a pool, or an encoder's
+    states) in `batch` requests."""
     s = k.stride()
     dims = (1, k.shape[0]) if k.dim() == 3 else tuple(k.shape[:2])
     kv = _kv(k, k, *dims, k.shape[-2], k.shape[-1], (0, 0, 0) if k.dim() == 3 else s[:3], (0, 0, 0))
     queries = _QUERIES.pack(0, 0, 0, 0, 0, 0, 0, q.shape[0], q.shape[1], batch, max_q, max_kv, 0.0)
     with _On(_cuda("q", q), None):
-        return load().tq_attention_workspace_bytes(queries, kv, max_pages)
+        return load().tq_attention_workspace_bytes(queries, kv)
 
 
 def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True, softmax_scale=0.0, max_q=0, max_kv=0, out=None,
@@ -208,8 +208,8 @@ def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True,
 
     q: [rows, n_q_heads, head_dim] of the pools' type, request b's rows at [q_starts[b], q_starts[b + 1]); kv_lens[b]: its
     tokens with the new ones, in the pages of table row seq_ids[b] (None: row b). max_q: no request has more rows (0:
-    unknown); max_kv: about the longest request's tokens (0: unknown); both choose the kernel and the splits. Returns out, of
-    q's shape; rows behind the last request stay as they are."""
+    unknown; few rows take a kernel of their own); max_kv: no request has more tokens (0: unknown; short calls launch fewer
+    CTAs). Returns out, of q's shape; rows behind the last request stay as they are."""
     device, kv = _pools(k_pool, v_pool)
     if table.dtype is not torch.int32 or table.dim() != 2 or table.device != device or not table.shape[0] or not table.shape[1] or table.stride(1) != 1:
         raise ValueError(f"table: expected int32 [max_seqs, max_pages] with contiguous rows on {device}")
@@ -223,7 +223,7 @@ def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True,
 
     with _On(device, stream, q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, out, workspace, status) as on:
         return _attend(q, k_pool.dtype, k_pool.shape[2], k_pool.shape[3], device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv,
-                       max_pages, call)
+                       call)
 
 
 def cross_attention(q, k, v, q_starts, kv_lens=None, kv_starts=None, softmax_scale=0.0, max_q=0, max_kv=0, out=None, workspace=None,
@@ -254,7 +254,7 @@ def cross_attention(q, k, v, q_starts, kv_lens=None, kv_starts=None, softmax_sca
                                         ws, ws_bytes, word, raw))
 
     with _On(device, stream, q, k, v, q_starts, kv_lens, kv_starts, out, workspace, status) as on:
-        return _attend(q, k.dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv, 0, call)
+        return _attend(q, k.dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv, call)
 
 
 class BlockPool:

@@ -260,7 +260,7 @@ def test_paged_attention(dtype, d, heads, case):
 @pytest.mark.parametrize("nq,kv", [([1, 1], [9000, 1]), ([3], [20000]), ([1, 2, 1], [5000, 4999, 130]), ([100], [9000]), ([40, 1], [6000, 7000])])
 def test_paged_attention_over_split_sequences(d, nq, kv):
     q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, d, torch.bfloat16, False, 7 + d, tail=1)
-    assert paged.attention_workspace_bytes(q, pool[0], max(nq), max(kv), len(nq), table.shape[1]) > 0
+    assert paged.attention_workspace_bytes(q, pool[0], max(nq), max(kv), len(nq)) > 0
     out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
     paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=max(nq), max_kv=max(kv), out=out)
     check_rows(out, q, ks, vs, nq, kv, True, 1 / math.sqrt(d))
@@ -376,7 +376,7 @@ def test_a_captured_step_replays_on_new_lengths():
     k = torch.zeros((room, hkv, d), dtype=torch.bfloat16, device=DEV)
     v, q = torch.zeros_like(k), torch.zeros((room, hq, d), dtype=torch.bfloat16, device=DEV)
     out = torch.zeros_like(q)
-    need = paged.attention_workspace_bytes(q, cache.kv[0, 0], room, 2048, 2, pool.table.shape[1])
+    need = paged.attention_workspace_bytes(q, cache.kv[0, 0], room, 2048, 2)
     ws = torch.empty(max(need, 256), dtype=torch.uint8, device=DEV)
 
     def step():
