@@ -8,6 +8,8 @@
 // requests.
 #pragma once
 
+#include <atomic>
+
 #include "tq_attention.cuh"
 
 namespace tq {
@@ -178,8 +180,8 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, int64_t least, Lin
     if (i < warp) start += warp_sums[i];
     total += warp_sums[i];
   }
-  const int64_t sum_up = total + gridDim.x - 1;
-  const int64_t q = max(least, sum_up < (1ll << 32) ? (int64_t)((uint32_t)sum_up / gridDim.x) : sum_up / gridDim.x);
+  // an equal share, a millionth up so that no rounding leaves work over
+  const int64_t q = max(least, (int64_t)((float)total * __frcp_rn((float)gridDim.x) * 1.000001f) + 1);
   const int64_t p0 = q * blockIdx.x, p1 = min(total, p0 + q);
   if (threadIdx.x == 0) {
     st.p0 = p0;
@@ -338,6 +340,20 @@ __global__ void __launch_bounds__(JoinShape<T>::kWarps * 32) k_attn_join(const _
     else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
   }
+}
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device; asked once per device (`known`: one bit
+// each).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>& known) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (known.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) known.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // `rows`: the most rows that a request has (no tile has more).

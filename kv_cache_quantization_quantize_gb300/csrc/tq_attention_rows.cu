@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
   for (int at = 0;; ++at) {
     const int pi = at % kParts;
     ok = ok && warp_wait(&part_full[pi], (at / kParts) & 1);
-    Part g;
+    Part g = {};
     if (ok) g = parts[pi];
     give_up();
     if (consumers_any(!ok)) break;
@@ -215,10 +215,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
       for (int i = 0; i < 2 * NP; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        m[t][x] = -INFINITY;
         l[t][x] = 0.f;
         const int f = g.f0 + t * 16 + g8 + x * 8;
         lim[t][x] = f < g.rows ? seen(a, r, a.div_g(f)) : 0;
+        m[t][x] = f < g.rows ? -INFINITY : INFINITY;  // a row past the last, of any scores, never outgrows its maximum
       }
     }
     const int lim_all = seen(a, r, a.div_g(g.f0));  // what every row of the tile sees needs no mask
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
         need |= top[t][0] > m[t][0] + kLazy || top[t][1] > m[t][1] + kLazy;
       }
       float sum[MT][2];
-      auto weights = [&] {
+      for (;;) {  // twice where a maximum outgrew its range: the code is not doubled, since a cold path costs its fetches
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
@@ -323,15 +323,13 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
                            : "memory");
           }
         }
-      };
-      weights();
-      give_up();
-      if (consumers_any(need || !ok)) {
+        give_up();
+        if (!consumers_any(need || !ok)) break;
         if (*(volatile int*)&gave_up) {
           left = true;
           break;
         }
-        // a maximum outgrew its range: new ones for all rows, from all four warps
+        // new maxima for all rows, from all four warps
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -352,17 +350,19 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
             m[t][x] = mn;
             l[t][x] *= alpha[x];
           }
+          if (k > 0) {
 #pragma unroll
-          for (int i = 0; i < 2 * NP; ++i) {
-            o[t][i][0] *= alpha[0];
-            o[t][i][1] *= alpha[0];
-            o[t][i][2] *= alpha[1];
-            o[t][i][3] *= alpha[1];
+            for (int i = 0; i < 2 * NP; ++i) {
+              o[t][i][0] *= alpha[0];
+              o[t][i][1] *= alpha[0];
+              o[t][i][2] *= alpha[1];
+              o[t][i][3] *= alpha[1];
+            }
           }
         }
-        weights();
-        consumers_any(false);
+        need = false;  // no weight is above 1 now
       }
+      if (left) break;
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         l[t][0] += sum[t][0];
@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
 template <int D, int MT, bool BF16>
 cudaError_t launch_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, cudaStream_t s) {
   using Sh = RowsShape<D, MT>;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_rows<D, MT, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  static std::atomic<uint64_t> known{0};
+  cudaError_t e = allow_smem(k_attn_rows<D, MT, BF16>, Sh::kSmem, known);
   if (e == cudaSuccess)
     e = launch_pdl(k_attn_rows<D, MT, BF16>, dim3(p.ctas), dim3(kRowsThreads), Sh::kSmem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;

@@ -31,6 +31,9 @@ struct TcShape {
   // S_t is made while the softmax works on this one.
   static constexpr bool kOwnP = D != 128;
   static constexpr uint32_t kP = kOwnP ? (D == 64 ? 256 : 128) : 0, kPStep = kOwnP ? 64 : 128;
+  // At D = 256 one tile has to hide its own softmax: S and P are doubled (64 and 32 columns apart), so that the scores
+  // of the next unit are made before this one's products, and weights can be written while the last ones are used.
+  static constexpr int kBufs = D == 256 ? 2 : 1;
   static constexpr uint32_t kO = D == 64 ? 384 : 256;
   // At D = 128 the tiles' softmaxes take turns: left alone they fall into step, share the special function units and
   // then leave the tensor pipe idle together (2900 cycles per unit against 2500; the SMs differed by 30 %). At D = 64
@@ -117,11 +120,13 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(skv + ST * kTile);
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;       // per tile: queries are in shared memory
-  uint64_t* s_full = q_full + NT;      // per tile: scores are in TMEM
-  uint64_t* p_full = s_full + NT;      // per tile and half of the unit: weights are in TMEM, O is rescaled
-  uint64_t* o_full = p_full + 2 * NT;  // per tile: the product with V is done
-  uint64_t* s_free = o_full + NT;      // per tile: the softmax has read the scores (kOwnP)
-  uint64_t* v_clean = s_free + NT;     // per ring entry: V rows behind the sequence are zeroed
+  // per tile and buffer of S and P (one barrier each, so that none is ever two phases ahead of a waiting warp):
+  constexpr int NB = NT * Sh::kBufs;
+  uint64_t* s_full = q_full + NT;      // scores are in TMEM
+  uint64_t* p_full = s_full + NB;      // and half of the unit: weights are in TMEM, O is rescaled
+  uint64_t* o_full = p_full + 2 * NB;  // the product with V is done
+  uint64_t* s_free = o_full + NB;      // the softmax has read the scores (kOwnP)
+  uint64_t* v_clean = s_free + NB;     // per ring entry: V rows behind the sequence are zeroed
   uint64_t* turn = v_clean + ST;       // per tile: the other tile's warps have made their weights
   uint64_t* part_full = turn + NT;     // ring of parts
   uint64_t* part_empty = part_full + kParts;
@@ -145,12 +150,14 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     }
     for (int i = 0; i < NT; ++i) {
       mbar_init(&q_full[i], 4);
+      mbar_init(&turn[i], 4);
+    }
+    for (int i = 0; i < NB; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[2 * i], 4);
       mbar_init(&p_full[2 * i + 1], 4);
       mbar_init(&o_full[i], 1);
       mbar_init(&s_free[i], 4);
-      mbar_init(&turn[i], 4);
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&part_full[i], 1);
@@ -171,6 +178,9 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   find_start<W, Sh::kThreads>(a, kMinPart, first, warp_sums);
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_base);
+  // unit j of a tile uses buffer j % kBufs for the (j / kBufs)-th time
+  auto buf_of = [](int j) { return j % Sh::kBufs; };
+  auto turn_of = [](int j) { return (j / Sh::kBufs) & 1; };
   bool ok = true;
   int at = 0;  // parts taken from the ring
   // the next part of the ring into registers; false: no more (or a wait gave up)
@@ -238,11 +248,13 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       int made = 0;    // units whose products are issued
       int loaded = 0;  // query tiles taken
       uint32_t cleaned = 0;  // parities of v_clean: an entry is cleaned again only after this warp gave it back
-      // S_t = Q_t K^T of ring entry `entry`, or nothing; the entry is given back either way, once it has been filled
-      auto scores = [&](int entry, bool wanted, uint64_t* after, int parity) {
-        const int st = entry % ST;
+      // S_t = Q_t K^T of unit j from ring entry `entry`, or nothing; the entry is given back either way, once it has been
+      // filled. Where S_t goes, the scores of unit j - kBufs have been read, and with P_t over them, used.
+      auto scores = [&](int entry, bool wanted, int j) {
+        const int st = entry % ST, before = j - Sh::kBufs;
         ok = ok && warp_wait(&full[st], (entry / ST) & 1);
-        if (wanted && after) ok = ok && warp_wait(after, parity & 1);
+        if (wanted && before >= 0)
+          ok = ok && warp_wait((Sh::kOwnP ? s_free : o_full) + t * Sh::kBufs + buf_of(before), turn_of(before));
         if (!ok) return;
         tc_fence_after();
         if (leader) {
@@ -251,9 +263,9 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               const uint32_t step = (i & 3) * 2;
-              umma_bf16_lo(sd, q_lo + (i >> 2) * 1024 + step, ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
+              umma_bf16_lo(sd + buf_of(j) * 64, q_lo + (i >> 2) * 1024 + step, ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
             }
-            umma_commit(&s_full[t]);
+            umma_commit(&s_full[t * Sh::kBufs + buf_of(j)]);
           }
           umma_commit(&empty[st]);
         }
@@ -267,11 +279,9 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           ok = warp_wait(&q_full[t], loaded & 1);
           ++loaded;
         }
-        // where S_t goes: the last unit's scores have been read, and with P_t over them, its product is done
-        uint64_t* const s_ready = Sh::kOwnP ? &s_free[t] : &o_full[t];
-        scores(e, n > 0, made > 0 ? s_ready : nullptr, made - 1);
+        scores(e, n > 0, made);
         for (int k = 0; k < n_all && ok; ++k, e += 2) {
-          if (Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, s_ready, made);
+          if (Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1);
           const int vs = (e + 1) % ST;
           ok = ok && warp_wait(&full[vs], ((e + 1) / ST) & 1);
           if (!ok) break;
@@ -299,21 +309,21 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
             const uint32_t va = kv_lo + vs * (kTile >> 4) + ((uint32_t)(BN * 128 >> 4) << 16);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && warp_wait(&p_full[2 * t + half], made & 1);
+              ok = ok && warp_wait(&p_full[2 * (t * Sh::kBufs + buf_of(made)) + half], turn_of(made));
               if (!ok) break;
               tc_fence_after();
               if (leader) {
 #pragma unroll
                 for (int i = half * (BN / 32); i < (half + 1) * (BN / 32); ++i)
-                  if (i < steps) umma_ts_lo(od, pa + i * 8, va + i * (2048 >> 4), kIdescO, k > 0 || i > 0);
+                  if (i < steps) umma_ts_lo(od, pa + buf_of(made) * 32 + i * 8, va + i * (2048 >> 4), kIdescO, k > 0 || i > 0);
               }
             }
             if (!ok) break;
-            if (leader) umma_commit(&o_full[t]);
+            if (leader) umma_commit(&o_full[t * Sh::kBufs + buf_of(made)]);
             ++made;
           }
           if (leader) umma_commit(&empty[vs]);
-          if (!Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, s_ready, made - 1);
+          if (!Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, made);
         }
       }
       // leave only when every product is done
@@ -393,7 +403,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
       float m = -INFINITY, l = 0.f;
       for (int k = 0; k < n; ++k) {
-        ok = warp_wait(&s_full[t], made & 1);
+        const int bi = t * Sh::kBufs + buf_of(made);
+        ok = warp_wait(&s_full[bi], turn_of(made));
         if (!ok) break;
         tc_fence_after();
         // the other tile's weights are made: now this one has the special function units, and that one the tensor pipe
@@ -403,12 +414,12 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         float s[BN];
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + c, s + c);
+        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + buf_of(made) * 64 + c, s + c);
         tmem_wait_ld();
         if constexpr (Sh::kOwnP) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_free[t]);
+          if (lane == 0) mbar_arrive(&s_free[bi]);
         }
         const int base = (u0 + k) * BN;
         if (base + BN > lim_all) {
@@ -429,8 +440,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         if (mx > m + kLazy || m == -INFINITY) mn = fmaxf(m, mx);
         const bool grew = mn != m && m != -INFINITY;
         const bool rescale = __any_sync(0xffffffffu, grew);
-        if (rescale || (Sh::kOwnP && made > 0)) {  // O_t is whole, and P_t has been used
-          ok = warp_wait(&o_full[t], (made - 1) & 1);
+        // O_t is whole before it is rescaled, and P_t has been used before it is written again
+        const int last = rescale ? made - 1 : Sh::kOwnP ? made - Sh::kBufs : -1;
+        if (last >= 0) {
+          ok = warp_wait(&o_full[t * Sh::kBufs + buf_of(last)], turn_of(last));
           if (!ok) break;
           tc_fence_after();
         }
@@ -463,12 +476,12 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               sum[i & 1] = add2(sum[i & 1], y);
               p[i] = pack2<BF16>(y.x, y.y);
             }
-            tmem_st16(tp + c / 2, p);
+            tmem_st16(tp + buf_of(made) * 32 + c / 2, p);
           }
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+          if (lane == 0) mbar_arrive(&p_full[2 * bi + half]);
         }
         if (k < both) {
           if (lane == 0) mbar_arrive(&turn[1 - t]);
@@ -491,7 +504,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       if (!ok) break;
       if (have) load_q();
       if (n > 0) {
-        ok = warp_wait(&o_full[t], (made - 1) & 1);
+        ok = warp_wait(&o_full[t * Sh::kBufs + buf_of(made - 1)], turn_of(made - 1));
         if (!ok) break;
         tc_fence_after();
       }
@@ -531,7 +544,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
 template <int D, bool BF16>
 cudaError_t launch_tc_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, cudaStream_t s) {
   using Sh = TcShape<D>;
-  cudaError_t e = cudaFuncSetAttribute(k_attn_tc<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  static std::atomic<uint64_t> known{0};
+  cudaError_t e = allow_smem(k_attn_tc<D, BF16>, Sh::kSmem, known);
   if (e == cudaSuccess)
     e = launch_pdl(k_attn_tc<D, BF16>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
