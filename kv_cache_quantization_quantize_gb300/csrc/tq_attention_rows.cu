@@ -7,15 +7,14 @@ namespace {
 // =============================================================================================
 // k_attn_rows: a CTA takes its part of the line (tq_attention_line.cuh) in tiles of up to 16 MT rows (query, head of
 // the group) of one request and KV head. Every K and V byte is used by all rows of the tile and read once, which
-// bounds the kernel: DRAM. A producer warp walks the parts and keeps a ring of K and V tiles (64 tokens) in flight
-// with TMA, over the ends of parts. Four consumer warps share each unit: for the scores each takes 16 tokens, for the
-// sums each takes D / 4 channels of all 64, with the weights handed over through shared memory. So no warp holds more
+// bounds the kernel: DRAM. A producer warp walks the parts and keeps a ring of K and V tiles in flight
+// with TMA, over the ends of parts. Four consumer warps share each unit: for the scores each takes a quarter of its
+// tokens, for the sums each takes D / 4 channels of all of them, with the weights handed over through shared memory. So no warp holds more
 // than D / 4 channels of the sums and nothing has to be joined at the end; one barrier per unit hands over the weights
 // and tells whether a maximum outgrew its range (kLazy), which is rare after a tile's first unit. Scores and sums run
 // on mma.sync m16n8k16: at 16 or 32 rows the tensor pipe has a few percent of its work, and its register operands
 // need no copies.
 // =============================================================================================
-constexpr int kUnit = 64;
 constexpr int kRowsThreads = 160;  // four consumer warps, one producer warp
 constexpr int kTileCost = 64;      // start and end of a tile, as one unit
 constexpr int kMinPart = 192;      // no CTA gets less than this (3 units)
@@ -23,12 +22,13 @@ constexpr int kMinPart = 192;      // no CTA gets less than this (3 units)
 template <int D, int MT>
 struct RowsShape {
   static constexpr int R = 16 * MT;
-  static constexpr int kEntry = kUnit * D * 2;                                   // bytes of K or V of one unit
-  static constexpr int kCtas = D == 256 ? 1 : 2;                                 // CTAs per SM
-  static constexpr int kEntries = D == 64 ? 10 : D == 128 ? 5 : (MT == 1 ? 6 : 5);  // 80 KB (160 to 192) in flight
+  static constexpr int U = D == 64 ? 128 : 64;    // tokens of a unit: 16 KB of K and as much of V (32 at head_dim 256)
+  static constexpr int kEntry = U * D * 2;        // bytes of K or V of one unit
+  static constexpr int kCtas = D == 256 ? 1 : 2;  // CTAs per SM
+  static constexpr int kEntries = D == 256 && MT == 1 ? 6 : 5;  // 80 KB per CTA in flight (160 to 192 at head_dim 256)
   static constexpr int kQRow = D * 2 + 16;  // bytes of a query row: 16 more than it has, so that ldmatrix meets no conflicts
   static constexpr int kQ = R * kQRow;
-  static constexpr int kP = R * kUnit * 2;  // weights of one unit
+  static constexpr int kP = R * U * 2;  // weights of one unit
   static constexpr int kSmem = 1024 + kEntries * kEntry + 2 * kQ + 2 * kP;
 };
 
@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
     k_attn_rows(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
   using Sh = RowsShape<D, MT>;
-  using W = Walk<Sh::R, kUnit, kTileCost, 0>;
+  using W = Walk<Sh::R, Sh::U, kTileCost, 0>;
+  constexpr int U = Sh::U, TW = U / 4, NS = TW / 8;  // tokens of a warp, tiles of 8 of them
   constexpr int R = Sh::R, ST = Sh::kEntries, KS = D / 16, NP = D / 64;  // NP: pairs of 8-channel tiles of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
       int2 place = make_int2(0, 0);
       for (int k = 0; k < g.n_all && ok; ++k, e += 2) {
         if ((k & 31) == 0 && k + lane < g.n_all) {
-          const int tok = (g.u0 + k + lane) * kUnit;
+          const int tok = (g.u0 + k + lane) * U;
           place = page_place(a, r, tok / kPage, err);
           place.y += tok % kPage;
         }
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
             mbar_expect_tx(&full[st], Sh::kEntry);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
-              tma_load_4d(dst + c * (kUnit * 128), which ? &map_v : &map_k, c * 64, py, g.h, pw, &full[st]);
+              tma_load_4d(dst + c * (U * 128), which ? &map_v : &map_k, c * 64, py, g.h, pw, &full[st]);
             issued = e + which + 1;
           }
         }
@@ -238,10 +239,10 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
     }
     bool left = false;
     for (int k = 0; k < g.n_all; ++k, e += 2, ++unit) {
-      const int base = (g.u0 + k) * kUnit, t0 = base + warp * 16;
+      const int base = (g.u0 + k) * U, t0 = base + warp * TW;
       const uint32_t pb = pbase + (unit & 1) * Sh::kP;
-      float s[MT][2][4], top[MT][2];
-      // scores of 16 tokens
+      float s[MT][NS][4], top[MT][2];
+      // scores of this warp's tokens
       {
         const int st = e % ST;
         ok = ok && warp_wait(&full[st], (e / ST) & 1);
@@ -249,39 +250,51 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int n = 0; n < 2; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
+          for (int n = 0; n < NS; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
         if (ok && t0 < g.kv) {
-          float s2[MT][2][4] = {};  // odd steps: half the chain of dependent products
+          // at 16 tokens per warp the odd steps have sums of their own: half the chain of dependent products
+          constexpr int kChains = NS == 2 ? 2 : 1;
+          float s2[kChains == 2 ? MT : 1][2][4] = {};
 #pragma unroll
           for (int ks = 0; ks < KS; ks += 2) {
-            uint32_t bk[2][4];
+            uint32_t bk[2][NS / 2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              ldsm4(bk[x], kt + sw_off(kUnit, warp * 16 + (mi >> 1) * 8 + ri, (ks + x) * 2 + (mi & 1)));
+#pragma unroll
+              for (int n = 0; n < NS / 2; ++n)
+                ldsm4(bk[x][n], kt + sw_off(U, warp * TW + n * 16 + (mi >> 1) * 8 + ri, (ks + x) * 2 + (mi & 1)));
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
-              uint32_t af[2][4];
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
+                uint32_t af[4];
                 if constexpr (kHoldQ) {
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) af[x][i] = aq[t][ks + x][i];
+                  for (int i = 0; i < 4; ++i) af[i] = aq[t][ks + x][i];
                 } else {
-                  ldsm4(af[x], qb + t * 16 * Sh::kQRow + (ks + x) * 32);
+                  ldsm4(af, qb + t * 16 * Sh::kQRow + (ks + x) * 32);
+                }
+#pragma unroll
+                for (int n = 0; n < NS / 2; ++n) {
+                  if constexpr (kChains == 2) {
+                    mma16816<BF16>(x ? s2[t][0] : s[t][0], af, bk[x][n][0], bk[x][n][1]);
+                    mma16816<BF16>(x ? s2[t][1] : s[t][1], af, bk[x][n][2], bk[x][n][3]);
+                  } else {
+                    mma16816<BF16>(s[t][2 * n], af, bk[x][n][0], bk[x][n][1]);
+                    mma16816<BF16>(s[t][2 * n + 1], af, bk[x][n][2], bk[x][n][3]);
+                  }
                 }
               }
-              mma16816<BF16>(s[t][0], af[0], bk[0][0], bk[0][1]);
-              mma16816<BF16>(s[t][1], af[0], bk[0][2], bk[0][3]);
-              mma16816<BF16>(s2[t][0], af[1], bk[1][0], bk[1][1]);
-              mma16816<BF16>(s2[t][1], af[1], bk[1][2], bk[1][3]);
             }
           }
+          if constexpr (kChains == 2) {
 #pragma unroll
-          for (int t = 0; t < MT; ++t)
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+              for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s[t][n][i] += s2[t][n][i];
+                for (int i = 0; i < 4; ++i) s[t][n][i] += s2[t][n][i];
+          }
         }
         __syncwarp();
         if (ok && lane == 0) mbar_arrive(&empty[st]);
@@ -292,12 +305,12 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
       for (int t = 0; t < MT; ++t) {
         top[t][0] = top[t][1] = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NS; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             float& x = s[t][n][i];
             x *= a.scale_log2;
-            if (base + kUnit > lim_all) x = t0 + n * 8 + c2 + (i & 1) < lim[t][i >> 1] ? x : -INFINITY;
+            if (base + U > lim_all) x = t0 + n * 8 + c2 + (i & 1) < lim[t][i >> 1] ? x : -INFINITY;
             top[t][i >> 1] = fmaxf(top[t][i >> 1], x);
           }
         need |= top[t][0] > m[t][0] + kLazy || top[t][1] > m[t][1] + kLazy;
@@ -309,7 +322,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
           const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
           sum[t][0] = sum[t][1] = 0.f;
 #pragma unroll
-          for (int n = 0; n < 2; ++n) {
+          for (int n = 0; n < NS; ++n) {
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -318,7 +331,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-              asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(pb + sw_off(R, t * 16 + g8 + x * 8, warp * 2 + n) + c2 * 2),
+              asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(pb + sw_off(R, t * 16 + g8 + x * 8, warp * NS + n) + c2 * 2),
                            "r"(pack2<BF16>(w[2 * x], w[2 * x + 1]))
                            : "memory");
           }
@@ -368,15 +381,15 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
         l[t][0] += sum[t][0];
         l[t][1] += sum[t][1];
       }
-      // sums of D / 4 channels over all 64 tokens
+      // sums of D / 4 channels over all tokens of the unit
       {
         const int st = (e + 1) % ST;
         ok = warp_wait(&full[st], ((e + 1) / ST) & 1);
         const uint32_t vt = ring + st * Sh::kEntry;
         if (ok) {
-          constexpr int kGroup = D * MT <= 128 ? 4 : 2;  // steps whose operands are loaded together
+          constexpr int kGroup = D * MT <= 128 ? 4 : 2;  // steps of 16 tokens whose operands are loaded together
 #pragma unroll
-          for (int k0 = 0; k0 < 4; k0 += kGroup) {
+          for (int k0 = 0; k0 < U / 16; k0 += kGroup) {
             uint32_t ap[kGroup][MT][4], bv[kGroup][NP][4];
 #pragma unroll
             for (int j = 0; j < kGroup; ++j) {
@@ -385,9 +398,9 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
               for (int t = 0; t < MT; ++t) ldsm4(ap[j][t], pb + sw_off(R, t * 16 + (mi & 1) * 8 + ri, ks * 2 + (mi >> 1)));
 #pragma unroll
               for (int np = 0; np < NP; ++np)
-                ldsm4t(bv[j][np], vt + sw_off(kUnit, ks * 16 + (mi & 1) * 8 + ri, (warp * NP + np) * 2 + (mi >> 1)));
+                ldsm4t(bv[j][np], vt + sw_off(U, ks * 16 + (mi & 1) * 8 + ri, (warp * NP + np) * 2 + (mi >> 1)));
             }
-            if (g.kv < base + kUnit) {  // the unit that the sequence ends in: V rows behind it are zeroed (0 x NaN is NaN)
+            if (g.kv < base + U) {  // the unit that the sequence ends in: V rows behind it are zeroed (0 x NaN is NaN)
 #pragma unroll
               for (int j = 0; j < kGroup; ++j) {
                 const int n0 = g.kv - (base + (k0 + j) * 16 + c2), n1 = n0 - 8;
@@ -485,8 +498,8 @@ cudaError_t launch_type(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p,
 
 AttnShape attn_rows_shape(int d, int64_t rows, int sms) {
   const int tile = rows <= 16 ? 16 : 32;
-  const int ctas = sms * (d == 256 ? 1 : 2);
-  return {tile, kUnit, ctas, cta_bytes(tile, d), kTileCost, kMinPart};
+  const int ctas = sms * (d == 256 ? RowsShape<256, 1>::kCtas : RowsShape<128, 1>::kCtas);
+  return {tile, d == 64 ? RowsShape<64, 1>::U : RowsShape<128, 1>::U, ctas, cta_bytes(tile, d), kTileCost, kMinPart};
 }
 cudaError_t launch_attn_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {
   return dtype == TQ_BF16 ? launch_type<true>(a, m, p, d, s) : launch_type<false>(a, m, p, d, s);

@@ -9,9 +9,9 @@ namespace {
 // k_attn_tc: one CTA takes NT tiles of 128 rows (query, head of the group) of one request and KV head, and one
 // split of its tokens. The rows of a group share K and V, so a tile is full at any group size.
 //   - a TMA warp keeps a ring of K and V tiles (BN tokens) in flight, in the 128-byte swizzle;
-//   - an MMA warp per tile issues S_t = Q_t K^T into TMEM, and O_t += P_t V with P_t read from TMEM and V taken as it
-//     lies (tokens x channels, the MN-major operand form); with a warp per tile, neither tile's waits hold up the
-//     other's products;
+//   - two MMA warps issue S_t = Q_t K^T into TMEM, and O_t += P_t V with P_t read from TMEM and V taken as it lies
+//     (tokens x channels, the MN-major operand form): one per tile, or where there is one tile, one for the scores and
+//     one for the sums, so that one's waits do not hold up the other's products;
 //   - a warpgroup per tile reads S_t (a thread per row, so row sums need no exchange), writes P_t = 2^(s - m) in 16
 //     bits over it, and rescales O_t only where a row's maximum grew by more than 2^8: the weights stay below
 //     2^8, far inside fp32 and f16, and the final division takes the factor out.
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], NT);
+      mbar_init(&empty[i], NT);  // a commit by each warp that uses the entry
       mbar_init(&v_clean[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
@@ -161,9 +161,9 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], NT * 4 + 1 + NT);
+      mbar_init(&part_empty[i], NT * 4 + 3);
     }
-    mbar_init(drained, NT);
+    mbar_init(drained, 2);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -238,9 +238,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         if (!ok) err |= TQ_DEV_ERR_TIMEOUT;
       }
       if (err && a.status) atomicOr(a.status, err);
-    } else if (warp == kMmaWarp || (NT == 2 && warp == kMmaWarp1)) {
-      // ---- products of tile t ----
-      const int t = warp == kMmaWarp ? 0 : 1;
+    } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+      // ---- products of tile t, or of one tile its scores and its sums ----
+      const int t = NT == 2 && warp == kMmaWarp1;
+      const bool does_s = NT == 2 || warp == kMmaWarp, does_o = NT == 2 || warp == kMmaWarp1;
       const bool leader = elect_one();
       const uint32_t q_lo = umma_desc_sw128_lo(smem_u32(smem)) + t * (Sh::kQ >> 4), kv_lo = smem_u32(skv) >> 4;
       const uint32_t sd = tmem + t * 128, pa = tmem + Sh::kP + t * Sh::kPStep, od = tmem + Sh::kO + t * D;
@@ -275,13 +276,19 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         const int n_all = uniform(g.n_all), n = uniform(t == 0 ? g.n_of[0] : g.n_of[NT - 1]);
         const int kv = uniform(g.kv), u0 = uniform(g.u0);
         if (n_all == 0) continue;
-        if (n > 0) {
-          ok = warp_wait(&q_full[t], loaded & 1);
-          ++loaded;
+        if (does_s) {
+          if (n > 0) {
+            ok = warp_wait(&q_full[t], loaded & 1);
+            ++loaded;
+          }
+          scores(e, n > 0, made);
         }
-        scores(e, n > 0, made);
         for (int k = 0; k < n_all && ok; ++k, e += 2) {
-          if (Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1);
+          if (Sh::kOwnP && does_s && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1);
+          if (!does_o) {
+            made += k < n;
+            continue;
+          }
           const int vs = (e + 1) % ST;
           ok = ok && warp_wait(&full[vs], ((e + 1) / ST) & 1);
           if (!ok) break;
