@@ -40,7 +40,8 @@ struct AttnArgs {
   FastDiv div_g;             // by G
   int max_seqs, outer, tokens;   // max_seqs: padded: the outer size
   int most_kv;               // paged, padded: tokens of a request at most
-  int slope;                 // cost that each tile of a causal request has over the one before (tq_attention_line.cuh)
+  int slope, shift;          // cost that each tile of a causal request has over the one before, and the scale of costs
+                             // (tq_attention_line.cuh)
   int mode, causal;
   int max_rows;              // rows (query, head of the group) of a request and KV head at most
 };

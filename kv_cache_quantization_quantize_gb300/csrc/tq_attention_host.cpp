@@ -174,7 +174,16 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void*
   a.outer = kv.outer;
   a.tokens = kv.tokens;
   a.max_rows = (int)p.max_rows;
-  a.slope = a.causal ? std::max(1, p.tile_rows * 64 / (a.G * p.unit)) : 0;
+  // Costs are 64ths of a unit >> shift. The line's length is below tiles x (the longest tile's cost); the shift keeps
+  // that below 2^30. Launches that need one have lines of more than 2^30 / 64 units, and costs that much coarser.
+  const double slope = a.causal ? std::max(1, p.tile_rows * 64 / (a.G * p.unit)) : 0;
+  const double tiles = ((double)a.n_rows * a.G / p.tile_rows + a.batch) * a.hkv;
+  const double longest = (double)a.most_kv * 64 / p.unit + p.cost + 2 + slope * ((double)p.max_rows / p.tile_rows + 2);
+  a.shift = 0;
+  while (a.shift < 30 && tiles * (std::ldexp(longest, -a.shift) + 1) >= 1073741824.0) ++a.shift;
+  if (tiles * (std::ldexp(longest, -a.shift) + 1) >= 1073741824.0)
+    return fail(TQ_ERR_UNSUPPORTED, "batch x heads x rows: too many tiles for one launch");
+  a.slope = (int)slope >> a.shift;
   tq::AttnMaps m;
   e = tq::attn_tensor_map(kv, false, p.unit, &m.k);
   if (e == cudaSuccess) e = tq::attn_tensor_map(kv, true, p.unit, &m.v);
@@ -315,7 +324,7 @@ tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t
   a.kv_lens = d_kv_lens;
   a.kv_starts = d_kv_starts;
   a.max_seqs = kv->outer;
-  a.most_kv = kv->tokens;
+  a.most_kv = kv->tokens;  // packed: the most that one request can have
   return attend(q, kv, a, d_workspace, workspace_bytes, d_status, stream);
 }
 

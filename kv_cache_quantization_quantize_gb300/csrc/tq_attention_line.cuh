@@ -1,7 +1,8 @@
 // The split of the work of one attention launch, shared by both kernels.
 //
 // All tiles of all requests and KV heads lie on one line, in the order (request, head, tile); each takes as much of it
-// as it is estimated to cost, in 64ths of a unit: its tokens and a fixed cost for its start and end. CTA c takes
+// as it is estimated to cost, in 64ths of a unit (2^a.shift of them where a launch's line would pass 2^30): its tokens
+// and a fixed cost for its start and end. CTA c takes
 // [c Q, (c + 1) Q); a tile that is cut there has its units divided in proportion, and the parts are joined by
 // k_attn_join. So every SM gets the same amount of work whatever the lengths are, at most two cut tiles per CTA go
 // through memory, and the host needs no lengths. Costs have closed sums, so finding a place takes one pass over the
@@ -17,9 +18,9 @@ namespace {
 
 // A tile that begins in this CTA and ends in a later one.
 struct CutTile {
-  int64_t s, e, q;  // its place on the line, and Q
+  int32_t s, e, q;  // its place on the line, and Q
   int32_t units;    // 0: there is no such tile
-  int32_t f0, rows, h, q0, pad;
+  int32_t f0, rows, h, q0;
 };
 
 // What a CTA does of one tile, as its warps read it from a ring in shared memory that one warp fills. n_all < 0: no
@@ -36,8 +37,8 @@ constexpr int kParts = 4;
 
 // First unit of the part of a tile [s, e) that begins at place p of the line: (p - s) units / (e - s), in fp32 steps
 // that never fall with p (each rounding is monotone), so that neighbouring CTAs and the join, which compute it from the
-// same numbers, cut the tile alike. A 64-bit division would be several hundred cycles on the way to the first load.
-__device__ __forceinline__ int cut_at(int64_t p, int64_t s, int64_t e, int units) {
+// same numbers, cut the tile alike.
+__device__ __forceinline__ int cut_at(int p, int s, int e, int units) {
   if (p <= s) return 0;
   if (p >= e) return units;
   const float x = __fmul_rn(__fmul_rn((float)(p - s), (float)units), __frcp_rn((float)(e - s)));
@@ -46,8 +47,7 @@ __device__ __forceinline__ int cut_at(int64_t p, int64_t s, int64_t e, int units
 
 // Where a CTA starts: its part [p0, p1) of the line, and the tile that holds p0.
 struct LineStart {
-  int64_t p0, p1, s;
-  int b, h, t;
+  int p0, p1, s, b, h, t;
   Request r;
 };
 
@@ -55,8 +55,8 @@ struct LineStart {
 // that have units of their own (n_of).
 template <int T, int BN, int COST, int NT>
 struct Walk {
-  int64_t p0, p1, s, e;  // this CTA's part of the line, and the tile in hand
-  int64_t fixed;
+  int p0, p1, s, e;  // this CTA's part of the line, and the tile in hand
+  int fixed;         // cost of its first tile, but for the slope
   Request r;
   int b, h, t, nt, rows;
 
@@ -67,14 +67,15 @@ struct Walk {
     if (r.n_q * (int64_t)a.G > a.max_rows) err |= TQ_DEV_ERR_SPLITS;
     else rows = r.n_q * a.G;
     nt = (rows + T - 1) / T;
-    fixed = (int64_t)(a.causal ? max(0, r.kv - r.n_q) : r.kv) * 64 / BN + COST;
+    const int tokens = a.causal ? max(0, r.kv - r.n_q) : r.kv;
+    fixed = max(1, (int)(((uint32_t)tokens / (BN / 32) * 2 + COST) >> a.shift));
   }
   __device__ __forceinline__ void load(const AttnArgs& a, int request, uint32_t& err) {
     const Request found = find_request(a, request, err);
     take(a, request, found, err);
   }
-  __device__ __forceinline__ int64_t before(const AttnArgs& a, int tile) const {
-    return tile * fixed + a.slope * ((int64_t)tile * (tile + 1) / 2);
+  __device__ __forceinline__ int before(const AttnArgs& a, int tile) const {
+    return tile * fixed + a.slope * (int)((uint32_t)tile * (tile + 1) / 2);
   }
   // The tile in hand, or the first one of a later request.
   __device__ __forceinline__ void settle(const AttnArgs& a) {
@@ -89,7 +90,7 @@ struct Walk {
       }
       load(a, b + 1, err);
     }
-    e = s + fixed + (int64_t)a.slope * (t + 1);
+    e = s + fixed + a.slope * (t + 1);
   }
   __device__ __forceinline__ void start(const AttnArgs& a, const LineStart& st) {
     p0 = st.p0;
@@ -154,35 +155,35 @@ struct Walk {
 // This CTA's part of the line, into `st` in shared memory (as warp_sums, THREADS / 32 entries): prefix sums of the
 // requests' costs over the block. No CTA gets less than `least`. Bad requests are reported once, by CTA 0.
 template <typename W, int THREADS>
-__device__ __forceinline__ void find_start(const AttnArgs& a, int64_t least, LineStart& st, int64_t* warp_sums) {
+__device__ __forceinline__ void find_start(const AttnArgs& a, int least, LineStart& st, int* warp_sums) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   W w;
   uint32_t err = 0;
   const int per = (a.batch + THREADS - 1) / THREADS;
   const int lo = min(a.batch, (int)threadIdx.x * per), hi = min(a.batch, lo + per);
-  int64_t sum = 0;
+  int sum = 0;
   for (int b = lo; b < hi; ++b) {
     w.load(a, b, err);
     sum += a.hkv * w.before(a, w.nt);
   }
   if (blockIdx.x == 0 && err && a.status) atomicOr(a.status, err);
-  int64_t inc = sum;
+  int inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int64_t start = inc - sum, total = 0;
+  int start = inc - sum, total = 0;
 #pragma unroll
   for (int i = 0; i < THREADS / 32; ++i) {
     if (i < warp) start += warp_sums[i];
     total += warp_sums[i];
   }
   // an equal share, a millionth up so that no rounding leaves work over
-  const int64_t q = max(least, (int64_t)((float)total * __frcp_rn((float)gridDim.x) * 1.000001f) + 1);
-  const int64_t p0 = q * blockIdx.x, p1 = min(total, p0 + q);
+  const int q = max(max(1, least >> a.shift), (int)((float)total * __frcp_rn((float)gridDim.x) * 1.000001f) + 1);
+  const int p0 = min((int64_t)total, (int64_t)q * blockIdx.x), p1 = min((int64_t)total, (int64_t)p0 + q);
   if (threadIdx.x == 0) {
     st.p0 = p0;
     st.p1 = p1;
@@ -190,7 +191,7 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, int64_t least, Lin
   if (p0 >= start && p0 < start + sum) {  // one thread's requests hold p0
     for (int b = lo; b < hi; ++b) {
       if (per > 1) w.load(a, b, err);
-      const int64_t one = w.before(a, w.nt);
+      const int one = w.before(a, w.nt);
       if (p0 >= start + a.hkv * one) {
         start += a.hkv * one;
         continue;

@@ -17,7 +17,7 @@ namespace {
 // =============================================================================================
 constexpr int kRowsThreads = 160;  // four consumer warps, one producer warp
 constexpr int kTileCost = 64;      // start and end of a tile, as one unit
-constexpr int kMinPart = 192;      // no CTA gets less than this (3 units)
+constexpr int kMinPart = 128;      // no CTA gets less than a tile of one unit costs
 
 template <int D, int MT>
 struct RowsShape {
@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
   __shared__ alignas(8) uint64_t full[ST], empty[ST], q_full[2], q_empty[2], part_full[kParts], part_empty[kParts];
   __shared__ Part parts[kParts];
   __shared__ LineStart first;
-  __shared__ int64_t warp_sums[kRowsThreads / 32];
+  __shared__ int warp_sums[kRowsThreads / 32];
   __shared__ float sx[4][R];  // row maxima or sums of each warp
   __shared__ int gave_up;
 

@@ -25,7 +25,8 @@ struct TcShape {
   static constexpr int kStages = D == 64 ? 8 : 4;  // 128 KB of K and V in flight
   static constexpr int kThreads = kNT * 128 + 128;
   static constexpr int kQ = 128 * D * 2;           // bytes of a tile's queries
-  static constexpr int kSmem = 1024 + kNT * kQ + kStages * kTile + 512;
+  static constexpr int kStage = 4096;              // of a softmax warp, for its results on their way out
+  static constexpr int kSmem = 1024 + kNT * kQ + kStages * kTile + kNT * 4 * kStage + 512;
   // TMEM columns: S_t at t * 128, P_t at kP + t * kPStep, O_t at kO + t * D. At D = 128 they fill all 512 columns
   // with P_t over S_t, so that the next S_t waits for P_t's product; else P_t has a place of its own, and the next
   // S_t is made while the softmax works on this one.
@@ -100,7 +101,7 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
 }
 
 constexpr int kTileCost = 96;  // start and end of a tile, as 1.5 units
-constexpr int kMinPart = 320;  // no CTA gets less than this (5 units): short work takes fewer CTAs
+constexpr int kMinPart = 160;  // no CTA gets less than a tile of one unit costs: short work takes fewer CTAs
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* skv = smem + NT * Sh::kQ;
-  uint64_t* full = reinterpret_cast<uint64_t*>(skv + ST * kTile);
+  uint8_t* sout = skv + ST * kTile;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sout + NT * 4 * Sh::kStage);
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;       // per tile: queries are in shared memory
   // per tile and buffer of S and P (one barrier each, so that none is ever two phases ahead of a waiting warp):
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint64_t* part_empty = part_full + kParts;
   uint64_t* drained = part_empty + kParts;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drained + 1);
-  __shared__ int64_t warp_sums[Sh::kThreads / 32];
+  __shared__ int warp_sums[Sh::kThreads / 32];
   __shared__ Part parts[kParts];
   __shared__ LineStart first;
 
@@ -503,9 +505,18 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       // this one
       const bool direct = g.direct;
       const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-      uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(g.q0 + qi) * a.o_row +
-                      (int64_t)(g.h * a.G + (mine ? f - qi * a.G : 0)) * a.o_head;
-      float* po = cut_o<T, D>(a, gridDim.x, blockIdx.x, g.slot) + (size_t)(t * 128 + row_t) * D;
+      // eight rows of the warp's 32 per lane go out by this lane: row 4 i + lane / 8, 16 bytes of every 128
+      int64_t to_row[8];
+      uint32_t rows_out = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = (warp & 3) * 32 + i * 4 + (lane >> 3), fr = g.f0 + t * 128 + row;
+        if (fr < g.rows) rows_out |= 1u << i;
+        const int q = a.div_g(min(fr, g.rows - 1));
+        to_row[i] = direct ? (int64_t)(g.q0 + q) * a.o_row + (int64_t)(g.h * a.G + min(fr, g.rows - 1) - q * a.G) * a.o_head
+                           : (int64_t)(t * 128 + row) * D;
+      }
+      float* po = cut_o<T, D>(a, gridDim.x, blockIdx.x, g.slot);
       if (!direct) cut_ml<T>(a, gridDim.x, blockIdx.x, g.slot)[t * 128 + row_t] = make_float2(m, l);
       have = take(g);
       if (!ok) break;
@@ -515,27 +526,48 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         if (!ok) break;
         tc_fence_after();
       }
+      // Through shared memory, 128 bytes of each row at a time, so that a store of the warp covers four whole lines and
+      // not 16 bytes of 32 of them.
+      uint8_t* stage = sout + warp * Sh::kStage;
+      const int step = direct ? 64 : 32;  // columns: 16-bit results, fp32 sums
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        float o[32];
+      for (int c = 0; c < D; c += step) {
+        uint4 v[8];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (x == 1 && !direct) break;
+          float o[32];
+          __syncwarp();
+          if (n > 0) {
+            tmem_ld32_async(to + c + 32 * x, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * inv : 0.f;
+          if (direct) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              v[4 * x + i] = make_uint4(pack2<BF16>(o[8 * i], o[8 * i + 1]), pack2<BF16>(o[8 * i + 2], o[8 * i + 3]),
+                                        pack2<BF16>(o[8 * i + 4], o[8 * i + 5]), pack2<BF16>(o[8 * i + 6], o[8 * i + 7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                                __float_as_uint(o[4 * i + 3]));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(stage + lane * 128 + ((i ^ (lane & 7)) << 4)) = v[i];
         __syncwarp();
-        if (n > 0) {
-          tmem_ld32_async(to + c, o);
-          tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = i * 4 + (lane >> 3);
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+          if (!(rows_out >> i & 1)) continue;
+          if (direct) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to_row[i] + c + (lane & 7) * 8) = x;
+          else *reinterpret_cast<uint4*>(po + to_row[i] + c + (lane & 7) * 4) = x;
         }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = n > 0 ? o[i] * inv : 0.f;
-        if (!direct) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(po + c + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        } else if (mine) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 8)
-            *reinterpret_cast<uint4*>(dst + c + i) =
-                make_uint4(pack2<BF16>(o[i], o[i + 1]), pack2<BF16>(o[i + 2], o[i + 3]),
-                           pack2<BF16>(o[i + 4], o[i + 5]), pack2<BF16>(o[i + 6], o[i + 7]));
-        }
+        __syncwarp();
       }
       tc_fence_before();
     }
