@@ -40,6 +40,7 @@ struct AttnArgs {
   FastDiv div_g;             // by G
   int max_seqs, outer, tokens;   // max_seqs: padded: the outer size
   int most_kv;               // paged, padded: tokens of a request at most
+  int q_tma;                 // tensor-core kernel: queries come by TMA (their map is valid)
   int slope, shift;          // cost that each tile of a causal request has over the one before, and the scale of costs
                              // (tq_attention_line.cuh)
   int mode, causal;
@@ -133,11 +134,13 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 
 // ---- launchers ----
 struct AttnMaps {
-  CUtensorMap k, v;
+  CUtensorMap k, v, q;  // q: with AttnArgs::q_tma
 };
 // Tensor map of K or V for boxes of 64 channels x box_tokens tokens of one head, 128-byte swizzle: dimensions
 // {head_dim, tokens, heads, outer}.
 cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m);
+// Tensor map of the queries for boxes of 64 channels x the G heads of a group x 128 / G queries: 128 rows of a tile.
+cudaError_t query_tensor_map(const tq_queries& q, int head_dim, int dtype, int G, CUtensorMap* m);
 // A kernel's tiles and launch: rows (query, head of the group) of a tile, tokens of a unit, CTAs at most, bytes of
 // workspace per CTA; a tile's fixed cost and the least work of a CTA (tq_attention_line.cuh).
 struct AttnShape {

@@ -11,7 +11,9 @@
 
 namespace tq {
 
-cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m) {
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -19,7 +21,23 @@ cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtens
     return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn)
                                                                 : nullptr;
   }();
+  return encode;
+}
+
+cudaError_t encode_map(CUtensorMap* m, int dtype, int rank, void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box) {
+  const auto encode = encoder();
   if (!encode) return cudaErrorNotSupported;
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(m, dtype == TQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                            base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m) {
   const int64_t* st = values ? kv.v_strides : kv.k_strides;
   void* base = values ? kv.v : kv.k;
   const cuuint64_t d = (cuuint64_t)kv.head_dim;
@@ -29,11 +47,16 @@ cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtens
   auto bytes = [&](cuuint64_t n, int64_t stride) { return n > 1 ? (cuuint64_t)stride * 2 : d * 2; };
   const cuuint64_t strides[3] = {bytes(tokens, st[1]), bytes(dims[2], st[2]), bytes(outer, st[0])};
   const cuuint32_t box[4] = {64, (cuuint32_t)box_tokens, 1, 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = encode(m, kv.dtype == TQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
-                            base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode_map(m, kv.dtype, 4, base, dims, strides, box);
+}
+
+cudaError_t query_tensor_map(const tq_queries& q, int head_dim, int dtype, int G, CUtensorMap* m) {
+  const cuuint64_t d = (cuuint64_t)head_dim;
+  const cuuint64_t dims[3] = {d, (cuuint64_t)q.n_q_heads, (cuuint64_t)q.n_rows};
+  auto bytes = [&](cuuint64_t n, int64_t stride) { return n > 1 ? (cuuint64_t)stride * 2 : d * 2; };
+  const cuuint64_t strides[2] = {bytes(dims[1], q.q_strides[1]), bytes(dims[2], q.q_strides[0])};
+  const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)(128 / G)};
+  return encode_map(m, dtype, 3, const_cast<void*>(q.q), dims, strides, box);
 }
 
 }  // namespace tq
@@ -184,9 +207,15 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void*
   if (tiles * (std::ldexp(longest, -a.shift) + 1) >= 1073741824.0)
     return fail(TQ_ERR_UNSUPPORTED, "batch x heads x rows: too many tiles for one launch");
   a.slope = (int)slope >> a.shift;
-  tq::AttnMaps m;
+  tq::AttnMaps m = {};
   e = tq::attn_tensor_map(kv, false, p.unit, &m.k);
   if (e == cudaSuccess) e = tq::attn_tensor_map(kv, true, p.unit, &m.v);
+  // a tile's 128 rows are whole queries where the group's size divides 128; strides as TMA takes them
+  auto fits = [](int64_t n, int64_t stride) { return n <= 1 || (stride > 0 && stride < (int64_t)1 << 38); };
+  if (p.tc && 128 % a.G == 0 && fits(a.hq, a.q_head) && fits(a.n_rows, a.q_row)) {
+    a.q_tma = 1;
+    if (e == cudaSuccess) e = tq::query_tensor_map(*q, kv.head_dim, kv.dtype, a.G, &m.q);
+  }
   if (e == cudaSuccess)
     e = p.tc ? tq::launch_attn_tc(a, m, p, kv.head_dim, kv.dtype, (cudaStream_t)stream)
              : tq::launch_attn_rows(a, m, p, kv.head_dim, kv.dtype, (cudaStream_t)stream);

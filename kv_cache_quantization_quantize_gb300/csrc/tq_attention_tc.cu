@@ -73,6 +73,13 @@ __device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, float* r) {
         "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]), "=f"(r[30]), "=f"(r[31])
       : "r"(taddr));
 }
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          smem_u32(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 // Shared-memory writes of this thread become visible to the async proxy (TMA, MMA operands).
@@ -106,7 +113,7 @@ constexpr int kMinPart = 160;  // no CTA gets less than a tile of one unit costs
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     k_attn_tc(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
-              const __grid_constant__ CUtensorMap map_v) {
+              const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q) {
   using Sh = TcShape<D>;
   constexpr int NT = Sh::kNT, BN = Sh::kBN, ST = Sh::kStages, T = 128 * NT;
   using W = Walk<T, BN, kTileCost, NT>;
@@ -122,9 +129,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sout + NT * 4 * Sh::kStage);
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;       // per tile: queries are in shared memory
+  uint64_t* q_empty = q_full + NT;     // per tile: their last scores are made (q_tma)
   // per tile and buffer of S and P (one barrier each, so that none is ever two phases ahead of a waiting warp):
   constexpr int NB = NT * Sh::kBufs;
-  uint64_t* s_full = q_full + NT;      // scores are in TMEM
+  uint64_t* s_full = q_empty + NT;     // scores are in TMEM
   uint64_t* p_full = s_full + NB;      // and half of the unit: weights are in TMEM, O is rescaled
   uint64_t* o_full = p_full + 2 * NB;  // the product with V is done
   uint64_t* s_free = o_full + NB;      // the softmax has read the scores (kOwnP)
@@ -143,6 +151,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   if (threadIdx.x == 32) {
     prefetch_map(&map_k);
     prefetch_map(&map_v);
+    if (a.q_tma) prefetch_map(&map_q);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -151,7 +160,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       mbar_init(&v_clean[i], 1);
     }
     for (int i = 0; i < NT; ++i) {
-      mbar_init(&q_full[i], 4);
+      mbar_init(&q_full[i], a.q_tma ? 1 : 4);
+      mbar_init(&q_empty[i], 1);
       mbar_init(&turn[i], 4);
     }
     for (int i = 0; i < NB; ++i) {
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       uint32_t cleaned = 0;  // parities of v_clean: an entry is cleaned again only after this warp gave it back
       // S_t = Q_t K^T of unit j from ring entry `entry`, or nothing; the entry is given back either way, once it has been
       // filled. Where S_t goes, the scores of unit j - kBufs have been read, and with P_t over them, used.
-      auto scores = [&](int entry, bool wanted, int j) {
+      auto scores = [&](int entry, bool wanted, int j, bool last) {
         const int st = entry % ST, before = j - Sh::kBufs;
         ok = ok && warp_wait(&full[st], (entry / ST) & 1);
         if (wanted && before >= 0)
@@ -269,6 +279,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               umma_bf16_lo(sd + buf_of(j) * 64, q_lo + (i >> 2) * 1024 + step, ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
             }
             umma_commit(&s_full[t * Sh::kBufs + buf_of(j)]);
+            if (last && a.q_tma) umma_commit(&q_empty[t]);
           }
           umma_commit(&empty[st]);
         }
@@ -283,10 +294,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
             ok = warp_wait(&q_full[t], loaded & 1);
             ++loaded;
           }
-          scores(e, n > 0, made);
+          scores(e, n > 0, made, n == 1);
         }
         for (int k = 0; k < n_all && ok; ++k, e += 2) {
-          if (Sh::kOwnP && does_s && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1);
+          if (Sh::kOwnP && does_s && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1, k + 2 == n);
           if (!does_o) {
             made += k < n;
             continue;
@@ -332,7 +343,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
             ++made;
           }
           if (leader) umma_commit(&empty[vs]);
-          if (!Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, made);
+          if (!Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, made, k + 2 == n);
         }
       }
       // leave only when every product is done
@@ -344,6 +355,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       W w;
       w.start(a, first);
       CutTile cut = {};
+      int loads[NT] = {};
       for (bool more = true; more;) {
         Part g = {};
         more = w.next(a, g, cut);
@@ -353,7 +365,26 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         parts[i] = g;
         mbar_arrive(&part_full[i]);
         ++at;
+        // its queries, once the last scores with the ones before them are made; rows past the last are other requests'
+        // or zeros: their results are not written
+        if (more && a.q_tma) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (g.n_of[t] == 0) continue;
+            if (loads[t] > 0) ok = ok && mbar_wait(&q_empty[t], (loads[t] - 1) & 1);
+            if (!ok) break;
+            mbar_expect_tx(&q_full[t], Sh::kQ);
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem + t * Sh::kQ + c * 16384, &map_q, c * 64, g.h * a.G, g.q0 + a.div_g(g.f0 + t * 128), &q_full[t]);
+            ++loads[t];
+          }
+          if (!ok) break;
+        }
       }
+      // leave only when every copy has landed
+      for (int t = 0; t < NT; ++t)
+        if (loads[t] > 0) ok &= mbar_wait(&q_full[t], (loads[t] - 1) & 1);
       cut_tiles(a)[blockIdx.x] = cut;
       if (!ok && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
     }
@@ -367,9 +398,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     int made = 0;
     int turns = 0;  // units that both tiles have made
     Part g = {};
-    // a part's queries into shared memory, as a K-major operand; rows past the last are zero
+    // a part's queries into shared memory, as a K-major operand, where they do not come by TMA (group sizes such as 3 or
+    // 6); rows past the last are zero
     auto load_q = [&] {
-      if ((t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
+      if (a.q_tma || (t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
       constexpr int kBatch = D == 64 ? 8 : 16;
       constexpr int kChunks = D / 8, kRowsStep = 128 / kChunks;  // 16-byte chunks of a row; rows of one step
       const int c = row_t % kChunks;
@@ -410,7 +442,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const int lim_all = seen(a, r, a.div_g(min(g.f0 + t * 128, g.rows - 1)));
       const int u0 = g.u0;
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
-      float m = -INFINITY, l = 0.f;
+      float m = mine ? -INFINITY : INFINITY, l = 0.f;  // a row past the last never outgrows its maximum
       for (int k = 0; k < n; ++k) {
         const int bi = t * Sh::kBufs + buf_of(made);
         ok = warp_wait(&s_full[bi], turn_of(made));
@@ -586,7 +618,7 @@ cudaError_t launch_tc_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p
   static std::atomic<uint64_t> known{0};
   cudaError_t e = allow_smem(k_attn_tc<D, BF16>, Sh::kSmem, known);
   if (e == cudaSuccess)
-    e = launch_pdl(k_attn_tc<D, BF16>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, m.k, m.v);
+    e = launch_pdl(k_attn_tc<D, BF16>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, m.k, m.v, m.q);
   if (e != cudaSuccess) return e;
   return launch_join<D, 128 * Sh::kNT, BF16>(a, p.ctas, p.max_rows, s);
 }
