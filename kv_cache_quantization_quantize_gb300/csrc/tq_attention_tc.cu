@@ -107,8 +107,8 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-constexpr int kTileCost = 96;  // start and end of a tile, as 1.5 units
-constexpr int kMinPart = 160;  // no CTA gets less than a tile of one unit costs: short work takes fewer CTAs
+constexpr int kTileCost = 192;  // start and end of a tile, as 3 units
+constexpr int kMinPart = 256;   // no CTA gets less than a tile of one unit costs: short work takes fewer CTAs
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
