@@ -36,99 +36,117 @@ _QUERIES = struct.Struct("@PP4qP5if")  # tq_queries
 _STRIDES = struct.Struct("@2q")
 
 
+_I32 = torch.int32
+_HALVES = (torch.bfloat16, torch.float16)
+
+
 class _On:
-    """The device and raw stream of a call. Outputs made inside belong to that stream; the caller's tensors are
-    recorded on it where it is not the current one."""
+    """The device and stream of a call that is not made on the current ones: outputs made inside belong to that stream, and
+    the caller's tensors are recorded on it."""
 
-    __slots__ = ("raw", "_device", "_stream")
+    __slots__ = ("_device", "_stream")
 
-    def __init__(self, device, stream, *tensors):
-        index = device.index
-        self._device = torch.cuda.device(index) if torch.cuda.current_device() != index else None
-        self._stream = None
-        if stream is None:
-            self.raw = torch._C._cuda_getCurrentRawStream(index)
-        else:
-            if stream.device != device:
-                raise ValueError(f"stream of {stream.device}, tensors on {device}")
-            self.raw = stream.cuda_stream
-            if self.raw != torch._C._cuda_getCurrentRawStream(index):
-                self._stream = torch.cuda.stream(stream)
-                for t in tensors:
-                    if t is not None:
-                        t.record_stream(stream)
+    def __init__(self, index, stream, tensors):
+        self._device = torch.cuda.device(index)
+        self._stream = stream
+        if stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+            self._stream = torch.cuda.stream(stream)
 
     def __enter__(self):
-        if self._device is not None:
-            self._device.__enter__()
+        self._device.__enter__()
         if self._stream is not None:
             self._stream.__enter__()
-        return self
 
     def __exit__(self, *exc):
         if self._stream is not None:
             self._stream.__exit__(*exc)
-        if self._device is not None:
-            self._device.__exit__(*exc)
+        self._device.__exit__(*exc)
 
 
-def _ints(name, t, device, n=None):
+def _here(index, stream, tensors):
+    """(raw stream, context or None) of a call on device `index`; no context where all is current."""
+    current = torch._C._cuda_getDevice() == index
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        return raw, None if current else _On(index, None, ())
+    if stream.device.index != index:
+        raise ValueError(f"stream of {stream.device}, tensors on cuda:{index}")
+    if stream.cuda_stream == raw:
+        return raw, None if current else _On(index, None, ())
+    return stream.cuda_stream, _On(index, stream, tensors)
+
+
+def _ints(name, t, index, n=0):
     """The address of a contiguous int32 vector on the device, with at least n entries."""
-    if t.dtype is not torch.int32 or t.device != device or t.dim() != 1 or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous int32 vector on {device}")
-    if n is not None and t.shape[0] < n:
-        raise ValueError(f"{name}: {t.shape[0]} entries, {n} are needed")
-    return t.data_ptr()
+    if t.dtype is _I32 and t.get_device() == index and t.dim() == 1 and t.is_contiguous() and t.shape[0] >= n:
+        return t.data_ptr()
+    if t.dtype is not _I32 or t.get_device() != index or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 vector on cuda:{index}")
+    raise ValueError(f"{name}: {t.shape[0]} entries, {n} are needed")
 
 
-def _optional(name, t, device, n=None):
-    return None if t is None else _ints(name, t, device, n)
+def _table(table, index):
+    """(address, max_seqs, max_pages, row stride) of a block table."""
+    if table.dtype is _I32 and table.dim() == 2 and table.get_device() == index >= 0:
+        rows, pages = table.shape
+        stride, one = table.stride()
+        if rows and pages and one == 1:
+            return table.data_ptr(), rows, pages, stride if rows > 1 or stride > pages else pages
+    raise ValueError("table: expected int32 [max_seqs, max_pages] with contiguous rows on the others' CUDA device")
 
 
-def _cuda(name, t):
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    return t.device
-
-
-def _table(table, free, n_free):
-    device = _cuda("table", table)
-    if table.dtype is not torch.int32 or table.dim() != 2 or not table.shape[0] or not table.shape[1] or table.stride(1) != 1:
-        raise ValueError("table: expected int32 [max_seqs, max_pages] with contiguous rows")
-    stride = table.stride(0) if table.shape[0] > 1 else max(table.stride(0), table.shape[1])
-    return device, (table.data_ptr(), table.shape[0], table.shape[1], stride, _ints("free", free, device, 1), free.shape[0],
-                    _ints("n_free", n_free, device, 1))
+def _map_args(table, free, n_free):
+    index = table.get_device()
+    return index, (*_table(table, index), _ints("free", free, index, 1), free.shape[0], _ints("n_free", n_free, index, 1))
 
 
 def map_blocks(table, free, n_free, seq_ids, lens, n_new, max_tokens, out=None, status=None, stream=None):
     """Blocks and slots of a step's new tokens (tq_blocks_map): (slots [max_tokens], starts [batch + 1],
     totals [batch]), int32. table, free and n_free are changed in place. out: the three tensors to write instead."""
-    device, args = _table(table, free, n_free)
+    index, args = _map_args(table, free, n_free)
     batch = seq_ids.shape[0]
-    ids = (_ints("seq_ids", seq_ids, device), _ints("lens", lens, device, batch), _ints("n_new", n_new, device, batch))
-    word = _optional("status", status, device, 1)
-    with _On(device, stream, table, free, n_free, seq_ids, lens, n_new, status, *(out or ())) as on:
-        if out is None:
-            # one allocation: [slots | starts | totals], each part 16-byte aligned
-            a = (max(max_tokens, 0) + 3) & ~3
-            b = a + ((batch + 4) & ~3)
-            buf = torch.empty(b + batch, dtype=torch.int32, device=device)
-            out = (buf[:max(max_tokens, 0)], buf[a:a + batch + 1], buf[b:])
+    ids = (_ints("seq_ids", seq_ids, index), _ints("lens", lens, index, batch), _ints("n_new", n_new, index, batch))
+    word = None if status is None else _ints("status", status, index, 1)
+    raw, on = _here(index, stream, (table, free, n_free, seq_ids, lens, n_new, status, *(out or ())))
+    if on is not None:
+        with on:
+            return _map_blocks(args, ids, batch, max_tokens, out, word, raw, index, table.device)
+    return _map_blocks(args, ids, batch, max_tokens, out, word, raw, index, table.device)
+
+
+def _map_blocks(args, ids, batch, max_tokens, out, word, raw, index, device):
+    if out is None:
+        # one allocation: [slots | starts | totals], each part 16-byte aligned
+        n = max(max_tokens, 0)
+        a = (n + 3) & ~3
+        b = a + ((batch + 4) & ~3)
+        buf = torch.empty(b + batch, dtype=_I32, device=device)
+        at = buf.data_ptr()
+        places = (at + 4 * a, at + 4 * b, at)
+        out = (buf.as_strided((n,), (1,)), buf.as_strided((batch + 1,), (1,), a), buf.as_strided((batch,), (1,), b))
+    else:
         slots, starts, totals = out
-        check(load().tq_blocks_map(*args, *ids, batch, _ints("starts", starts, device, batch + 1),
-                                   _ints("totals", totals, device, batch), _ints("slots", slots, device, max_tokens), max_tokens,
-                                   word, on.raw))
-    return slots, starts, totals
+        places = (_ints("starts", starts, index, batch + 1), _ints("totals", totals, index, batch), _ints("slots", slots, index, max_tokens))
+    check(load().tq_blocks_map(*args, *ids, batch, *places, max_tokens, word, raw))
+    return out
 
 
 def release_blocks(table, free, n_free, seq_ids, keep=None, status=None, stream=None):
     """Gives back the blocks behind each request's first keep[b] tokens, all of them without keep (tq_blocks_release)."""
-    device, args = _table(table, free, n_free)
+    index, args = _map_args(table, free, n_free)
     batch = seq_ids.shape[0]
-    ids = (_ints("seq_ids", seq_ids, device), _optional("keep", keep, device, batch))
-    word = _optional("status", status, device, 1)
-    with _On(device, stream, table, free, n_free, seq_ids, keep, status) as on:
-        check(load().tq_blocks_release(*args, *ids, batch, word, on.raw))
+    ids = _ints("seq_ids", seq_ids, index)
+    kept = None if keep is None else _ints("keep", keep, index, batch)
+    word = None if status is None else _ints("status", status, index, 1)
+    raw, on = _here(index, stream, (table, free, n_free, seq_ids, keep, status))
+    if on is not None:
+        with on:
+            check(load().tq_blocks_release(*args, ids, kept, batch, word, raw))
+    else:
+        check(load().tq_blocks_release(*args, ids, kept, batch, word, raw))
 
 
 def _kv(k, v, outer, tokens, heads, d, k_strides, v_strides):
@@ -136,58 +154,73 @@ def _kv(k, v, outer, tokens, heads, d, k_strides, v_strides):
 
 
 def _pools(k_pool, v_pool):
-    device = _cuda("k_pool", k_pool)
-    if (k_pool.dim() != 4 or k_pool.shape[1] != PAGE or k_pool.shape != v_pool.shape or k_pool.dtype is not v_pool.dtype
-            or k_pool.dtype not in (torch.bfloat16, torch.float16) or v_pool.device != device):
+    """(device index, tq_kv, head_dim, heads, type) of a pool."""
+    shape, dtype, index = k_pool.shape, k_pool.dtype, k_pool.get_device()
+    if index < 0:
+        raise ValueError("k_pool: expected a CUDA tensor")
+    if (len(shape) != 4 or shape[1] != PAGE or shape != v_pool.shape or dtype is not v_pool.dtype or dtype not in _HALVES
+            or v_pool.get_device() != index):
         raise ValueError("k_pool, v_pool: expected two bf16 or f16 tensors [n_blocks, 128, n_kv_heads, head_dim] on one device")
     ks, vs = k_pool.stride(), v_pool.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("k_pool, v_pool: the channels of a head have to be contiguous")
-    blocks, _, heads, d = k_pool.shape
-    return device, _kv(k_pool, v_pool, blocks, PAGE, heads, d, ks[:3], vs[:3])
+    return index, _kv(k_pool, v_pool, shape[0], PAGE, shape[2], shape[3], ks[:3], vs[:3]), shape[3], shape[2], dtype
 
 
 def append(k, v, k_pool, v_pool, slots, status=None, stream=None):
     """Writes k, v [tokens, n_kv_heads, head_dim] (bf16, f16 or f32, any strides with contiguous channels) into the pools
     [n_blocks, 128, n_kv_heads, head_dim] at `slots` (tq_paged_append; -1 skips a row)."""
-    device, pool = _pools(k_pool, v_pool)
-    if (k.dim() != 3 or k.shape != v.shape or k.dtype is not v.dtype or k.dtype not in _DTYPES or k.device != device
-            or v.device != device or k.shape[1:] != k_pool.shape[2:]):
+    index, pool, d, heads, _ = _pools(k_pool, v_pool)
+    shape, dtype = k.shape, k.dtype
+    if (len(shape) != 3 or shape != v.shape or dtype is not v.dtype or dtype not in _DTYPES or k.get_device() != index
+            or v.get_device() != index or shape[1] != heads or shape[2] != d):
         raise ValueError("k, v: expected two tensors [tokens, n_kv_heads, head_dim] of one type that fit the pools")
     ks, vs = k.stride(), v.stride()
     if ks[2] != 1 or vs[2] != 1:
         raise ValueError("k, v: the channels of a head have to be contiguous")
-    n = k.shape[0]
-    with _On(device, stream, k, v, k_pool, v_pool, slots, status) as on:
-        check(load().tq_paged_append(pool, k.data_ptr(), v.data_ptr(), _DTYPES[k.dtype], _STRIDES.pack(ks[0], ks[1]),
-                                     _STRIDES.pack(vs[0], vs[1]), _ints("slots", slots, device, n), n,
-                                     _optional("status", status, device, 1), on.raw))
+    n = shape[0]
+    args = (pool, k.data_ptr(), v.data_ptr(), _DTYPES[dtype], _STRIDES.pack(ks[0], ks[1]), _STRIDES.pack(vs[0], vs[1]),
+            _ints("slots", slots, index, n), n, None if status is None else _ints("status", status, index, 1))
+    raw, on = _here(index, stream, (k, v, k_pool, v_pool, slots, status))
+    if on is not None:
+        with on:
+            check(load().tq_paged_append(*args, raw))
+    else:
+        check(load().tq_paged_append(*args, raw))
 
 
-def _attend(q, dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv, call):
-    if q.dim() != 3 or q.dtype is not dtype or q.device != device or q.shape[2] != d or q.shape[1] % heads or not q.shape[1]:
-        raise ValueError(f"q: expected a {dtype} tensor [rows, a multiple of {heads} heads, {d}] on {device}")
+def _attend(q, dtype, heads, d, index, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, stream, tensors, call):
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not dtype or q.get_device() != index or shape[2] != d or shape[1] % heads or not shape[1]:
+        raise ValueError(f"q: expected a {dtype} tensor [rows, a multiple of {heads} heads, {d}] on cuda:{index}")
+    batch = q_starts.shape[0] - 1
+    if batch < 0:
+        raise ValueError("q_starts: expected [batch + 1] entries")
+    raw, on = _here(index, stream, (q, q_starts, out, workspace, *tensors))
+    if on is not None:
+        with on:
+            return _attend_here(q, shape, dtype, index, batch, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, raw, call)
+    return _attend_here(q, shape, dtype, index, batch, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, raw, call)
+
+
+def _attend_here(q, shape, dtype, index, batch, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, raw, call):
     if out is None:
-        # rows behind the last request are not written
-        out = torch.empty(q.shape, dtype=dtype, device=device)
-    elif out.shape != q.shape or out.dtype is not dtype or out.device != device:
+        out = torch.empty(shape, dtype=dtype, device=q.device)  # rows behind the last request are not written
+    elif out.shape != shape or out.dtype is not dtype or out.get_device() != index:
         raise ValueError("out: expected a tensor of q's shape, type and device")
     qs, os = q.stride(), out.stride()
     if qs[2] != 1 or os[2] != 1:
         raise ValueError("q, out: the channels of a head have to be contiguous")
-    batch = q_starts.shape[0] - 1
-    if batch < 0:
-        raise ValueError("q_starts: expected [batch + 1] entries")
-    queries = _QUERIES.pack(q.data_ptr(), out.data_ptr(), qs[0], qs[1], os[0], os[1], _ints("q_starts", q_starts, device), q.shape[0],
-                            q.shape[1], batch, max_q, max_kv, softmax_scale)
+    queries = _QUERIES.pack(q.data_ptr(), out.data_ptr(), qs[0], qs[1], os[0], os[1], _ints("q_starts", q_starts, index), shape[0], shape[1],
+                            batch, max_q, max_kv, softmax_scale)
     if workspace is None:
         n = load().tq_attention_workspace_bytes(queries, kv)
         if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on {device}")
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    call(queries, *ws, batch, on.raw)
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{index}")
+    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    check(call(queries, kv, batch, ws, size, raw))
     return out
 
 
@@ -198,7 +231,7 @@ def attention_workspace_bytes(q, k, max_q=0, max_kv=0, batch=1):
     dims = (1, k.shape[0]) if k.dim() == 3 else tuple(k.shape[:2])
     kv = _kv(k, k, *dims, k.shape[-2], k.shape[-1], (0, 0, 0) if k.dim() == 3 else s[:3], (0, 0, 0))
     queries = _QUERIES.pack(0, 0, 0, 0, 0, 0, 0, q.shape[0], q.shape[1], batch, max_q, max_kv, 0.0)
-    with _On(_cuda("q", q), None):
+    with torch.cuda.device(q.device):
         return load().tq_attention_workspace_bytes(queries, kv)
 
 
@@ -210,20 +243,16 @@ def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True,
     tokens with the new ones, in the pages of table row seq_ids[b] (None: row b). max_q: no request has more rows (0:
     unknown; few rows take a kernel of their own); max_kv: no request has more tokens (0: unknown; short calls launch fewer
     CTAs). Returns out, of q's shape; rows behind the last request stay as they are."""
-    device, kv = _pools(k_pool, v_pool)
-    if table.dtype is not torch.int32 or table.dim() != 2 or table.device != device or not table.shape[0] or not table.shape[1] or table.stride(1) != 1:
-        raise ValueError(f"table: expected int32 [max_seqs, max_pages] with contiguous rows on {device}")
-    max_seqs, max_pages = table.shape
-    stride = table.stride(0) if max_seqs > 1 else max(table.stride(0), max_pages)
-    word = _optional("status", status, device, 1)
+    index, kv, d, heads, dtype = _pools(k_pool, v_pool)
+    pages = _table(table, index)
+    word = None if status is None else _ints("status", status, index, 1)
 
-    def call(queries, ws, ws_bytes, batch, raw):
-        check(load().tq_paged_attention(queries, kv, table.data_ptr(), max_seqs, max_pages, stride, _optional("seq_ids", seq_ids, device, batch),
-                                        _ints("kv_lens", kv_lens, device, batch), 1 if causal else 0, ws, ws_bytes, word, raw))
+    def call(queries, kv, batch, ws, size, raw):
+        return load().tq_paged_attention(queries, kv, *pages, None if seq_ids is None else _ints("seq_ids", seq_ids, index, batch),
+                                         _ints("kv_lens", kv_lens, index, batch), 1 if causal else 0, ws, size, word, raw)
 
-    with _On(device, stream, q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, out, workspace, status) as on:
-        return _attend(q, k_pool.dtype, k_pool.shape[2], k_pool.shape[3], device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv,
-                       call)
+    return _attend(q, dtype, heads, d, index, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, stream,
+                   (k_pool, v_pool, table, seq_ids, kv_lens, status), call)
 
 
 def cross_attention(q, k, v, q_starts, kv_lens=None, kv_starts=None, softmax_scale=0.0, max_q=0, max_kv=0, out=None, workspace=None,
@@ -231,30 +260,32 @@ def cross_attention(q, k, v, q_starts, kv_lens=None, kv_starts=None, softmax_sca
     """Attention of q [rows, n_q_heads, head_dim] to an encoder's states (tq_cross_attention): packed k, v [states,
     n_kv_heads, head_dim] with kv_starts [batch + 1], or padded ones [batch, states, n_kv_heads, head_dim] with kv_lens
     [batch]. Every state of a request is visible to all its queries; a request without states gets zeros."""
-    device = _cuda("k", k)
-    if k.shape != v.shape or k.dtype is not v.dtype or k.dtype not in (torch.bfloat16, torch.float16) or v.device != device or k.dim() not in (3, 4):
+    shape, dtype, index = k.shape, k.dtype, k.get_device()
+    if index < 0:
+        raise ValueError("k: expected a CUDA tensor")
+    if shape != v.shape or dtype is not v.dtype or dtype not in _HALVES or v.get_device() != index or len(shape) not in (3, 4):
         raise ValueError("k, v: expected two bf16 or f16 tensors [states, n_kv_heads, head_dim] or [batch, states, n_kv_heads, head_dim]")
-    packed = k.dim() == 3
+    packed = len(shape) == 3
     if packed != (kv_starts is not None) or packed == (kv_lens is not None):
         raise ValueError("packed states take kv_starts, padded ones take kv_lens")
     ks, vs = k.stride(), v.stride()
     if ks[-1] != 1 or vs[-1] != 1:
         raise ValueError("k, v: the channels of a head have to be contiguous")
-    heads, d = k.shape[-2:]
+    heads, d = shape[-2:]
     if not heads:
         raise ValueError("k, v: no heads")
     if packed:
-        kv = _kv(k, v, 1, k.shape[0], heads, d, (0, ks[0], ks[1]), (0, vs[0], vs[1]))
+        kv = _kv(k, v, 1, shape[0], heads, d, (0, ks[0], ks[1]), (0, vs[0], vs[1]))
     else:
-        kv = _kv(k, v, k.shape[0], k.shape[1], heads, d, ks[:3], vs[:3])
-    word = _optional("status", status, device, 1)
+        kv = _kv(k, v, shape[0], shape[1], heads, d, ks[:3], vs[:3])
+    word = None if status is None else _ints("status", status, index, 1)
 
-    def call(queries, ws, ws_bytes, batch, raw):
-        check(load().tq_cross_attention(queries, kv, _optional("kv_starts", kv_starts, device, batch + 1), _optional("kv_lens", kv_lens, device, batch),
-                                        ws, ws_bytes, word, raw))
+    def call(queries, kv, batch, ws, size, raw):
+        return load().tq_cross_attention(queries, kv, _ints("kv_starts", kv_starts, index, batch + 1) if packed else None,
+                                         None if packed else _ints("kv_lens", kv_lens, index, batch), ws, size, word, raw)
 
-    with _On(device, stream, q, k, v, q_starts, kv_lens, kv_starts, out, workspace, status) as on:
-        return _attend(q, k.dtype, heads, d, device, q_starts, max_q, max_kv, softmax_scale, out, workspace, on, kv, call)
+    return _attend(q, dtype, heads, d, index, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, stream,
+                   (k, v, kv_lens, kv_starts, status), call)
 
 
 class BlockPool:
