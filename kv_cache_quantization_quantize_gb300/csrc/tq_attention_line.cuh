@@ -98,7 +98,9 @@ struct Walk {
     b = a.batch;
     t = nt = h = 0;
     s = p1;
-    if (p0 >= p1) return;
+    // (starts that fall can give requests more rows together than there are, and sums past 32 bits: then nobody may have
+    // found p0, and some outputs stay unwritten)
+    if (p0 >= p1 || st.b >= a.batch) return;
     uint32_t err = 0;
     take(a, st.b, st.r, err);
     h = st.h;
@@ -174,6 +176,7 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, int least, LineSta
     if (lane >= o) inc += v;
   }
   if (lane == 31) warp_sums[warp] = inc;
+  if (threadIdx.x == 0) st.b = a.batch;
   __syncthreads();
   int start = inc - sum, total = 0;
 #pragma unroll
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(JoinShape<T>::kWarps * 32) k_attn_join(const _
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp % Sh::kGroups;
   const int row0 = blockIdx.y * Sh::kRows + warp / Sh::kGroups;
   if (!c.units || c.f0 + (int)blockIdx.y * Sh::kRows >= c.rows) return;
-  const int i0 = blockIdx.x, i1 = (int)((c.e - 1) / c.q);
+  const int i0 = blockIdx.x, i1 = min(ctas - 1, (c.e - 1) / c.q);
   if (warp == 0) {  // the CTAs that had units of it
     int n = 0;
     for (int base = i0; base <= i1; base += 32) {

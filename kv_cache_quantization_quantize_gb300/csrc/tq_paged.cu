@@ -2,6 +2,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "tq_device.cuh"
 
@@ -18,6 +19,7 @@ namespace cg = cooperative_groups;
 // The work is a few KB to a few hundred KB: latency bounds it (launch, three dependent rounds of loads, two
 // barriers), not bandwidth.
 // =============================================================================================
+constexpr int kMaxBatch = 4096;
 constexpr int kMapCtas = 8;
 constexpr int kMapThreads = 512;
 constexpr int kMapWarps = kMapThreads / 32;
@@ -178,6 +180,7 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
     }
   }
   report(a.status, err);
+  __threadfence();  // the table is read by kernels that start early (programmatic dependent launch)
   cl.sync();  // every CTA has read *n_free (and done with the others' shared memory)
   if (fits && rank == 0 && threadIdx.x == 0) *a.n_free = n_free + total;
 }
@@ -264,6 +267,7 @@ __global__ void __cluster_dims__(kMapCtas, 1, 1) __launch_bounds__(kMapThreads) 
   if (threadIdx.x == 0) most = 0;
   __syncthreads();
   if (rank == 0 && taken > 0) atomicMax(&most, taken);
+  __threadfence();  // the table is read by kernels that start early (programmatic dependent launch)
   cl.sync();  // the new table entries are seen by the whole cluster, and every CTA has read *n_free
   if (rank == 0 && threadIdx.x == 0) *a.n_free = n_free - most;
   // slots: four packed tokens per thread; the request by bisection over the starts in shared memory
@@ -312,12 +316,20 @@ int owner_entries(int batch) {
   return n;
 }
 
+// The most shared memory that a call can need, allowed once per device (`known`: one bit each).
 template <typename K>
-cudaError_t launch_map(K kernel, MapArgs& a, int arrays, cudaStream_t s) {
+cudaError_t launch_map(K kernel, MapArgs& a, int arrays, std::atomic<uint64_t>& known, cudaStream_t s) {
   const int entries = owner_entries(a.batch);
   a.mask = entries - 1;
   const size_t smem = sizeof(int32_t) * ((size_t)arrays * a.batch + 2 * entries);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e == cudaSuccess && !(known.load(std::memory_order_relaxed) & bit)) {
+    const int most = (int)sizeof(int32_t) * (arrays * kMaxBatch + 2 * owner_entries(kMaxBatch));
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess) known.fetch_or(bit, std::memory_order_relaxed);
+  }
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(kMapCtas), dim3(kMapThreads), smem, s, a);
 }
@@ -410,7 +422,8 @@ cudaError_t launch_blocks_release(const BlockMap& m, cudaStream_t s) {
   a.max_pages = m.max_pages;
   a.n_blocks = m.n_blocks;
   a.batch = m.batch;
-  return launch_map(k_blocks_release, a, 1, s);
+  static std::atomic<uint64_t> known{0};
+  return launch_map(k_blocks_release, a, 1, known, s);
 }
 
 cudaError_t launch_blocks_map(const BlockMap& m, cudaStream_t s) {
@@ -431,7 +444,8 @@ cudaError_t launch_blocks_map(const BlockMap& m, cudaStream_t s) {
   a.n_blocks = m.n_blocks;
   a.batch = m.batch;
   a.max_tokens = m.max_tokens;
-  return launch_map(k_blocks_map, a, 3, s);
+  static std::atomic<uint64_t> known{0};
+  return launch_map(k_blocks_map, a, 3, known, s);
 }
 
 cudaError_t launch_paged_append(const tq_kv& p, const void* k, const void* v, int dt, const int64_t* ks,

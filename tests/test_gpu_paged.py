@@ -536,3 +536,72 @@ def test_refusals():
         paged.map_blocks(table, i32([0]), one, one, one, i32([]), 1)
     with pytest.raises(tqm.TQError):
         paged.map_blocks(table, i32([0]), one, one, one, one, -1)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_of_random_batches(seed):
+    """Ragged batches of both kernels: empty requests, requests shorter than their queries, cut tiles, all group sizes."""
+    gen = torch.Generator().manual_seed(1000 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (1,), generator=gen))]  # noqa: E731
+    d, g, hkv = pick(64, 128, 256), pick(1, 2, 3, 4, 5, 7, 8, 12, 16), pick(1, 2, 3)
+    batch, most_q, most_kv = pick(1, 2, 5, 9), pick(1, 2, 7, 30, 150, 400), pick(10, 100, 1000, 4000)
+    nq = torch.randint(0, most_q + 1, (batch,), generator=gen).tolist()
+    kv = torch.randint(0, most_kv + 1, (batch,), generator=gen).tolist()
+    nq[0], kv[0] = max(nq[0], 1), max(kv[0], 1)
+    dtype, causal = pick(torch.bfloat16, torch.float16), pick(True, True, False)
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, g * hkv, hkv, d, dtype, seed % 2 == 0, seed, tail=3)
+    out = torch.full(q.shape, 9.0, dtype=dtype, device=DEV)
+    status = i32([0])
+    paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), causal=causal, max_q=pick(0, max(nq)), max_kv=pick(0, max(kv)),
+                    out=out, status=status)
+    assert status.item() == 0
+    check_rows(out, q, ks, vs, nq, kv, causal, 1 / math.sqrt(d))
+    assert bool((out[sum(nq):] == 9).all())
+
+
+@pytest.mark.parametrize("batch,most_q", [(700, 1), (700, 3), (500, 40)])
+def test_attention_of_large_batches(batch, most_q):
+    """More requests than a CTA has threads: each thread sums several on the way to its CTA's place."""
+    gen = torch.Generator().manual_seed(batch + most_q)
+    nq = torch.randint(0, most_q + 1, (batch,), generator=gen).tolist()
+    kv = [n + int(x) for n, x in zip(nq, torch.randint(0, 60, (batch,), generator=gen))]
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, 64, torch.bfloat16, False, batch)
+    out = paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=max(nq))
+    check_rows(out, q, ks, vs, nq, kv, True, 1 / math.sqrt(64))
+
+
+@pytest.mark.parametrize("max_q", [0, 8])
+def test_starts_that_fall_are_reported(max_q):
+    """Requests that overlap: nothing outside the tensors is read or written, and the call says so."""
+    q = torch.randn((300, 8, 128), device=DEV).bfloat16()
+    x = torch.randn((400, 2, 128), device=DEV).bfloat16()
+    starts = [0, 300, 0, 300, 0, 300, -4, 301, 2 ** 31 - 1, 5]
+    status = i32([0])
+    guard = torch.full((302, 8, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    paged.cross_attention(q, x, x, i32(starts), kv_starts=i32([40 * i for i in range(len(starts))]), max_q=max_q, out=guard[1:301], status=status)
+    assert status.item() & paged.TQ_DEV_ERR_LENGTH
+    assert bool((guard[0] == 9).all()) and bool((guard[301] == 9).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_results_repeat_bit_for_bit(d):
+    """The division of the work follows from the lengths alone: two runs, also over dirty workspaces, agree in every bit."""
+    nq, kv = [70, 1, 300], [900, 5000, 2000]
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, d, torch.bfloat16, False, d)
+    outs = []
+    for fill in (0, 255):
+        n = paged.attention_workspace_bytes(q, pool[0], 300, 5000, 3)
+        ws = torch.full((n,), fill, dtype=torch.uint8, device=DEV)
+        outs.append(paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=300, max_kv=5000, workspace=ws))
+    assert torch.equal(outs[0], outs[1])
+
+
+def test_queries_with_strides():
+    """Query rows inside a fused projection, one head's memory for all (stride 0), and outputs inside a wider row."""
+    nq, kv = [40, 1], [300, 130]
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, 128, torch.bfloat16, True, 21)
+    for one in (q[:, :1].expand(41, 8, 128), q):
+        wide = torch.full((41, 20, 128), 9.0, dtype=q.dtype, device=DEV)
+        out = paged.attention(one, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=40, out=wide[:, 5:13])
+        check_rows(out, one, ks, vs, nq, kv, True, 1 / math.sqrt(128))
+        assert bool((wide[:, :5] == 9).all()) and bool((wide[:, 13:] == 9).all())
