@@ -245,8 +245,8 @@ __device__ __forceinline__ float* cut_o(const AttnArgs& a, int ctas, int cta, in
 // parts. Larger tiles have many rows and mostly two parts: a CTA per 16 rows, four of them to a warp.
 template <int T>
 struct JoinShape {
-  static constexpr int kGroups = T <= 32 ? 8 : 1;      // warps that share the parts of a row
-  static constexpr int kPer = T <= 32 ? 1 : 4;         // rows of a warp
+  static constexpr int kGroups = T == 16 ? 8 : T == 32 ? 4 : 1;  // warps that share the parts of a row
+  static constexpr int kPer = T <= 32 ? 1 : 4;                  // rows of a warp
   static constexpr int kWarps = T <= 32 ? 8 : 4;
   static constexpr int kRows = kWarps / kGroups * kPer;  // rows of a CTA
 };
@@ -256,8 +256,8 @@ __global__ void __launch_bounds__(JoinShape<T>::kWarps * 32) k_attn_join(const _
   constexpr int V = D / 32, R = Sh::kPer, kStep = Sh::kWarps / Sh::kGroups;  // row j of a warp: kStep j further
   __shared__ int16_t part[kMaxAttnCtas];
   __shared__ int parts;
-  __shared__ float2 s_ml[Sh::kWarps];
-  __shared__ float s_acc[Sh::kGroups > 1 ? Sh::kWarps : 1][Sh::kGroups > 1 ? D : 1];
+  __shared__ float2 s_ml[Sh::kWarps][R];
+  __shared__ float s_acc[Sh::kGroups > 1 ? Sh::kWarps : 1][R][Sh::kGroups > 1 ? D : 1];
   pdl_wait();
   const CutTile c = cut_tiles(a)[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp % Sh::kGroups;
@@ -314,20 +314,26 @@ __global__ void __launch_bounds__(JoinShape<T>::kWarps * 32) k_attn_join(const _
     }
   }
   if constexpr (Sh::kGroups > 1) {
-    if (lane == 0) s_ml[warp] = make_float2(top[0], sum[0]);
 #pragma unroll
-    for (int x = 0; x < V; ++x) s_acc[warp][lane * V + x] = acc[0][x];
+    for (int j = 0; j < R; ++j) {
+      if (lane == 0) s_ml[warp][j] = make_float2(top[j], sum[j]);
+#pragma unroll
+      for (int x = 0; x < V; ++x) s_acc[warp][j][lane * V + x] = acc[j][x];
+    }
     __syncthreads();
     if (group > 0) return;
 #pragma unroll
-    for (int i = 1; i < Sh::kGroups; ++i) {
-      const float2 ml = s_ml[warp + i];
-      const float mn = fmaxf(top[0], ml.x), mu = mn == -INFINITY ? 0.f : mn;
-      const float wa = exp2_fast(top[0] - mu), wb = exp2_fast(ml.x - mu);
-      top[0] = mn;
-      sum[0] = sum[0] * wa + ml.y * wb;
+    for (int j = 0; j < R; ++j) {
 #pragma unroll
-      for (int x = 0; x < V; ++x) acc[0][x] = acc[0][x] * wa + s_acc[warp + i][lane * V + x] * wb;
+      for (int i = 1; i < Sh::kGroups; ++i) {
+        const float2 ml = s_ml[warp + i][j];
+        const float mn = fmaxf(top[j], ml.x), mu = mn == -INFINITY ? 0.f : mn;
+        const float wa = exp2_fast(top[j] - mu), wb = exp2_fast(ml.x - mu);
+        top[j] = mn;
+        sum[j] = sum[j] * wa + ml.y * wb;
+#pragma unroll
+        for (int x = 0; x < V; ++x) acc[j][x] = acc[j][x] * wa + s_acc[warp + i][j][lane * V + x] * wb;
+      }
     }
   }
 #pragma unroll
