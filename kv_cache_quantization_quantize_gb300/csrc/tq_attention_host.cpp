@@ -145,7 +145,10 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
   return TQ_OK;
 }
 
-// Requests of few rows take the rows kernel, others the tensor cores.
+// Requests of up to 32 rows (queries x query heads per KV head) take the rows kernel, others the tensor cores. Measured
+// with 4 query heads per KV head, head_dim 128: 32 rows, rows kernel against tensor cores: 19.8 against 26.9 us over
+// 8192 tokens, 56 against 61 us over 65536; 64 rows, which would be two tiles: 22.8 against 27.0 us over 8192 tokens, but
+// 83 against 63 us over 65536, and 28 against 22 us for 16 requests of 512.
 tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   tq::AttnPlan p;
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * (q.n_q_heads / kv.n_kv_heads);
@@ -154,7 +157,7 @@ tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   p.tc = tc;
   p.max_rows = rows;
   p.ctas = std::min(p.ctas, tq::kMaxAttnCtas);
-  if (q.max_kv > 0) {  // no more CTAs than the most work there can be feeds
+  if (q.max_kv > 0) {  // no more CTAs than the most work there can be feeds: one tile of 64 tokens takes one
     const double tiles = (double)q.batch * kv.n_kv_heads * ((rows + p.tile_rows - 1) / p.tile_rows);
     const double most = tiles * ((double)q.max_kv * 64 / p.unit + 64 + p.cost);
     if (most < (double)p.ctas * p.least) p.ctas = std::max(1, (int)std::ceil(most / p.least));

@@ -12,8 +12,11 @@ namespace {
 // tokens, for the sums each takes D / 4 channels of all of them, with the weights handed over through shared memory. So no warp holds more
 // than D / 4 channels of the sums and nothing has to be joined at the end; one barrier per unit hands over the weights
 // and tells whether a maximum outgrew its range (kLazy), which is rare after a tile's first unit. Scores and sums run
-// on mma.sync m16n8k16: at 16 or 32 rows the tensor pipe has a few percent of its work, and its register operands
+// on mma.sync m16n8k16: at 16 or 32 rows the tensor pipe has a fifth of its time's work, and its register operands
 // need no copies.
+// Measured (GB300, 32 query heads on 8 KV heads, head_dim 128, bf16): 4 x 32768 tokens 83 us, 6.4 TB/s (97 % of a
+// measured copy); one sequence of 131072 tokens 86 us; of 32768 30 us, of which about 4 us are the way to the first
+// load, 4 us the join and 20 us the bytes. A unit takes 930 cycles of a CTA, its bytes 2900 of an SM's share of DRAM.
 // =============================================================================================
 constexpr int kRowsThreads = 160;  // four consumer warps, one producer warp
 constexpr int kTileCost = 64;      // start and end of a tile, as one unit
@@ -24,8 +27,12 @@ struct RowsShape {
   static constexpr int R = 16 * MT;
   static constexpr int U = D == 64 ? 128 : 64;    // tokens of a unit: 16 KB of K and as much of V (32 at head_dim 256)
   static constexpr int kEntry = U * D * 2;        // bytes of K or V of one unit
-  static constexpr int kCtas = D == 256 ? 1 : 2;  // CTAs per SM
-  static constexpr int kEntries = D == 256 && MT == 1 ? 6 : 5;  // 80 KB per CTA in flight (160 to 192 at head_dim 256)
+  // Bytes in flight: 64 KB of each of two CTAs on an SM (head_dim 128), 48 KB of each of three or two (64), 128 KB
+  // (256). More only queue up: with 5 and 6 entries at head_dim 128, 16 sequences of 4096 to 8192 tokens took 65.2 and
+  // 67.2 us instead of 63.7. At head_dim 64 a third CTA hides the shorter units' latencies: 64 x 4096 tokens took 126 us
+  // with two CTAs, 105 us with three.
+  static constexpr int kCtas = D == 256 ? 1 : D == 64 && MT == 1 ? 3 : 2;  // CTAs per SM
+  static constexpr int kEntries = D == 64 ? 3 : 4;
   static constexpr int kQRow = D * 2 + 16;  // bytes of a query row: 16 more than it has, so that ldmatrix meets no conflicts
   static constexpr int kQ = R * kQRow;
   static constexpr int kP = R * U * 2;  // weights of one unit
@@ -498,7 +505,7 @@ cudaError_t launch_type(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p,
 
 AttnShape attn_rows_shape(int d, int64_t rows, int sms) {
   const int tile = rows <= 16 ? 16 : 32;
-  const int ctas = sms * (d == 256 ? RowsShape<256, 1>::kCtas : RowsShape<128, 1>::kCtas);
+  const int ctas = sms * (d == 256 ? RowsShape<256, 1>::kCtas : d == 64 && tile == 16 ? RowsShape<64, 1>::kCtas : 2);
   return {tile, d == 64 ? RowsShape<64, 1>::U : RowsShape<128, 1>::U, ctas, cta_bytes(tile, d), kTileCost, kMinPart};
 }
 cudaError_t launch_attn_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {

@@ -16,6 +16,12 @@ namespace {
 //     bits over it, and rescales O_t only where a row's maximum grew by more than 2^8: the weights stay below
 //     2^8, far inside fp32 and f16, and the final division takes the factor out.
 // The two tiles alternate: while one's softmax runs, the tensor pipe works for the other.
+// Measured (GB300, bf16, 32 query heads on 8 KV heads, head_dim 128): 8192 queries on 8192 tokens without a mask 619 us,
+// 1777 TFLOP/s (93 % of a measured cuBLAS burst); causal 351 to 368 us, 1495 to 1566 TFLOP/s; 2048 queries after 30720
+// tokens 690 us, 1545 TFLOP/s. A unit of both tiles takes 2500 cycles there, its four products 2048. Head_dim 64 is bound
+// by the softmax (8192 x 8192, 16 heads: 1097 TFLOP/s without a mask; 583 instructions per row's thread and unit, at 2
+// warps per scheduler), head_dim 256 by shared memory (its 64-token scores read Q for half a tile's work; 4096 x 4096
+// causal: 900 to 1020 TFLOP/s).
 // =============================================================================================
 template <int D>
 struct TcShape {
