@@ -191,6 +191,7 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void*
   a.part = ws;
   const double scale = q->softmax_scale > 0.f ? (double)q->softmax_scale : 1.0 / std::sqrt((double)kv.head_dim);
   a.scale_log2 = (float)(scale * 1.4426950408889634);
+  if (!std::isfinite(a.scale_log2)) return fail(TQ_ERR_INVALID_ARG, "softmax_scale %g is too large", scale);
   a.n_rows = q->n_rows;
   a.batch = q->batch;
   a.hq = q->n_q_heads;

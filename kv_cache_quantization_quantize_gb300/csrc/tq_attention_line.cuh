@@ -199,7 +199,7 @@ __device__ __forceinline__ void find_start(const AttnArgs& a, int least, LineSta
         start += a.hkv * one;
         continue;
       }
-      int head = min(a.hkv - 1, (int)((float)(p0 - start) / (float)one));  // within a few of the quotient
+      int head = max(0, min(a.hkv - 1, (int)((float)(p0 - start) / (float)one)));  // within a few of the quotient
       while (head > 0 && start + head * one > p0) --head;
       while (head + 1 < a.hkv && start + (head + 1) * one <= p0) ++head;
       start += head * one;
