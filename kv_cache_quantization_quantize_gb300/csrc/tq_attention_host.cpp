@@ -179,6 +179,7 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void*
   if (!kv.outer || !kv.tokens) {  // nothing to read: the tensor maps need an address all the same
     kv.k = kv.v = const_cast<void*>(q->q);
     kv.outer = kv.tokens = 0;
+    for (int i = 0; i < 3; ++i) kv.k_strides[i] = kv.v_strides[i] = kv.head_dim;  // an empty tensor's may be anything
   }
   a.q = q->q;
   a.out = q->out;

@@ -355,6 +355,15 @@ def test_cross_attention_without_any_state():
     assert paged.cross_attention(q[:0], none, none, i32([0, 0, 0]), kv_lens=i32([0, 0])).shape == (0, 4, 64)
 
 
+def test_cross_attention_to_an_empty_view():
+    """Strides of a tensor without elements are never taken: here 67 elements from head to head."""
+    q = torch.randn((3, 4, 64), device=DEV).half()
+    none = torch.empty((0, 2, 67), dtype=torch.float16, device=DEV)[..., :64]
+    assert not paged.cross_attention(q, none, none, i32([0, 1, 3]), kv_starts=i32([0, 0, 0])).any()
+    none = torch.empty((2, 0, 2, 67), dtype=torch.float16, device=DEV)[..., :64]
+    assert not paged.cross_attention(q, none, none, i32([0, 1, 3]), kv_lens=i32([0, 0])).any()
+
+
 def test_cross_attention_reports_bad_arrays():
     q = torch.randn((2, 2, 64), device=DEV).half()
     x = torch.randn((10, 2, 64), device=DEV).half()
