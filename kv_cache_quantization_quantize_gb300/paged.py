@@ -118,6 +118,8 @@ def map_blocks(table, free, n_free, seq_ids, lens, n_new, max_tokens, out=None, 
 
 
 def _map_blocks(args, ids, batch, max_tokens, out, word, raw, index, device):
+    if max_tokens > 1 << 30:
+        raise ValueError(f"max_tokens {max_tokens}: at most 2^30")
     if out is None:
         # one allocation: [slots | starts | totals], each part 16-byte aligned
         n = max(max_tokens, 0)
@@ -158,7 +160,7 @@ def _pools(k_pool, v_pool):
     shape, dtype, index = k_pool.shape, k_pool.dtype, k_pool.get_device()
     if index < 0:
         raise ValueError("k_pool: expected a CUDA tensor")
-    if (len(shape) != 4 or shape[1] != PAGE or shape != v_pool.shape or dtype is not v_pool.dtype or dtype not in _HALVES
+    if (len(shape) != 4 or shape[1] != PAGE or not shape[2] or shape != v_pool.shape or dtype is not v_pool.dtype or dtype not in _HALVES
             or v_pool.get_device() != index):
         raise ValueError("k_pool, v_pool: expected two bf16 or f16 tensors [n_blocks, 128, n_kv_heads, head_dim] on one device")
     ks, vs = k_pool.stride(), v_pool.stride()
@@ -311,7 +313,7 @@ class BlockPool:
         release_blocks(self.table, self.free, self.n_free, seq_ids, keep, self.status, stream)
 
     def check_status(self, clear=True):
-        """The TQ_DEV_ERR_* bits that calls on this pool have set (waits for the device)."""
+        """The TQ_DEV_ERR_* bits that calls on this pool have set (waits for the current stream)."""
         word = int(self.status.item())
         if clear and word:
             self.status.zero_()

@@ -512,6 +512,7 @@ def test_refusals():
     bad(ValueError, q=q.cpu())
     bad(ValueError, v_pool=pool[:2])
     bad(ValueError, k_pool=pool.float(), v_pool=pool.float())
+    bad(ValueError, k_pool=pool[:, :, :0], v_pool=pool[:, :, :0])
     bad(ValueError, k_pool=pool[:, :64], v_pool=pool[:, :64])
     bad(ValueError, table=table.long())
     bad(ValueError, q_starts=torch.tensor([0, 1], device=DEV))
@@ -545,6 +546,8 @@ def test_refusals():
         paged.map_blocks(table, i32([0]), one, one, one, i32([]), 1)
     with pytest.raises(tqm.TQError):
         paged.map_blocks(table, i32([0]), one, one, one, one, -1)
+    with pytest.raises(ValueError):
+        paged.map_blocks(table, i32([0]), one, one, one, one, (1 << 32) + 1)
 
 
 @pytest.mark.parametrize("seed", range(24))
@@ -614,3 +617,48 @@ def test_queries_with_strides():
         out = paged.attention(one, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=40, out=wide[:, 5:13])
         check_rows(out, one, ks, vs, nq, kv, True, 1 / math.sqrt(128))
         assert bool((wide[:, :5] == 9).all()) and bool((wide[:, 13:] == 9).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(8, 2), (6, 2)])
+@pytest.mark.parametrize("n", [2, 90, 500])
+def test_one_sequence_for_several_requests(d, heads, n):
+    """Two requests read one table row (samples of one prompt). Rows before the first and behind the last request hold NaN,
+    and are left alone."""
+    hq, hkv = heads
+    m = 1500
+    q, pool, table, rows, ks, vs = paged_inputs([n], [m], hq, hkv, d, torch.bfloat16, False, n + d, tail=n + 9)
+    q[:4] = q[4 + 2 * n:] = float("nan")
+    starts = [4, 4 + n, 4 + 2 * n]
+    out = torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+    paged.attention(q, pool[0], pool[1], table, rows.repeat(2), i32(starts), i32([m, m]), max_q=n, out=out)
+    check_rows(out, q, ks * 2, vs * 2, [n, n], [m, m], True, 1 / math.sqrt(d), starts)
+    assert bool((out[:4] == 9).all()) and bool((out[starts[2]:] == 9).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [(8, 2), (6, 2)])
+@pytest.mark.parametrize("nq,kv", [([1, 2, 1], [5000, 4999, 130]), ([300, 1, 77], [3000, 9000, 100])])
+def test_outputs_in_the_queries_place(d, heads, nq, kv):
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, *heads, d, torch.float16, False, d, tail=2)
+    q0 = q.clone()
+    out = paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), max_q=max(nq), out=q)
+    check_rows(out, q0, ks, vs, nq, kv, True, 1 / math.sqrt(d))
+    assert torch.equal(out[sum(nq):], q0[sum(nq):])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams that overlap on the GPU, each in its own workspace, give what one after the other gives."""
+    cases = [paged_inputs(nq, kv, 8, 2, 128, torch.bfloat16, False, 31 + i) + (nq, kv)
+             for i, (nq, kv) in enumerate([([1] * 8, [4000] * 8), ([400, 1], [6000, 3000])])]
+    args = [(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv)) for q, pool, table, rows, ks, vs, nq, kv in cases]
+    want = [paged.attention(*a, max_q=max(c[6])) for a, c in zip(args, cases)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i in (0, 1):
+            got[i].append(paged.attention(*args[i], max_q=max(cases[i][6]), stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(x, want[i]) for x in got[i])
