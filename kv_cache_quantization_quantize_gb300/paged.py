@@ -120,15 +120,12 @@ def map_blocks(table, free, n_free, seq_ids, lens, n_new, max_tokens, out=None, 
 def _map_blocks(args, ids, batch, max_tokens, out, word, raw, index, device):
     if max_tokens > 1 << 30:
         raise ValueError(f"max_tokens {max_tokens}: at most 2^30")
-    if out is None:
-        # one allocation: [slots | starts | totals], each part 16-byte aligned
-        n = max(max_tokens, 0)
-        a = (n + 3) & ~3
-        b = a + ((batch + 4) & ~3)
-        buf = torch.empty(b + batch, dtype=_I32, device=device)
-        at = buf.data_ptr()
-        places = (at + 4 * a, at + 4 * b, at)
-        out = (buf.as_strided((n,), (1,)), buf.as_strided((batch + 1,), (1,), a), buf.as_strided((batch,), (1,), b))
+    if out is None:  # three allocations: views of one take 5 us longer
+        slots = torch.empty(max(max_tokens, 0), dtype=_I32, device=device)
+        starts = torch.empty(batch + 1, dtype=_I32, device=device)
+        totals = torch.empty(batch, dtype=_I32, device=device)
+        out = (slots, starts, totals)
+        places = (starts.data_ptr(), totals.data_ptr(), slots.data_ptr())
     else:
         slots, starts, totals = out
         places = (_ints("starts", starts, index, batch + 1), _ints("totals", totals, index, batch), _ints("slots", slots, index, max_tokens))
