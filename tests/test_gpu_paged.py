@@ -44,7 +44,7 @@ def random_state(gen, max_seqs, max_pages, n_blocks, fill):
 
 @pytest.mark.parametrize("batch,max_pages,n_blocks,hist,new", [
     (1, 1, 4, 0, 1), (1, 4, 8, 300, 1), (3, 8, 64, 500, 200), (5, 8, 6, 300, 700), (33, 4, 200, 300, 5), (300, 6, 2000, 600, 129),
-    (1025, 3, 3200, 200, 100), (4, 300, 1300, 20000, 15000),
+    (1025, 3, 3200, 200, 100), (4, 300, 1300, 20000, 15000), (4096, 2, 7000, 150, 60),
 ])
 def test_map_and_release_follow_the_serial_form(batch, max_pages, n_blocks, hist, new):
     gen = torch.Generator().manual_seed(batch * 1000 + max_pages)
