@@ -38,6 +38,7 @@ _STRIDES = struct.Struct("@2q")
 
 _I32 = torch.int32
 _HALVES = (torch.bfloat16, torch.float16)
+_alloc, _free = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
 
 
 class _On:
@@ -212,14 +213,20 @@ def _attend_here(q, shape, dtype, index, batch, q_starts, max_q, max_kv, softmax
         raise ValueError("q, out: the channels of a head have to be contiguous")
     queries = _QUERIES.pack(q.data_ptr(), out.data_ptr(), qs[0], qs[1], os[0], os[1], _ints("q_starts", q_starts, index), shape[0], shape[1],
                             batch, max_q, max_kv, softmax_scale)
-    if workspace is None:
-        n = load().tq_attention_workspace_bytes(queries, kv)
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace: expected a contiguous tensor on cuda:{index}")
-    ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    check(call(queries, kv, batch, ws, size, raw))
+    if workspace is not None:
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected a contiguous tensor on cuda:{index}")
+        check(call(queries, kv, batch, workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw))
+        return out
+    # Memory of the call's stream, given back to it behind the launches: what comes next on that stream may take it. Without
+    # a tensor around it the call takes 11.7 us of the host instead of 17.6.
+    size = load().tq_attention_workspace_bytes(queries, kv)
+    ws = _alloc(size, raw) if size else None
+    try:
+        check(call(queries, kv, batch, ws, size, raw))
+    finally:
+        if size:
+            _free(ws)
     return out
 
 
@@ -241,7 +248,8 @@ def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True,
     q: [rows, n_q_heads, head_dim] of the pools' type, request b's rows at [q_starts[b], q_starts[b + 1]); kv_lens[b]: its
     tokens with the new ones, in the pages of table row seq_ids[b] (None: row b). max_q: no request has more rows (0:
     unknown; few rows take a kernel of their own); max_kv: no request has more tokens (0: unknown; short calls launch fewer
-    CTAs). Returns out, of q's shape; rows behind the last request stay as they are."""
+    CTAs). Returns out, of q's shape; rows of no request stay as they are. What the cache holds behind a request's
+    tokens does not matter; a token that any of its queries sees has to be finite."""
     index, kv, d, heads, dtype = _pools(k_pool, v_pool)
     pages = _table(table, index)
     word = None if status is None else _ints("status", status, index, 1)
