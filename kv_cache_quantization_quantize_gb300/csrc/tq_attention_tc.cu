@@ -29,10 +29,13 @@ struct TcShape {
   static constexpr int kBN = D == 256 ? 64 : 128;  // tokens of a K or V tile
   static constexpr int kTile = kBN * D * 2;        // its bytes
   static constexpr int kStages = D == 64 ? 8 : 4;  // 128 KB of K and V in flight
-  static constexpr int kThreads = kNT * 128 + 128;
+  // One tile's softmax is shared by two warpgroups that take its units in turn, each a buffer of S and P of its own: with
+  // one warp per scheduler it took 2000 cycles per unit of 64 tokens, the products 1280.
+  static constexpr bool kPair = kNT == 1;
+  static constexpr int kThreads = 384;
   static constexpr int kQ = 128 * D * 2;           // bytes of a tile's queries
   static constexpr int kStage = 4096;              // of a softmax warp, for its results on their way out
-  static constexpr int kSmem = 1024 + kNT * kQ + kStages * kTile + kNT * 4 * kStage + 512;
+  static constexpr int kSmem = 1024 + kNT * kQ + kStages * kTile + 8 * kStage + (kPair ? 1024 : 0) + 512;
   // TMEM columns: S_t at t * 128, P_t at kP + t * kPStep, O_t at kO + t * D. At D = 128 they fill all 512 columns
   // with P_t over S_t, so that the next S_t waits for P_t's product; else P_t has a place of its own, and the next
   // S_t is made while the softmax works on this one.
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* skv = smem + NT * Sh::kQ;
   uint8_t* sout = skv + ST * kTile;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sout + NT * 4 * Sh::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(sout + 8 * Sh::kStage + (Sh::kPair ? 1024 : 0));
   uint64_t* empty = full + ST;
   uint64_t* q_full = empty + ST;       // per tile: queries are in shared memory
   uint64_t* q_empty = q_full + NT;     // per tile: their last scores are made (q_tma)
@@ -147,13 +150,17 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint64_t* part_full = turn + NT;     // ring of parts
   uint64_t* part_empty = part_full + kParts;
   uint64_t* drained = part_empty + kParts;
-  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drained + 1);
+  // kPair, per warpgroup and warp: the row maxima after a unit, and the row sums, can be read; the part is written out
+  uint64_t* m_full = drained + 1;
+  uint64_t* l_full = m_full + 8;
+  uint64_t* written = l_full + 8;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(Sh::kPair ? written + 8 : drained + 1);
   __shared__ int warp_sums[Sh::kThreads / 32];
   __shared__ Part parts[kParts];
   __shared__ LineStart first;
 
   const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-  constexpr int kMmaWarp = NT * 4, kTmaWarp = NT * 4 + 1, kWalkWarp = NT * 4 + 2, kMmaWarp1 = NT * 4 + 3;
+  constexpr int kMmaWarp = 8, kTmaWarp = 9, kWalkWarp = 10, kMmaWarp1 = 11;
   if (threadIdx.x == 32) {
     prefetch_map(&map_k);
     prefetch_map(&map_v);
@@ -179,9 +186,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], NT * 4 + 3);
+      mbar_init(&part_empty[i], 8 + 3);
     }
     mbar_init(drained, 2);
+    for (int i = 0; Sh::kPair && i < 24; ++i) mbar_init(&m_full[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -213,10 +221,9 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     return g.n_all >= 0;
   };
   // The softmax threads hold a row of scores: they take registers from the other warps (8 x 32 x 216 + 4 x 32 x 72 =
-  // 384 x 168, what the block was launched with). One tile's warps have enough as it is.
-  constexpr bool kSplitRegs = NT == 2;
+  // 384 x 168, what the block was launched with).
   if (warp >= kMmaWarp) {
-    if constexpr (kSplitRegs) set_regs_dec<72>();
+    set_regs_dec<72>();
     if (warp == kTmaWarp) {
       // ---- K and V tiles: for every unit, ring entry e holds K and entry e + 1 its V ----
       int e = 0, issued = 0;
@@ -395,9 +402,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       if (!ok && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
     }
   } else {
-    if constexpr (kSplitRegs) set_regs_inc<216>();
-    // ---- softmax of tile t: a thread per row ----
-    const int t = warp >> 2, row_t = threadIdx.x & 127;
+    set_regs_inc<216>();
+    // ---- softmax of tile t: a thread per row (kPair: of every other unit) ----
+    constexpr bool kPair = Sh::kPair;
+    const int wg = warp >> 2, t = kPair ? 0 : wg, row_t = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t ts = tmem + t * 128 + lanes, tp = tmem + Sh::kP + t * Sh::kPStep + lanes;
     const uint32_t to = tmem + Sh::kO + t * D + lanes;
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     // a part's queries into shared memory, as a K-major operand, where they do not come by TMA (group sizes such as 3 or
     // 6); rows past the last are zero
     auto load_q = [&] {
-      if (a.q_tma || (t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
+      if (a.q_tma || (kPair && wg == 1) || (t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
       constexpr int kBatch = D == 64 ? 8 : 16;
       constexpr int kChunks = D / 8, kRowsStep = 128 / kChunks;  // 16-byte chunks of a row; rows of one step
       const int c = row_t % kChunks;
@@ -433,9 +441,22 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[t]);
     };
+    // kPair: the other warpgroup has the same rows in its warp of the same rank. A unit's maxima go from one to the other
+    // (through their owner's stage, which is free until the part is written out), so that O has one scale; the sums
+    // stay apart until the part's end.
+    const int mine8 = warp, other8 = warp ^ 4;
+    float* const m_own = reinterpret_cast<float*>(sout + warp * Sh::kStage) + lane;
+    const float* const m_other = reinterpret_cast<const float*>(sout + other8 * Sh::kStage) + lane;
+    float* const l_all = reinterpret_cast<float*>(sout + 8 * Sh::kStage) + row_t;  // [2][128]
+    int ends = 0, sums = 0;  // parts written out; of these, with tokens
     bool have = take(g);
     if (have) load_q();
     while (have) {
+      if (kPair && ends > 0) {  // O can be written again, and what the warpgroups exchange
+        ok = warp_wait(&written[other8], (ends - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+      }
       const int n = t == 0 ? g.n_of[0] : g.n_of[NT - 1];
       const int f = g.f0 + t * 128 + row_t;
       const bool mine = f < g.rows;
@@ -449,9 +470,10 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const int u0 = g.u0;
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
       float m = mine ? -INFINITY : INFINITY, l = 0.f;  // a row past the last never outgrows its maximum
-      for (int k = 0; k < n; ++k) {
-        const int bi = t * Sh::kBufs + buf_of(made);
-        ok = warp_wait(&s_full[bi], turn_of(made));
+      float ml = m;  // what l is relative to (kPair; else m)
+      for (int k = kPair ? (made ^ wg) & 1 : 0; k < n; k += kPair ? 2 : 1) {
+        const int j = made + k, bi = t * Sh::kBufs + buf_of(j);
+        ok = warp_wait(&s_full[bi], turn_of(j));
         if (!ok) break;
         tc_fence_after();
         // the other tile's weights are made: now this one has the special function units, and that one the tensor pipe
@@ -461,7 +483,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         float s[BN];
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + buf_of(made) * 64 + c, s + c);
+        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + buf_of(j) * 64 + c, s + c);
         tmem_wait_ld();
         if constexpr (Sh::kOwnP) {
           tc_fence_before();
@@ -483,12 +505,24 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[BN - 4 + i]);
         const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
+        if (kPair && k > 0) {
+          ok = warp_wait(&m_full[other8], turn_of(j - 1));
+          if (!ok) break;
+          m = *m_other;
+        }
         float mn = m;
         if (mx > m + kLazy || m == -INFINITY) mn = fmaxf(m, mx);
+        if constexpr (kPair) {
+          *m_own = mn;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m_full[mine8]);
+          if (mn != ml) l *= exp2_fast(ml - mn);
+          ml = mn;
+        }
         const bool grew = mn != m && m != -INFINITY;
         const bool rescale = __any_sync(0xffffffffu, grew);
         // O_t is whole before it is rescaled, and P_t has been used before it is written again
-        const int last = rescale ? made - 1 : Sh::kOwnP ? made - Sh::kBufs : -1;
+        const int last = rescale ? j - 1 : Sh::kOwnP ? j - Sh::kBufs : -1;
         if (last >= 0) {
           ok = warp_wait(&o_full[t * Sh::kBufs + buf_of(last)], turn_of(last));
           if (!ok) break;
@@ -496,7 +530,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         if (rescale) {
           const float alpha = grew ? exp2_fast(m - mn) : 1.f;
-          l *= alpha;
+          if constexpr (!kPair) l *= alpha;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -523,7 +557,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               sum[i & 1] = add2(sum[i & 1], y);
               p[i] = pack2<BF16>(y.x, y.y);
             }
-            tmem_st16(tp + buf_of(made) * 32 + c / 2, p);
+            tmem_st16(tp + buf_of(j) * 32 + c / 2, p);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -536,9 +570,23 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         const float2 all = add2(sum[0], sum[1]);
         l += all.x + all.y;
-        ++made;
       }
       if (!ok) break;
+      made += n;
+      if (kPair && n > 0) {
+        if (((made - 1) & 1) != wg) {
+          ok = warp_wait(&m_full[other8], turn_of(made - 1));
+          if (!ok) break;
+          m = *m_other;
+          if (m != ml) l *= exp2_fast(ml - m);
+        }
+        l_all[wg * 128] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&l_full[mine8]);
+        ok = warp_wait(&l_full[other8], sums++ & 1);
+        if (!ok) break;
+        l = l_all[0] + l_all[128];
+      }
       // where this part's result goes; then the next tile's queries, so that its scores are made under the end of
       // this one
       const bool direct = g.direct;
@@ -555,7 +603,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
                            : (int64_t)(t * 128 + row) * D;
       }
       float* po = cut_o<T, D>(a, gridDim.x, blockIdx.x, g.slot);
-      if (!direct) cut_ml<T>(a, gridDim.x, blockIdx.x, g.slot)[t * 128 + row_t] = make_float2(m, l);
+      if (!direct && (!kPair || wg == 0)) cut_ml<T>(a, gridDim.x, blockIdx.x, g.slot)[t * 128 + row_t] = make_float2(m, l);
       have = take(g);
       if (!ok) break;
       if (have) load_q();
@@ -569,7 +617,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       uint8_t* stage = sout + warp * Sh::kStage;
       const int step = direct ? 64 : 32;  // columns: 16-bit results, fp32 sums
 #pragma unroll 1
-      for (int c = 0; c < D; c += step) {
+      for (int c = kPair ? wg * (D / 2) : 0; c < (kPair ? (wg + 1) * (D / 2) : D); c += step) {
         uint4 v[8];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -608,6 +656,11 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         __syncwarp();
       }
       tc_fence_before();
+      if constexpr (kPair) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&written[mine8]);
+        ++ends;
+      }
     }
     if (!ok && lane == 0 && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
   }
