@@ -6,8 +6,8 @@ namespace tq {
 namespace {
 
 // =============================================================================================
-// k_attn_tc: one CTA takes NT tiles of 128 rows (query, head of the group) of one request and KV head, and one
-// split of its tokens. The rows of a group share K and V, so a tile is full at any group size.
+// k_attn_tc: a CTA takes its part of the line; at a time NT tiles of 128 rows (query, head of the group) of one request
+// and KV head, over their tokens or the part of them that is its own. The rows of a group share K and V, so a tile is full at any group size.
 //   - a TMA warp keeps a ring of K and V tiles (BN tokens) in flight, in the 128-byte swizzle;
 //   - two MMA warps issue S_t = Q_t K^T into TMEM, and O_t += P_t V with P_t read from TMEM and V taken as it lies
 //     (tokens x channels, the MN-major operand form): one per tile, or where there is one tile, one for the scores and
@@ -15,35 +15,47 @@ namespace {
 //   - a warpgroup per tile reads S_t (a thread per row, so row sums need no exchange), writes P_t = 2^(s - m) in 16
 //     bits over it, and rescales O_t only where a row's maximum grew by more than 2^8: the weights stay below
 //     2^8, far inside fp32 and f16, and the final division takes the factor out.
-// The two tiles alternate: while one's softmax runs, the tensor pipe works for the other.
+// The two tiles alternate: while one's softmax runs, the tensor pipe works for the other. One tile has both warpgroups:
+// they take its units in turn and hand each row's maximum on through shared memory; row sums meet at the end.
 // Measured (GB300, bf16, 32 query heads on 8 KV heads, head_dim 128): 8192 queries on 8192 tokens without a mask 619 us,
 // 1777 TFLOP/s (93 % of a measured cuBLAS burst); causal 351 to 368 us, 1495 to 1566 TFLOP/s; 2048 queries after 30720
 // tokens 690 us, 1545 TFLOP/s. A unit of both tiles takes 2500 cycles there, its four products 2048. Head_dim 64 is bound
 // by the softmax (8192 x 8192, 16 heads: 1097 TFLOP/s without a mask; 583 instructions per row's thread and unit, at 2
-// warps per scheduler), head_dim 256 by shared memory (its 64-token scores read Q for half a tile's work; 4096 x 4096
-// causal: 900 to 1020 TFLOP/s).
+// warps per scheduler), head_dim 256 by K and V, which pass shared memory for 128 rows only: 64 KB a unit, whose products
+// take 1024 cycles and which takes about 1700 (4096 x 4096, 16 heads: 204 us, 1350 TFLOP/s without a mask; causal 123 us,
+// 1120; 2048 queries after 14336 tokens 345 to 358 us, 1440 to 1490).
 // =============================================================================================
+// kPair: the queries are an operand in TMEM, in these columns. From shared memory, 64 tokens' scores would read 64 KB of
+// them in 512 cycles, beside 32 KB of K, 32 KB of V and 64 KB that arrive (2048 queries after 14336 tokens: 376 us with
+// the queries there, 345 so).
+constexpr uint32_t kTmemQ = 128;
+
 template <int D>
 struct TcShape {
   static constexpr int kNT = D == 256 ? 1 : 2;     // tiles of 128 rows: TMEM holds S and O of two up to D = 128
   static constexpr int kBN = D == 256 ? 64 : 128;  // tokens of a K or V tile
   static constexpr int kTile = kBN * D * 2;        // its bytes
   static constexpr int kStages = D == 64 ? 8 : 4;  // 128 KB of K and V in flight
-  // One tile's softmax is shared by two warpgroups that take its units in turn, each a buffer of S and P of its own: with
-  // one warp per scheduler it took 2000 cycles per unit of 64 tokens, the products 1280.
+  // One tile's softmax is shared by two warpgroups that take its units in turn, each with a buffer of S and P of its own:
+  // with one warp per scheduler it was the bound (2048 queries after 14336 tokens: 413 us, with two 376).
   static constexpr bool kPair = kNT == 1;
   static constexpr int kThreads = 384;
+  // Start and end of a tile, in 64ths of a unit: 3 units of 128 tokens, 5 of 64 (4096 x 4096 causal at D = 256: 138 us
+  // with 3 units, 123 with 5, 126 with 7). No CTA gets less than a tile of one unit costs: short work takes fewer CTAs.
+  static constexpr int kTileCost = D == 256 ? 320 : 192;
+  static constexpr int kMinPart = kTileCost + 64;
   static constexpr int kQ = 128 * D * 2;           // bytes of a tile's queries
   static constexpr int kStage = 4096;              // of a softmax warp, for its results on their way out
   static constexpr int kSmem = 1024 + kNT * kQ + kStages * kTile + 8 * kStage + (kPair ? 1024 : 0) + 512;
   // TMEM columns: S_t at t * 128, P_t at kP + t * kPStep, O_t at kO + t * D. At D = 128 they fill all 512 columns
-  // with P_t over S_t, so that the next S_t waits for P_t's product; else P_t has a place of its own, and the next
-  // S_t is made while the softmax works on this one.
-  static constexpr bool kOwnP = D != 128;
-  static constexpr uint32_t kP = kOwnP ? (D == 64 ? 256 : 128) : 0, kPStep = kOwnP ? 64 : 128;
-  // At D = 256 one tile has to hide its own softmax: S and P are doubled (64 and 32 columns apart), so that the scores
-  // of the next unit are made before this one's products, and weights can be written while the last ones are used.
+  // with P_t over S_t, so that the next S_t waits for P_t's product, and so they do at D = 256 with the queries; at
+  // D = 64 P_t has a place of its own, and the next S_t is made while the softmax works on this one.
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kP = kOwnP ? 256 : 0, kPStep = kOwnP ? 64 : 128;
+  // At D = 256 one tile has to hide its own softmax: S and P are doubled, so that the scores of the next unit are made
+  // before this one's products, and weights can be written while the last ones are used.
   static constexpr int kBufs = D == 256 ? 2 : 1;
+  static constexpr uint32_t kBuf = 64;  // columns from one buffer of S and P to the next
   static constexpr uint32_t kO = D == 64 ? 384 : 256;
   // At D = 128 the tiles' softmaxes take turns: left alone they fall into step, share the special function units and
   // then leave the tensor pipe idle together (2900 cycles per unit against 2500; the SMs differed by 30 %). At D = 64
@@ -116,8 +128,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
-constexpr int kTileCost = 192;  // start and end of a tile, as 3 units
-constexpr int kMinPart = 256;   // no CTA gets less than a tile of one unit costs: short work takes fewer CTAs
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
@@ -125,7 +135,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q) {
   using Sh = TcShape<D>;
   constexpr int NT = Sh::kNT, BN = Sh::kBN, ST = Sh::kStages, T = 128 * NT;
-  using W = Walk<T, BN, kTileCost, NT>;
+  using W = Walk<T, BN, Sh::kTileCost, NT>;
   constexpr uint32_t kTile = Sh::kTile;
   constexpr uint32_t kType = BF16 ? 1u : 0u;
   constexpr uint32_t kIdescS = (1u << 4) | (kType << 7) | (kType << 10) | ((uint32_t)(BN >> 3) << 17) | (8u << 24);
@@ -154,7 +164,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint64_t* m_full = drained + 1;
   uint64_t* l_full = m_full + 8;
   uint64_t* written = l_full + 8;
-  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(Sh::kPair ? written + 8 : drained + 1);
+  uint64_t* q_tmem = written + 8;  // the queries are in TMEM
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(Sh::kPair ? q_tmem + 1 : drained + 1);
   __shared__ int warp_sums[Sh::kThreads / 32];
   __shared__ Part parts[kParts];
   __shared__ LineStart first;
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     }
     for (int i = 0; i < NT; ++i) {
       mbar_init(&q_full[i], a.q_tma ? 1 : 4);
-      mbar_init(&q_empty[i], 1);
+      mbar_init(&q_empty[i], Sh::kPair ? 8 : 1);
       mbar_init(&turn[i], 4);
     }
     for (int i = 0; i < NB; ++i) {
@@ -190,6 +201,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     }
     mbar_init(drained, 2);
     for (int i = 0; Sh::kPair && i < 24; ++i) mbar_init(&m_full[i], 1);
+    if constexpr (Sh::kPair) mbar_init(q_tmem, 8);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
   uint32_t err = 0;
 
   tc_fence_before();
-  find_start<W, Sh::kThreads>(a, kMinPart, first, warp_sums);
+  find_start<W, Sh::kThreads>(a, Sh::kMinPart, first, warp_sums);
   tc_fence_after();
   const uint32_t tmem = uniform(*tmem_base);
   // unit j of a tile uses buffer j % kBufs for the (j / kBufs)-th time
@@ -289,10 +301,12 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               const uint32_t step = (i & 3) * 2;
-              umma_bf16_lo(sd + buf_of(j) * 64, q_lo + (i >> 2) * 1024 + step, ka + (i >> 2) * (BN * 128 >> 4) + step, kIdescS, i > 0);
+              const uint32_t kb = ka + (i >> 2) * (BN * 128 >> 4) + step;
+              if constexpr (Sh::kPair) umma_ts_lo(sd + buf_of(j) * Sh::kBuf, tmem + kTmemQ + i * 8, kb, kIdescS, i > 0);
+              else umma_bf16_lo(sd, q_lo + (i >> 2) * 1024 + step, kb, kIdescS, i > 0);
             }
             umma_commit(&s_full[t * Sh::kBufs + buf_of(j)]);
-            if (last && a.q_tma) umma_commit(&q_empty[t]);
+            if (!Sh::kPair && last && a.q_tma) umma_commit(&q_empty[t]);
           }
           umma_commit(&empty[st]);
         }
@@ -304,13 +318,13 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         if (n_all == 0) continue;
         if (does_s) {
           if (n > 0) {
-            ok = warp_wait(&q_full[t], loaded & 1);
+            ok = warp_wait(Sh::kPair ? q_tmem : &q_full[t], loaded & 1);
             ++loaded;
           }
           scores(e, n > 0, made, n == 1);
         }
         for (int k = 0; k < n_all && ok; ++k, e += 2) {
-          if (Sh::kOwnP && does_s && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1, k + 2 == n);
+          if ((Sh::kOwnP || Sh::kPair) && does_s && k + 1 < n_all) scores(e + 2, k + 1 < n, made + 1, k + 2 == n);
           if (!does_o) {
             made += k < n;
             continue;
@@ -348,7 +362,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               if (leader) {
 #pragma unroll
                 for (int i = half * (BN / 32); i < (half + 1) * (BN / 32); ++i)
-                  if (i < steps) umma_ts_lo(od, pa + buf_of(made) * 32 + i * 8, va + i * (2048 >> 4), kIdescO, k > 0 || i > 0);
+                  if (i < steps) umma_ts_lo(od, pa + buf_of(made) * Sh::kBuf + i * 8, va + i * (2048 >> 4), kIdescO, k > 0 || i > 0);
               }
             }
             if (!ok) break;
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
             ++made;
           }
           if (leader) umma_commit(&empty[vs]);
-          if (!Sh::kOwnP && k + 1 < n_all) scores(e + 2, k + 1 < n, made, k + 2 == n);
+          if (!Sh::kOwnP && !Sh::kPair && k + 1 < n_all) scores(e + 2, k + 1 < n, made, k + 2 == n);
         }
       }
       // leave only when every product is done
@@ -414,8 +428,35 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     Part g = {};
     // a part's queries into shared memory, as a K-major operand, where they do not come by TMA (group sizes such as 3 or
     // 6); rows past the last are zero
+    int loaded = 0;  // query tiles in TMEM
     auto load_q = [&] {
-      if (a.q_tma || (kPair && wg == 1) || (t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
+      if constexpr (kPair) {  // each warpgroup half of the channels, from where TMA put them or from memory, into TMEM
+        if (g.n_of[0] == 0) return;
+        if (a.q_tma) ok = warp_wait(&q_full[0], loaded & 1);
+        if (!ok) return;
+        const int f = g.f0 + row_t, qi = a.div_g(min(f, g.rows - 1)), head = g.h * a.G + min(f, g.rows - 1) - qi * a.G;
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(g.q0 + qi) * a.q_row + (int64_t)head * a.q_head;
+#pragma unroll 1
+        for (int x = wg * (D / 128); x < (wg + 1) * (D / 128); ++x) {  // 64 channels
+          uint32_t r[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = a.q_tma ? *reinterpret_cast<const uint4*>(smem + x * 16384 + row_t * 128 + ((i ^ (row_t & 7)) << 4))
+                                    : __ldg(reinterpret_cast<const uint4*>(src + x * 64 + i * 8));
+            r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+          }
+          tmem_st32(tmem + lanes + kTmemQ + x * 32, r);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (a.q_tma) mbar_arrive(&q_empty[0]);
+          mbar_arrive(q_tmem);
+        }
+        ++loaded;
+        return;
+      }
+      if (a.q_tma || (t == 0 ? g.n_of[0] : g.n_of[NT - 1]) == 0) return;
       constexpr int kBatch = D == 64 ? 8 : 16;
       constexpr int kChunks = D / 8, kRowsStep = 128 / kChunks;  // 16-byte chunks of a row; rows of one step
       const int c = row_t % kChunks;
@@ -451,7 +492,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     int ends = 0, sums = 0;  // parts written out; of these, with tokens
     bool have = take(g);
     if (have) load_q();
-    while (have) {
+    while (have && ok) {
       if (kPair && ends > 0) {  // O can be written again, and what the warpgroups exchange
         ok = warp_wait(&written[other8], (ends - 1) & 1);
         if (!ok) break;
@@ -483,7 +524,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         float s[BN];
 #pragma unroll
-        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + buf_of(j) * 64 + c, s + c);
+        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + buf_of(j) * Sh::kBuf + c, s + c);
         tmem_wait_ld();
         if constexpr (Sh::kOwnP) {
           tc_fence_before();
@@ -557,7 +598,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               sum[i & 1] = add2(sum[i & 1], y);
               p[i] = pack2<BF16>(y.x, y.y);
             }
-            tmem_st16(tp + buf_of(j) * 32 + c / 2, p);
+            tmem_st16(tp + buf_of(j) * Sh::kBuf + c / 2, p);
           }
           tmem_wait_st();
           tc_fence_before();
@@ -577,6 +618,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         if (((made - 1) & 1) != wg) {
           ok = warp_wait(&m_full[other8], turn_of(made - 1));
           if (!ok) break;
+          tc_fence_after();
           m = *m_other;
           if (m != ml) l *= exp2_fast(ml - m);
         }
@@ -607,6 +649,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       have = take(g);
       if (!ok) break;
       if (have) load_q();
+      if (!ok) break;
       if (n > 0) {
         ok = warp_wait(&o_full[t * Sh::kBufs + buf_of(made - 1)], turn_of(made - 1));
         if (!ok) break;
@@ -685,9 +728,10 @@ cudaError_t launch_tc_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p
 }  // namespace
 
 AttnShape attn_tc_shape(int d, int sms) {
-  const int tile = d == 256 ? 128 * TcShape<256>::kNT : 128 * TcShape<128>::kNT;
-  return {tile, d == 256 ? TcShape<256>::kBN : TcShape<128>::kBN, sms,
-          cta_bytes(tile, d), kTileCost, kMinPart};
+  using Wide = TcShape<256>;
+  using Other = TcShape<128>;
+  if (d == 256) return {128 * Wide::kNT, Wide::kBN, sms, cta_bytes(128 * Wide::kNT, d), Wide::kTileCost, Wide::kMinPart};
+  return {128 * Other::kNT, Other::kBN, sms, cta_bytes(128 * Other::kNT, d), Other::kTileCost, Other::kMinPart};
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {
