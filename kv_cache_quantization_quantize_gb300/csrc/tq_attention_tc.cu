@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     float* const m_own = reinterpret_cast<float*>(sout + warp * Sh::kStage) + lane;
     const float* const m_other = reinterpret_cast<const float*>(sout + other8 * Sh::kStage) + lane;
     float* const l_all = reinterpret_cast<float*>(sout + 8 * Sh::kStage) + row_t;  // [2][128]
-    int ends = 0, sums = 0;  // parts written out; of these, with tokens
+    int ends = 0;  // parts written out
     bool have = take(g);
     if (have) load_q();
     while (have && ok) {
@@ -614,8 +614,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       }
       if (!ok) break;
       made += n;
-      if (kPair && n > 0) {
-        if (((made - 1) & 1) != wg) {
+      if constexpr (kPair) {  // for parts without a unit too: a barrier must not run ahead of the other's wait by two phases
+        if (n > 0 && ((made - 1) & 1) != wg) {
           ok = warp_wait(&m_full[other8], turn_of(made - 1));
           if (!ok) break;
           tc_fence_after();
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         l_all[wg * 128] = l;
         __syncwarp();
         if (lane == 0) mbar_arrive(&l_full[mine8]);
-        ok = warp_wait(&l_full[other8], sums++ & 1);
+        ok = warp_wait(&l_full[other8], ends & 1);
         if (!ok) break;
         l = l_all[0] + l_all[128];
       }

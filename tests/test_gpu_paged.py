@@ -662,3 +662,18 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for i in (0, 1):
         assert all(torch.equal(x, want[i]) for x in got[i])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("some", [[0, 0, 70, 0], [0, 0, 0, 0], [3, 0, 0, 130]])
+def test_many_requests_without_tokens(d, causal, some):
+    """Tiles without a unit between tiles with one: they only write zeros, and what the warps exchange stays in step."""
+    nq = [40, 33, 40, 50] * 150
+    kv = some * 150
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 4, 4, d, torch.float16, False, d)
+    status = i32([0])
+    for _ in range(5):
+        out = paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), causal=causal, max_q=50, status=status)
+        assert status.item() == 0
+    check_rows(out, q, ks, vs, nq, kv, causal, 1 / math.sqrt(d))
