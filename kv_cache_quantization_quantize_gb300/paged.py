@@ -38,7 +38,17 @@ _STRIDES = struct.Struct("@2q")
 
 _I32 = torch.int32
 _HALVES = (torch.bfloat16, torch.float16)
-_alloc, _free = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
+_raw_memory = None  # see _raw_allocator
+
+
+def _raw_allocator():
+    """torch's stream-ordered allocation by raw address: (allocate(size, stream), free(address)). Looked up at the first call, so
+    that the package can be imported with a torch that lacks the two private names; (None, None) there."""
+    global _raw_memory
+    if _raw_memory is None:
+        names = ("_cuda_cudaCachingAllocator_raw_alloc", "_cuda_cudaCachingAllocator_raw_delete")
+        _raw_memory = tuple(getattr(torch._C, n) for n in names) if all(hasattr(torch._C, n) for n in names) else (None, None)
+    return _raw_memory
 
 
 class _On:
@@ -221,12 +231,17 @@ def _attend_here(q, shape, dtype, index, batch, q_starts, max_q, max_kv, softmax
     # Memory of the call's stream, given back to it behind the launches: what comes next on that stream may take it. Without
     # a tensor around it the call takes 11.7 us of the host instead of 17.6.
     size = load().tq_attention_workspace_bytes(queries, kv)
-    ws = _alloc(size, raw) if size else None
+    alloc, free = _raw_memory or _raw_allocator()
+    if alloc is None:
+        ws = torch.empty(size, dtype=torch.uint8, device=q.device)  # the call's stream is current here
+        check(call(queries, kv, batch, ws.data_ptr(), size, raw))
+        return out
+    ws = alloc(size, raw) if size else None
     try:
         check(call(queries, kv, batch, ws, size, raw))
     finally:
         if size:
-            _free(ws)
+            free(ws)
     return out
 
 

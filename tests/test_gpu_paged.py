@@ -677,3 +677,45 @@ def test_many_requests_without_tokens(d, causal, some):
         out = paged.attention(q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv), causal=causal, max_q=50, status=status)
         assert status.item() == 0
     check_rows(out, q, ks, vs, nq, kv, causal, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("d,room", [(64, 3), (128, 60), (256, 60)])
+def test_a_call_with_its_own_workspace_is_captured(d, room):
+    """Without `workspace=` the call's memory is the graph's: replays on new lengths, with other allocations between them, give what
+    a call outside the graph gives."""
+    hq, hkv, kv = 8, 2, [3000, 5000]
+    q, pool, table, rows, ks, vs = paged_inputs([room, room], kv, hq, hkv, d, torch.bfloat16, False, d + room)
+    starts, lens, out = i32([0, room, 2 * room]), i32(kv), torch.zeros_like(q)
+
+    def call(out=None):
+        return paged.attention(q, pool[0], pool[1], table, rows, starts, lens, max_q=room, max_kv=5000, out=out)
+
+    call(out)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g in graphs:
+        with torch.cuda.graph(g):
+            call(out)
+    kept = []
+    for i, (nq, now) in enumerate([([room, 1], [2900, 5000]), ([0, room], [10, 4000]), ([1, 1], [3000, 1]), ([room, room], [100, 4999])]):
+        starts.copy_(i32(starts_of(nq)))
+        lens.copy_(i32(now))
+        kept.append(torch.full((8 << 20,), 7.0, device=DEV))  # what the allocator gives out now is not the graph's
+        graphs[i % 2].replay()
+        check_rows(out, q, ks, vs, nq, now, True, 1 / math.sqrt(d))
+        assert torch.equal(out[:sum(nq)], call()[:sum(nq)])
+    assert all(bool((x == 7).all()) for x in kept)
+
+
+def test_a_workspace_without_the_raw_allocator(monkeypatch):
+    """Where torch lacks raw allocations the workspace is a tensor of the call's stream."""
+    nq, kv = [1, 60], [3000, 5000]
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, 8, 2, 128, torch.bfloat16, False, 77)
+    args = (q, pool[0], pool[1], table, rows, i32(starts_of(nq)), i32(kv))
+    want = paged.attention(*args, max_q=60)
+    monkeypatch.setattr(paged, "_raw_memory", (None, None))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = [paged.attention(*args, max_q=60), paged.attention(*args, max_q=60, stream=side)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)

@@ -1,6 +1,9 @@
 """CPU tests of the exact paged cache's entry points: what the host refuses before any launch."""
 import ctypes
+import os
 import struct
+import subprocess
+import sys
 
 import pytest
 
@@ -127,3 +130,20 @@ def test_the_binding_refuses_cpu_tensors():
     with pytest.raises(ValueError):
         paged.BlockPool(0, 1, 1)
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_the_package_imports_without_the_raw_allocator():
+    """A torch without these two private names (a CPU build) still has the host-only parts."""
+    pytest.importorskip("torch")
+    code = """
+import torch
+for name in ("_cuda_cudaCachingAllocator_raw_alloc", "_cuda_cudaCachingAllocator_raw_delete"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import kv_cache_quantization_quantize_gb300 as tqm
+assert tqm.config(head_dim=64).head_dim == 64
+assert tqm.paged._raw_allocator() == (None, None)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
