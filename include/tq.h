@@ -444,7 +444,10 @@ size_t tq_codec_kv_bytes(int codec, int n_layers, int n_kv_heads, int head_dim, 
  * stack that would pass n_blocks (a block freed twice) is left as it was, with TQ_DEV_ERR_POOL, and so are the
  * tables. Requests with an id outside [0, max_seqs), an id that an earlier request has, or a negative keep are
  * skipped with TQ_DEV_ERR_SEQ_ID (TQ_DEV_ERR_LENGTH for the keep). A table entry outside [-1, n_blocks) becomes -1
- * with TQ_DEV_ERR_BLOCK. batch in [0, 4096]. One launch. */
+ * with TQ_DEV_ERR_BLOCK. batch in [0, 4096]. One launch.
+ * Only the table and the stack change. Packed layers that share the table (tq_block_table_offset) keep the length of
+ * their sequences: a request that ends is emptied there with tq_reset_seqs, and since nothing shortens a packed
+ * sequence, d_keep is for tables without packed layers. */
 tq_status tq_blocks_release(int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride, int32_t* d_free,
                             int n_blocks, int32_t* d_n_free, const int32_t* d_seq_ids, const int32_t* d_keep,
                             int batch, uint32_t* d_status, tq_stream_t stream);
@@ -456,7 +459,7 @@ tq_status tq_blocks_release(int32_t* d_table, int max_seqs, int max_pages, int64
  *     stack, in the order of requests and pages. A page that has one keeps it.
  *   - A request is served if it needs no block, or if the needs of all requests up to and with it fit the free
  *     blocks. A refused one gets no block: its table stays, its slots are -1, its total is 0, and TQ_DEV_ERR_POOL
- *     is set.
+ *     is set. tq_quantize_append on the same table would grow its sequence all the same: its d_n_new has to be 0 there.
  *   - d_starts[batch + 1]: the packed place of each request's first new token; d_starts[batch] is their number.
  *   - d_totals[b]: lens + n_new (0 for a refused or skipped request): the lengths that attention takes.
  *   - d_slots[max_tokens]: block * 128 + place in the block for each packed token; -1 for a token of a request

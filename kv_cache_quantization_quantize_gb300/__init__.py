@@ -4,6 +4,7 @@ PyTorch only provides device memory and streams here. Every step of quantize-on-
 decode attention runs in libtq's kernels; there is no CPU or PyTorch fallback.
 """
 import ctypes
+import weakref
 
 import numpy as np
 import torch
@@ -86,6 +87,27 @@ class HostTables:
         check(self.lib.tq_records_to_page(self.ctx, keys.ctypes.data, values.ctypes.data, keys.shape[0],
                                           page.ctypes.data))
         return page
+
+
+class _PackedPool(paged.BlockPool):
+    """The pool of a TurboQuantCache's block table. Packed layers keep their sequences' lengths and rings on the device and have
+    no way back to an earlier length, so a request ends in them and in the table together, and is not cut back."""
+
+    def __init__(self, cache):
+        cfg = cache.cfg
+        super().__init__(cfg.n_blocks, cfg.max_seqs, cfg.max_ctx, table=cache.block_table)
+        self._cache = weakref.ref(cache)  # the cache holds the pool
+
+    def release(self, seq_ids, keep=None, stream=None):
+        """Ends requests: their blocks return to the pool (see paged.release_blocks) and their sequences are emptied in every
+        packed layer (TurboQuantCache.reset). keep is refused: packed layers would go on attending to the tokens behind it."""
+        if keep is not None:
+            raise ValueError("keep: a pool that packed layers share cannot be cut back; they have no call that shortens a sequence")
+        super().release(seq_ids, None, stream)
+        cache = self._cache()
+        if cache is not None:
+            with torch.cuda.device(self.device):
+                cache.reset(seq_ids, stream=stream)
 
 
 class TurboQuantCache(HostTables):
@@ -233,14 +255,15 @@ class TurboQuantCache(HostTables):
     def block_pool(self):
         """Paged cache: the paged.BlockPool of this cache's block table, made on first use, which is refused once the caller
         has mapped pages itself. Its map() and release() keep the table; exact layers share it through paged.PagedCache.
-        None when not paged."""
+        release() also empties the requests' sequences in every packed layer, and refuses `keep`. A request that map() refuses
+        (its total is 0) has no blocks for its new tokens: give append() no token of it, n_new * (totals > 0), and
+        decode_step() no such row (an id of -1 is skipped, with TQ_DEV_ERR_SEQ_ID). None when not paged."""
         if self.cfg.n_blocks <= 0:
             return None
         if self._pool is None:
-            table = self.block_table
-            if bool((table != -1).any()):
+            if bool((self.block_table != -1).any()):
                 raise ValueError("the block table already maps pages: a pool does not know which blocks are free")
-            self._pool = paged.BlockPool(self.cfg.n_blocks, self.cfg.max_seqs, self.cfg.max_ctx, table=table)
+            self._pool = _PackedPool(self)
         return self._pool
 
     def page(self, layer, slot, head, page):

@@ -15,7 +15,7 @@ One serving step:
     cache.append(layer, k, v, slots)                         # k, v: [tokens, n_kv_heads, head_dim]
     out = cache.attention(layer, q, seq_ids, starts, totals, max_q=..., max_kv=...)
     ...
-    pool.release(seq_ids_of_finished_requests)
+    pool.release(seq_ids_of_finished_requests)               # keep=lengths: back to these, without packed layers
 """
 import ctypes
 import struct
@@ -145,7 +145,8 @@ def _map_blocks(args, ids, batch, max_tokens, out, word, raw, index, device):
 
 
 def release_blocks(table, free, n_free, seq_ids, keep=None, status=None, stream=None):
-    """Gives back the blocks behind each request's first keep[b] tokens, all of them without keep (tq_blocks_release)."""
+    """Gives back the blocks behind each request's first keep[b] tokens, all of them without keep (tq_blocks_release). Only the
+    table and the stack change: what else knows the requests' lengths, such as packed layers, is the caller's."""
     index, args = _map_args(table, free, n_free)
     batch = seq_ids.shape[0]
     ids = _ints("seq_ids", seq_ids, index)
@@ -325,7 +326,8 @@ class BlockPool:
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
 
     def map(self, seq_ids, lens, n_new, max_tokens, out=None, stream=None):
-        """Blocks and slots of a step's new tokens: (slots, starts, totals); see map_blocks."""
+        """Blocks and slots of a step's new tokens: (slots, starts, totals); see map_blocks. The total of a request that is not
+        served is 0."""
         return map_blocks(self.table, self.free, self.n_free, seq_ids, lens, n_new, max_tokens, out, self.status, stream)
 
     def release(self, seq_ids, keep=None, stream=None):

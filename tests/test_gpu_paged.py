@@ -719,3 +719,89 @@ def test_a_workspace_without_the_raw_allocator(monkeypatch):
     got = [paged.attention(*args, max_q=60), paged.attention(*args, max_q=60, stream=side)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got)
+
+
+# ---- packed layers on a shared pool ----
+
+class Shared:
+    """A packed cache on a pool beside one without blocks, fed the same tokens; what both decode has to agree."""
+
+    def __init__(self, n_blocks, seqs=3, layers=2, max_ctx=1024):
+        dims = dict(head_dim=128, n_layers=layers, n_kv_heads=2, n_q_heads=8, max_seqs=seqs, max_ctx=max_ctx, seed=6)
+        self.packed, self.plain = tqm.TurboQuantCache(tqm.config(n_blocks=n_blocks, **dims)), tqm.TurboQuantCache(tqm.config(**dims))
+        self.pool, self.layers, self.seqs = self.packed.block_pool, layers, seqs
+        self.have, self.gen = [0] * seqs, torch.Generator(device=DEV).manual_seed(n_blocks)
+
+    def step(self, ids, count):
+        """Maps and appends count[b] tokens of sequence ids[b]; returns the totals."""
+        n_new = i32(count)
+        _, _, totals = self.pool.map(i32(ids), i32([self.have[i] for i in ids]), n_new, sum(count))
+        served = n_new * (totals > 0)
+        for layer in range(self.layers):
+            k, v = (torch.randn((len(ids), max(count), 2, 128), generator=self.gen, device=DEV).bfloat16() for _ in range(2))
+            for cache in (self.packed, self.plain):
+                cache.append(layer, k, v, i32(ids), served)
+        for i, n in zip(ids, served.tolist()):
+            self.have[i] += n
+        return totals.tolist()
+
+    def check(self):
+        live = [i for i in range(self.seqs) if self.have[i]]
+        q = torch.randn((len(live), 8, 128), generator=self.gen, device=DEV).bfloat16()
+        for layer in range(self.layers):
+            assert [self.packed.state(layer, i)[0] for i in range(self.seqs)] == self.have
+            assert torch.equal(self.packed.decode(layer, q, i32(live)), self.plain.decode(layer, q, i32(live)))
+        assert self.packed.check_status() == 0
+
+
+def test_a_released_slot_starts_anew_in_packed_layers():
+    s = Shared(12)
+    s.step([0, 1, 2], [200, 130, 300])
+    s.check()
+    side = torch.cuda.Stream()
+    for stream, ended in ((None, [1]), (side, [2, 0])):
+        side.wait_stream(torch.cuda.current_stream())
+        s.pool.release(i32(ended + [-1]), stream=stream)
+        torch.cuda.current_stream().wait_stream(side)
+        s.plain.reset(i32(ended))
+        for i in ended:
+            s.have[i] = 0
+        assert s.pool.check_status() == paged.TQ_DEV_ERR_SEQ_ID  # of the id -1
+        s.check()
+        s.step(ended, [140, 257][:len(ended)])
+        s.check()
+    assert s.pool.n_free.item() == 12 - sum(ref.pages(h) for h in s.have) and s.pool.check_status() == 0
+
+
+def test_packed_layers_are_not_cut_back():
+    s = Shared(12)
+    s.step([0, 1, 2], [200, 130, 300])
+    table, n_free = s.pool.table.clone(), s.pool.n_free.item()
+    with pytest.raises(ValueError):
+        s.pool.release(i32([0]), keep=i32([100]))
+    assert torch.equal(s.pool.table, table) and s.pool.n_free.item() == n_free
+    s.check()
+
+
+def test_a_refused_request_does_not_grow_packed_layers():
+    s = Shared(5)
+    assert s.step([0, 1], [200, 129]) == [200, 129]  # four blocks
+    s.check()
+    assert s.step([0, 2, 1], [40, 150, 1]) == [240, 0, 130]  # two would be needed, one is left
+    assert s.pool.check_status() == paged.TQ_DEV_ERR_POOL
+    s.check()
+    s.pool.release(i32([1]))
+    s.plain.reset(i32([1]))
+    s.have[1] = 0
+    assert s.step([2, 0], [150, 1]) == [150, 241]
+    s.check()
+    assert s.pool.check_status() == 0
+
+
+def test_a_pool_outlives_its_packed_cache():
+    s = Shared(5)
+    pool = s.pool
+    s.step([0], [200])
+    del s
+    pool.release(i32([0]))
+    assert pool.n_free.item() == 5 and pool.check_status() == 0
