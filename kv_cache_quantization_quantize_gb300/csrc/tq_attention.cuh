@@ -123,6 +123,18 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// Two results in the cache's type. A result is an average of values, so a finite one past f16's largest number is there
+// by the rounding of weights alone (up to 2^-11 of it; the next number is already infinite): it is that number.
+template <bool BF16>
+__device__ __forceinline__ uint32_t result2(float lo, float hi) {
+  if constexpr (!BF16) {
+    constexpr float kMost = 65504.f;
+    if (fabsf(lo) > kMost && fabsf(lo) < INFINITY) lo = copysignf(kMost, lo);
+    if (fabsf(hi) > kMost && fabsf(hi) < INFINITY) hi = copysignf(kMost, hi);
+  }
+  return pack2<BF16>(lo, hi);
+}
+
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w,
                                             uint64_t* bar) {
   asm volatile(

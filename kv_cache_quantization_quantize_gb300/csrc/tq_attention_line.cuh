@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(JoinShape<T>::kWarps * 32) k_attn_join(const _
     uint16_t* dst = static_cast<uint16_t*>(a.out) + (int64_t)(c.q0 + qi) * a.o_row + (int64_t)head * a.o_head + lane * V;
     uint32_t out[V / 2];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) out[i] = pack2<BF16>(acc[j][2 * i] * inv, acc[j][2 * i + 1] * inv);
+    for (int i = 0; i < V / 2; ++i) out[i] = result2<BF16>(acc[j][2 * i] * inv, acc[j][2 * i + 1] * inv);
     if constexpr (V == 2) *reinterpret_cast<uint32_t*>(dst) = out[0];
     else if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(out[0], out[1]);
     else *reinterpret_cast<uint4*>(dst) = make_uint4(out[0], out[1], out[2], out[3]);

@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
                           warp * (D / 4) + c2;
 #pragma unroll
           for (int i = 0; i < 2 * NP; ++i)
-            *reinterpret_cast<uint32_t*>(dst + i * 8) = pack2<BF16>(o[t][i][2 * x] * inv, o[t][i][2 * x + 1] * inv);
+            *reinterpret_cast<uint32_t*>(dst + i * 8) = result2<BF16>(o[t][i][2 * x] * inv, o[t][i][2 * x + 1] * inv);
         } else {
           float* po = cut_o<R, D>(a, gridDim.x, blockIdx.x, g.slot) + row * D + warp * (D / 4) + c2;
 #pragma unroll

@@ -676,8 +676,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           if (direct) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              v[4 * x + i] = make_uint4(pack2<BF16>(o[8 * i], o[8 * i + 1]), pack2<BF16>(o[8 * i + 2], o[8 * i + 3]),
-                                        pack2<BF16>(o[8 * i + 4], o[8 * i + 5]), pack2<BF16>(o[8 * i + 6], o[8 * i + 7]));
+              v[4 * x + i] = make_uint4(result2<BF16>(o[8 * i], o[8 * i + 1]), result2<BF16>(o[8 * i + 2], o[8 * i + 3]),
+                                        result2<BF16>(o[8 * i + 4], o[8 * i + 5]), result2<BF16>(o[8 * i + 6], o[8 * i + 7]));
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

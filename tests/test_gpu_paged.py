@@ -805,3 +805,31 @@ def test_a_pool_outlives_its_packed_cache():
     del s
     pool.release(i32([0]))
     assert pool.n_free.item() == 5 and pool.check_status() == 0
+
+
+# ---- the largest values and scores ----
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,m", [(1, 200), (1, 9000), (200, 200), (200, 9000)])
+def test_averages_of_f16s_largest_value_are_finite(d, sign, n, m):
+    """Weights of 1 and of 2^-1 (1 + 2^-11 + 2^-13), which rounds up by almost 2^-11 of itself, of values of 65504: unclamped the
+    results would pass 65520, where f16 rounds to infinity. Few and many rows, tiles in one CTA and in several."""
+    q = torch.zeros((n, 4, d), dtype=torch.float16, device=DEV)
+    k = torch.zeros((m, 2, d), dtype=torch.float16, device=DEV)
+    q[..., 0] = 1
+    k[torch.arange(m, device=DEV) % 16 != 0, :, 0] = -1
+    v = torch.full_like(k, 65504.0 * sign)
+    scale = (1 - math.log2(1 + 2 ** -11 + 2 ** -13)) * math.log(2)
+    out = paged.cross_attention(q, k, v, i32([0, n]), kv_starts=i32([0, m]), softmax_scale=scale, max_q=n, max_kv=m)
+    check_rows(out, q, [k], [v], [n], [m], False, scale)
+
+
+def test_infinite_values_stay_infinite():
+    k = torch.zeros((40, 2, 64), dtype=torch.float16, device=DEV)
+    q, v = torch.zeros((20, 4, 64), dtype=torch.float16, device=DEV), torch.ones_like(k)
+    v[3, 0, 5], v[3, 1, 6] = math.inf, -math.inf
+    for n in (1, 20):
+        out = paged.cross_attention(q[:n], k, v, i32([0, n]), kv_starts=i32([0, 40]), max_q=n)
+        assert bool((out[:, :2, 5] == math.inf).all()) and bool((out[:, 2:, 6] == -math.inf).all())
+        assert int(torch.isinf(out).sum()) == 4 * n
