@@ -29,6 +29,9 @@ namespace {
 // them in 512 cycles, beside 32 KB of K, 32 KB of V and 64 KB that arrive (2048 queries after 14336 tokens: 376 us with
 // the queries there, 345 so).
 constexpr uint32_t kTmemQ = 128;
+// Scores (times log2 e) past this are 2 and more apart in fp32 and take steps of their own: 8192 queries on as many tokens
+// took 253.2 us without them at D = 64 and take 254.1 (causal 142.8 and 144.7), 619 and 623 at D = 128, 204 at D = 256.
+constexpr float kFar = 16777216.f;
 
 template <int D>
 struct TcShape {
@@ -510,7 +513,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const int lim_all = seen(a, r, a.div_g(min(g.f0 + t * 128, g.rows - 1)));
       const int u0 = g.u0;
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
-      float m = mine ? -INFINITY : INFINITY, l = 0.f;  // a row past the last never outgrows its maximum
+      float m = mine ? -INFINITY : kFar, l = 0.f;  // a row past the last never outgrows its maximum (or does so for nothing)
       float ml = m;  // what l is relative to (kPair; else m)
       for (int k = kPair ? (made ^ wg) & 1 : 0; k < n; k += kPair ? 2 : 1) {
         const int j = made + k, bi = t * Sh::kBufs + buf_of(j);
@@ -561,28 +564,39 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           ml = mn;
         }
         const bool grew = mn != m && m != -INFINITY;
-        const bool rescale = __any_sync(0xffffffffu, grew);
+        float mu = mn == -INFINITY ? 0.f : mn;
+        const bool far = fabsf(mu) > kFar;
+        const bool special = __any_sync(0xffffffffu, grew || far);
         // O_t is whole before it is rescaled, and P_t has been used before it is written again
-        const int last = rescale ? j - 1 : Sh::kOwnP ? j - Sh::kBufs : -1;
+        const int last = special ? j - 1 : Sh::kOwnP ? j - Sh::kBufs : -1;
         if (last >= 0) {
           ok = warp_wait(&o_full[t * Sh::kBufs + buf_of(last)], turn_of(last));
           if (!ok) break;
           tc_fence_after();
         }
-        if (rescale) {
-          const float alpha = grew ? exp2_fast(m - mn) : 1.f;
-          if constexpr (!kPair) l *= alpha;
+        if (special) {
+          if (__any_sync(0xffffffffu, grew)) {
+            const float alpha = grew ? exp2_fast(m - mn) : 1.f;
+            if constexpr (!kPair) l *= alpha;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + c, o);
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(to + c, o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(to + c, o);
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tmem_st32(to + c, o);
+            }
+          }
+          // s * scale - mu in one rounding is off by what mu was rounded by, the same for all tokens of the row. Past kFar
+          // it would leave the weights' range: there the scores are rounded as mu was, and then taken from it.
+          if (__any_sync(0xffffffffu, far)) {
+            const float back = 1.f / a.scale_log2;
+#pragma unroll
+            for (int c = 0; c < BN; ++c) s[c] = __fsub_rn(__fmul_rn(s[c], a.scale_log2), mu) * back;
+            mu = 0.f;
           }
         }
         m = mn;
-        const float mu = m == -INFINITY ? 0.f : m;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-mu, -mu);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll

@@ -833,3 +833,29 @@ def test_infinite_values_stay_infinite():
         out = paged.cross_attention(q[:n], k, v, i32([0, n]), kv_starts=i32([0, 40]), max_q=n)
         assert bool((out[:, :2, 5] == math.inf).all()) and bool((out[:, 2:, 6] == -math.inf).all())
         assert int(torch.isinf(out).sum()) == 4 * n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("n,causal", [(1, False), (90, False), (90, True), (400, True)])
+def test_scores_far_from_zero_pick_one_token(dtype, d, sign, n, causal):
+    """Scores of 2^31 and more, all exact in fp32 and 2^20 or more apart: the largest has all the weight, so each result is a row of
+    V, whichever kernel makes it. An fp32 score has no place for the difference from its maximum there unless both are rounded
+    alike."""
+    few = dtype == torch.bfloat16  # distinct whole numbers that the type holds: of 8 bits, of 11 bits
+    m, low = (110, 128) if few else (1400, 512)
+    n = min(n, m)
+    gen = torch.Generator(device=DEV).manual_seed(d + n)
+    size = 2.0 ** 18 if few else 16.0
+    c = torch.randperm(m, generator=gen, device=DEV) + low
+    k = (c * size)[:, None, None].expand(m, 2, d).to(dtype).contiguous()
+    q = torch.full((n, 8, d), sign * (2.0 ** 18 if few else 2.0 ** 15), dtype=dtype, device=DEV)
+    v = torch.randn((m, 2, d), generator=gen, device=DEV).to(dtype)
+    pool = torch.zeros((2, ref.pages(m), 128, 2, d), dtype=dtype, device=DEV)
+    pool[0].view(-1, 2, d)[:m], pool[1].view(-1, 2, d)[:m] = k, v
+    table = torch.arange(ref.pages(m), dtype=torch.int32, device=DEV)[None]
+    out = paged.attention(q, pool[0], pool[1], table, None, i32([0, n]), i32([m]), causal=causal, max_q=n, max_kv=m)
+    for i, see in enumerate(visible_of(n, m, causal)):
+        top = int((sign * c[:see]).argmax())
+        assert torch.equal(out[i], v[top].repeat_interleave(4, 0)), i
