@@ -499,8 +499,8 @@ tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dt
                           tq_stream_t stream);
 
 /* Queries and outputs of attention: packed rows [n_rows][n_q_heads][head_dim] of the cache's type at strides
- * {row, head} in elements, 16-byte aligned rows. Rows [d_q_starts[b], d_q_starts[b + 1]) are request b's; what
- * other rows hold does not matter, and they are not written. out may be q itself. Query head h attends KV head
+ * {row, head} in elements, 16-byte aligned rows (the stride of a size of 1 can be any). Rows [d_q_starts[b],
+ * d_q_starts[b + 1]) are request b's; what other rows hold does not matter, and they are not written. out may be q itself. Query head h attends KV head
  * h / (n_q_heads / n_kv_heads); the quotient can be any whole number up to 1024. */
 typedef struct tq_queries {
   const void* q;

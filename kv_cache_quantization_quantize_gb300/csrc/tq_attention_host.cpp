@@ -139,8 +139,9 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
   if (!q->batch || !q->n_rows) return TQ_OK;
   if (!q->q || !q->out || !q->d_q_starts) return fail(TQ_ERR_INVALID_ARG, "q, out or d_q_starts is NULL");
   if (!aligned(q->q, 16) || !aligned(q->out, 16)) return fail(TQ_ERR_INVALID_ARG, "q and out have to be 16-byte aligned");
+  const int size[2] = {q->n_rows, q->n_q_heads};  // the stride of a size of 1 is never taken
   for (int i = 0; i < 2; ++i)
-    if (q->q_strides[i] % 8 || q->out_strides[i] % 8)
+    if (size[i] > 1 && (q->q_strides[i] % 8 || q->out_strides[i] % 8))
       return fail(TQ_ERR_INVALID_ARG, "strides of q and out: multiples of 8 elements");
   return TQ_OK;
 }

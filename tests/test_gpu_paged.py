@@ -859,3 +859,21 @@ def test_scores_far_from_zero_pick_one_token(dtype, d, sign, n, causal):
     for i, see in enumerate(visible_of(n, m, causal)):
         top = int((sign * c[:see]).argmax())
         assert torch.equal(out[i], v[top].repeat_interleave(4, 0)), i
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (40, 1), (1, 1)])
+def test_strides_of_a_single_row_or_head_are_not_taken(heads):
+    """One row of a projection that is not a multiple of 8 wide (few rows, and 40 heads on one: the other kernel); one head."""
+    hq, hkv = heads
+    n, d, m = (3 if hq == 1 else 1), 128, 700
+    q, pool, table, rows, ks, vs = paged_inputs([n], [m], hq, hkv, d, torch.bfloat16, False, hq)
+    if hq == 1:
+        q = torch.as_strided(q.contiguous(), (n, 1, d), (d, 3, 1))
+        out = torch.as_strided(torch.zeros_like(q, memory_format=torch.contiguous_format), (n, 1, d), (d, 5, 1))
+    else:
+        wide = torch.zeros((1, hq * d + 3), dtype=q.dtype, device=DEV)
+        wide[:, :hq * d] = q.reshape(1, hq * d)
+        q = torch.as_strided(wide, (1, hq, d), (hq * d + 3, d, 1))
+        out = torch.as_strided(torch.zeros_like(q, memory_format=torch.contiguous_format), (1, hq, d), (hq * d + 3, d, 1))
+    paged.attention(q, pool[0], pool[1], table, rows, i32([0, n]), i32([m]), max_q=n, max_kv=m, out=out)
+    check_rows(out, q, ks, vs, [n], [m], True, 1 / math.sqrt(d))

@@ -147,3 +147,12 @@ assert tqm.paged._raw_allocator() == (None, None)
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("over", [{"rows": 1, "qs": (1027, 64), "os": (3, 64)}, {"heads": 1, "batch": 1, "qs": (64, 7), "os": (64, 1)}])
+def test_strides_of_a_single_row_or_head_are_not_checked(over):
+    """What comes next is the device or the workspace, whichever this machine lacks."""
+    lib = _abi.load()
+    lib.tq_paged_attention(queries(**over), kv(heads=1), P, 4, 4, 4, None, P, 1, None, 0, None, None)
+    text = lib.tq_last_error().decode()
+    assert "workspace" in text or "device" in text, text
