@@ -877,3 +877,27 @@ def test_strides_of_a_single_row_or_head_are_not_taken(heads):
         out = torch.as_strided(torch.zeros_like(q, memory_format=torch.contiguous_format), (1, hq, d), (hq * d + 3, d, 1))
     paged.attention(q, pool[0], pool[1], table, rows, i32([0, n]), i32([m]), max_q=n, max_kv=m, out=out)
     check_rows(out, q, ks, vs, [n], [m], True, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("hkv,batch,causal,most_q,most_kv", [
+    (2, 16, True, 1, 3000), (2, 16, False, 3, 3000), (8, 64, True, 1, 600), (8, 64, True, 3, 30), (2, 24, True, 200, 3000), (2, 24, False, 60, 3000),
+    (8, 64, True, 30, 600)])
+def test_a_table_of_the_most_pages(d, hkv, batch, causal, most_q, most_kv):
+    """2^20 pages, most of them without a block: by their number a request could have 2^27 tokens, 2^20 units of 128 or 2^21 of 64.
+    So the line of work would pass 2^30, and its costs are 4 (16 requests of one token) to 128 times as coarse; the cuts and
+    the joins follow from them."""
+    gen = torch.Generator().manual_seed(batch + most_q + d)
+    nq = torch.randint(1, most_q + 1, (batch,), generator=gen).tolist()
+    kv = torch.randint(0, most_kv + 1, (batch,), generator=gen).tolist()
+    kv[0] = most_kv
+    hq = 4 * hkv
+    q, pool, table, rows, ks, vs = paged_inputs(nq, kv, hq, hkv, d, torch.bfloat16, False, d + batch, tail=1)
+    wide = torch.full((table.shape[0], 1 << 20), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = table
+    for hint in (0, most_kv):
+        status, out = i32([0]), torch.full(q.shape, 9.0, dtype=q.dtype, device=DEV)
+        paged.attention(q, pool[0], pool[1], wide, rows, i32(starts_of(nq)), i32(kv), causal=causal, max_q=max(nq), max_kv=hint, out=out, status=status)
+        assert status.item() == 0
+        check_rows(out, q, ks, vs, nq, kv, causal, 1 / math.sqrt(d))
+        assert bool((out[sum(nq):] == 9).all())
