@@ -444,7 +444,7 @@ size_t tq_codec_kv_bytes(int codec, int n_layers, int n_kv_heads, int head_dim, 
  * stack that would pass n_blocks (a block freed twice) is left as it was, with TQ_DEV_ERR_POOL, and so are the
  * tables. Requests with an id outside [0, max_seqs), an id that an earlier request has, or a negative keep are
  * skipped with TQ_DEV_ERR_SEQ_ID (TQ_DEV_ERR_LENGTH for the keep). A table entry outside [-1, n_blocks) becomes -1
- * with TQ_DEV_ERR_BLOCK. batch in [0, 4096]. One launch.
+ * with TQ_DEV_ERR_BLOCK. batch in [0, 4096], n_blocks in [1, 2^24 - 1]. One launch.
  * Only the table and the stack change. Packed layers that share the table (tq_block_table_offset) keep the length of
  * their sequences: a request that ends is emptied there with tq_reset_seqs, and since nothing shortens a packed
  * sequence, d_keep is for tables without packed layers. */
@@ -467,7 +467,7 @@ tq_status tq_blocks_release(int32_t* d_table, int max_seqs, int max_pages, int64
  *   - A request with an id outside [0, max_seqs) or that an earlier request has (TQ_DEV_ERR_SEQ_ID), a negative
  *     length or count, more than max_pages pages, or an end past max_tokens (TQ_DEV_ERR_LENGTH) is not served; its
  *     tokens keep their places (none for a negative count), and starts never pass max_tokens.
- * batch in [0, 4096], n_blocks <= 2^24. One launch. */
+ * batch in [0, 4096], n_blocks in [1, 2^24 - 1]. One launch. */
 tq_status tq_blocks_map(int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride, const int32_t* d_free,
                         int n_blocks, int32_t* d_n_free, const int32_t* d_seq_ids, const int32_t* d_lens,
                         const int32_t* d_n_new, int batch, int32_t* d_starts, int32_t* d_totals, int32_t* d_slots,

@@ -4,9 +4,12 @@
 // as it is estimated to cost, in 64ths of a unit (2^a.shift of them where a launch's line would pass 2^30): its tokens
 // and a fixed cost for its start and end. CTA c takes
 // [c Q, (c + 1) Q); a tile that is cut there has its units divided in proportion, and the parts are joined by
-// k_attn_join. So every SM gets the same amount of work whatever the lengths are, at most two cut tiles per CTA go
+// k_attn_join. So CTAs get nearly the same amount of work whatever the lengths are, at most two cut tiles per CTA go
 // through memory, and the host needs no lengths. Costs have closed sums, so finding a place takes one pass over the
-// requests.
+// requests. What a cut adds, a second start and end and the join's bytes, is not in the costs, and a piece can be as short
+// as one unit: in long work that is lost in the rest, short work pays for it (8 ragged prompts of 20 heads have 135 cut
+// tiles in 270 pieces on 152 CTAs, 114 of the pieces of 3 units or less; 16 single tokens against 700 to 1500 states of 16 heads
+// have all 256 tiles cut).
 #pragma once
 
 #include <atomic>

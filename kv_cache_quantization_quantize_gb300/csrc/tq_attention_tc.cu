@@ -430,7 +430,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     int turns = 0;  // units that both tiles have made
     Part g = {};
     // a part's queries into shared memory, as a K-major operand, where they do not come by TMA (group sizes such as 3 or
-    // 6); rows past the last are zero
+    // 6), with zeros in rows past the last; with kPair into TMEM, from either place, where such rows repeat the last one
+    // or hold what TMA brought
     int loaded = 0;  // query tiles in TMEM
     auto load_q = [&] {
       if constexpr (kPair) {  // each warpgroup half of the channels, from where TMA put them or from memory, into TMEM
