@@ -14,9 +14,10 @@ namespace {
 // and tells whether a maximum outgrew its range (kLazy), which is rare after a tile's first unit. Scores and sums run
 // on mma.sync m16n8k16: at 16 or 32 rows the tensor pipe has a fifth of its time's work, and its register operands
 // need no copies.
-// Measured (GB300, 32 query heads on 8 KV heads, head_dim 128, bf16): 4 x 32768 tokens 83 us, 6.4 TB/s (97 % of a
-// measured copy); one sequence of 131072 tokens 86 us; of 32768 30 us, of which about 4 us are the way to the first
-// load, 4 us the join and 20 us the bytes. A unit takes 930 cycles of a CTA, its bytes 2900 of an SM's share of DRAM.
+// Measured (GB300, 32 query heads on 8 KV heads, head_dim 128, bf16, with the join): 4 x 32768 tokens 86 us, 6.2 TB/s, 93 %
+// of a measured copy (the kernel alone 84 us); one sequence of 131072 tokens 88 us; of 32768 30 to 34 us, of which about 4 us
+// are the way to the first load, 4 us the join and 20 us the bytes. A unit takes 930 cycles of a CTA, its bytes 2900 of an
+// SM's share of DRAM.
 // =============================================================================================
 constexpr int kRowsThreads = 160;  // four consumer warps, one producer warp
 constexpr int kTileCost = 64;      // start and end of a tile, as one unit

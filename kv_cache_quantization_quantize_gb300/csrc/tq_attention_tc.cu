@@ -17,13 +17,15 @@ namespace {
 //     2^8, far inside fp32 and f16, and the final division takes the factor out.
 // The two tiles alternate: while one's softmax runs, the tensor pipe works for the other. One tile has both warpgroups:
 // they take its units in turn and hand each row's maximum on through shared memory; row sums meet at the end.
-// Measured (GB300, bf16, 32 query heads on 8 KV heads, head_dim 128): 8192 queries on 8192 tokens without a mask 619 us,
-// 1777 TFLOP/s (93 % of a measured cuBLAS burst); causal 351 to 368 us, 1495 to 1566 TFLOP/s; 2048 queries after 30720
-// tokens 690 us, 1545 TFLOP/s. A unit of both tiles takes 2500 cycles there, its four products 2048. Head_dim 64 is bound
-// by the softmax (8192 x 8192, 16 heads: 1097 TFLOP/s without a mask; 583 instructions per row's thread and unit, at 2
-// warps per scheduler), head_dim 256 by K and V, which pass shared memory for 128 rows only: 64 KB a unit, whose products
-// take 1024 cycles and which takes about 1700 (4096 x 4096, 16 heads: 204 us, 1350 TFLOP/s without a mask; causal 123 us,
-// 1120; 2048 queries after 14336 tokens 345 to 358 us, 1440 to 1490).
+// Measured (GB300, bf16, calls back to back on one input of random values; the ranges are of several boxes), 32 query heads
+// on 8 KV heads, head_dim 128: 8192 queries on 8192 tokens without a mask 618 to 632 us, 1740 to 1780 TFLOP/s (91 to 93 % of
+// a measured cuBLAS burst); causal 338 to 368 us, 1495 to 1628; 2048 queries after 30720 tokens 629 to 646 us, 1650 to 1695
+// (708 us where keys have strong channels and inputs change from call to call). A unit of both tiles takes 2500 cycles
+// there, its four products 2048. Head_dim 64 is bound by the softmax, at 2 warps per scheduler: a unit takes 2290 cycles, its
+// products 1024 (8192 x 8192, 16 heads: 254 us, 1083 TFLOP/s without a mask; causal 144.5 us, 951). Head_dim 256 is bound by
+// K and V, which pass shared memory for 128 rows only: 64 KB a unit, whose products take 1024 cycles and which takes about
+// 1750 (4096 x 4096, 16 heads on 4: 204 us, 1350 TFLOP/s without a mask; causal 123 to 126 us, 1090 to 1120; 2048 queries
+// after 14336 tokens 345 to 372 us, 1385 to 1490).
 // =============================================================================================
 // kPair: the queries are an operand in TMEM, in these columns. From shared memory, 64 tokens' scores would read 64 KB of
 // them in 512 cycles, beside 32 KB of K, 32 KB of V and 64 KB that arrive (2048 queries after 14336 tokens: 376 us with
@@ -62,7 +64,7 @@ struct TcShape {
   static constexpr uint32_t kO = D == 64 ? 384 : 256;
   // At D = 128 the tiles' softmaxes take turns: left alone they fall into step, share the special function units and
   // then leave the tensor pipe idle together (2900 cycles per unit against 2500; the SMs differed by 30 %). At D = 64
-  // the special function units are the bound and turns only add waits (1670 against 2290 cycles per unit).
+  // the softmax is the bound and turns only add waits (2290 cycles per unit without them, 2900 with).
   static constexpr bool kTurns = D == 128;
 };
 
