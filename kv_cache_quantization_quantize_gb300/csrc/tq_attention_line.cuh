@@ -113,8 +113,11 @@ struct Walk {
   // The next tile of which this CTA has a part; cut is filled for one that it begins and does not end.
   __device__ __forceinline__ bool next(const AttnArgs& a, Part& g, CutTile& cut) {
     for (;;) {
+      // Behind this CTA's part there is nothing to find: 1020 requests without queries behind 4 with one each, as in a padded
+      // batch, made 15 us 108.
+      if (s >= p1) break;
       settle(a);  // here and not behind the last tile: a part is given out before the next request is read
-      if (b >= a.batch || s >= p1) break;
+      if (b >= a.batch) break;
       g.f0 = t * T;
       g.rows = rows;
       g.kv = tile_kv(a, r, t, T);
