@@ -521,7 +521,8 @@ typedef struct tq_queries {
  * With causal = 1, query i sits at position kv_len - n + i and sees every token up to its own; with causal = 0 it
  * sees all kv_len. softmax(scale q k) v in fp32 statistics; the weights are rounded to the cache's type for the
  * product with V, the result once. A query that sees no token gets zeros. Pages may hold anything, also NaN,
- * behind a request's tokens; a token that some query of the request sees has to be finite.
+ * behind a request's tokens; a token that some query of the request sees has to be finite. Sums are fp32, of weights
+ * up to 2^8: bf16 values have to be small enough that 2^8 x tokens x |v| stays below 2^128.
  * A page without a block in the table reads as zeros (TQ_DEV_ERR_BLOCK); a bad id, length or start makes the
  * request's outputs zeros or unwritten (TQ_DEV_ERR_SEQ_ID, TQ_DEV_ERR_LENGTH).
  *   - K and V: base and strides a multiple of 16 bytes, positive (also where a size is 1, if read).
