@@ -55,7 +55,12 @@ typedef enum tq_status {
   TQ_ERR_DEVICE = 5 /* the device status word is non-zero (see tq_check_status) */
 } tq_status;
 
-typedef enum tq_dtype { TQ_BF16 = 0, TQ_F32 = 1, TQ_F16 = 2 /* exact pools and attention only */ } tq_dtype;
+typedef enum tq_dtype {
+  TQ_BF16 = 0,
+  TQ_F32 = 1,
+  TQ_F16 = 2, /* exact pools and attention only */
+  TQ_E4M3 = 3 /* pools of 8 bits only */
+} tq_dtype;
 
 /* Device status word bits. */
 #define TQ_DEV_ERR_CAPACITY 0x1u /* an append would grow a sequence past max_ctx; the row was skipped */
@@ -485,7 +490,7 @@ typedef struct tq_kv {
   int32_t tokens;
   int32_t n_kv_heads;
   int32_t head_dim; /* 64, 128 or 256 */
-  int32_t dtype;    /* TQ_BF16 or TQ_F16 */
+  int32_t dtype;    /* TQ_BF16 or TQ_F16; TQ_E4M3 where a call takes scales */
 } tq_kv;
 
 /* tq_paged_append: writes n_tokens new rows of K and V into a pool: row t goes to block slots[t] / 128, place
@@ -497,6 +502,76 @@ typedef struct tq_kv {
 tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dtype dt, const int64_t* k_strides,
                           const int64_t* v_strides, const int32_t* d_slots, int n_tokens, uint32_t* d_status,
                           tq_stream_t stream);
+
+/* ---- Rotary positions, and a step's new tokens rotated on their way into a paged cache of 16 or 8 bits ---- */
+
+/* Angles of rotary positions. The first rotary_dim channels of a head are rotary_dim / 2 pairs: (i, i + rotary_dim / 2), or
+ * with interleaved = 1 (2 i, 2 i + 1). At position p, pair i becomes factor * (a cos w - b sin w, b cos w + a sin w) with
+ * w = 2 pi p turns[i]; the channels behind stay. turns are given in units of 2^-64 (modulo 1: a position is a whole
+ * number), so that the angle of any position in int32 is taken modulo a turn without error, and cosines and sines
+ * are good to about 1e-7 however far the position is. */
+typedef struct tq_rotary {
+  const uint64_t* d_turns; /* [rotary_dim / 2], on the device, 8-byte aligned */
+  int32_t rotary_dim;      /* a multiple of 8, at most head_dim */
+  int32_t interleaved;
+  float factor;            /* 1, or what a scaling to longer contexts multiplies with */
+} tq_rotary;
+
+/* tq_rotate: out = rotated x for n_tokens rows of n_heads heads of head_dim channels (a multiple of 8, at most 1024), of
+ * type dt (TQ_BF16, TQ_F16 or TQ_F32) at strides {row, head} in elements; row t has position d_positions[t]. The
+ * arithmetic is fp32, the result is rounded once. inverse = 1 takes the angles with the other sign, still times factor:
+ * the transposed map, which is the gradient's. out may be x itself (with its strides); it may not overlap it otherwise.
+ * Any alignment is served; 16-byte aligned rows with rotary_dim and head_dim multiples of 16 are faster. One launch. */
+tq_status tq_rotate(const tq_rotary* rot, const void* x, void* out, tq_dtype dt, const int64_t* x_strides,
+                    const int64_t* out_strides, const int32_t* d_positions, int n_tokens, int n_heads, int head_dim,
+                    int inverse, tq_stream_t stream);
+
+/* Scales of a cache of 8 bits (tq_kv of type TQ_E4M3): a number x of block o, head h stands for x * k[o * k_block + h] (v
+ * for the values). tq_paged_extend writes powers of two between 2^-60 and 2^60. */
+typedef struct tq_scales {
+  float* k;
+  float* v;
+  int64_t k_block; /* entries from one block to the next */
+  int64_t v_block;
+} tq_scales;
+
+/* New rows of K and V, and of queries that are rotated beside them (q NULL: none): packed rows [n_rows][heads][head_dim] of
+ * type dtype at strides {row, head} in elements. */
+typedef struct tq_new_rows {
+  const void* k;
+  const void* v;
+  const void* q;
+  void* q_out;
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+  int64_t q_strides[2];
+  int64_t q_out_strides[2];
+  const int32_t* d_positions; /* [n_rows] positions to rotate by; NULL: the tokens' places in their requests */
+  int32_t n_rows;
+  int32_t n_q_heads;
+  int32_t dtype; /* TQ_BF16, TQ_F16 or TQ_F32 */
+} tq_new_rows;
+
+/* tq_paged_extend: the new tokens of a step into a pool, K rotated on the way. Request b's new rows are
+ * [d_starts[b], d_starts[b + 1]); they are the last of its d_totals[b] tokens, in the pages of table row d_seq_ids[b] (NULL: b),
+ * all as tq_blocks_map gives them. A request with total 0 is skipped, and so are rows behind the last request.
+ *   - rot NULL: K is not rotated. q is rotated as K is, into q_out (which may be q), its type kept; rows of requests
+ *     that are not served stay as they are.
+ *   - A pool of TQ_BF16 or TQ_F16 (scales NULL): each value is rounded once. One launch.
+ *   - A pool of TQ_E4M3: for each block and head that gets tokens, the scale is the smallest power of two in
+ *     [2^-60, 2^60] with which the largest finite value of the new tokens is at most 448 scales, and no less than the
+ *     scale that the block has, if it holds earlier tokens of the request (its first new token is not its first); then the
+ *     numbers of those are brought to the new scale. Values are rounded to nearest even; one past 448 scales becomes
+ *     that, NaN stays NaN. A block's scale is that of the tokens in it, so two requests must not extend one block.
+ *     Base and strides of the pool: multiples of 16. One launch.
+ *   - Not served, with a status bit: ids outside [0, max_seqs) (TQ_DEV_ERR_SEQ_ID); starts that fall or pass n_rows, a
+ *     total below the number of new rows or past max_pages pages (TQ_DEV_ERR_LENGTH); pages without a block in the
+ *     pool (TQ_DEV_ERR_BLOCK: the page's tokens alone).
+ * batch in [0, 65535]. The host reads no array; calls can be captured. */
+tq_status tq_paged_extend(const tq_kv* pool, const tq_scales* scales, const tq_new_rows* rows, const tq_rotary* rot,
+                          const int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride,
+                          const int32_t* d_seq_ids, const int32_t* d_starts, const int32_t* d_totals, int batch,
+                          uint32_t* d_status, tq_stream_t stream);
 
 /* Queries and outputs of attention: packed rows [n_rows][n_q_heads][head_dim] of the cache's type at strides
  * {row, head} in elements, 16-byte aligned rows (the stride of a size of 1 can be any). Rows [d_q_starts[b],
@@ -537,7 +612,18 @@ tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t
                              int causal, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
                              tq_stream_t stream);
 
-/* tq_cross_attention: the same over an encoder's states, of another length than the queries, every state visible.
+/* tq_paged_attention8: the same over a pool of 8 bits (kv of type TQ_E4M3, with the scales that tq_paged_extend keeps) for queries
+ * and outputs of type q_dtype, TQ_BF16 or TQ_F16. Numbers of e4m3 are exact in f16, in which the products run: queries in bf16 are
+ * taken there by a power of two for each row and head. The scales of K multiply scores, those of V the weights' exponents and
+ * the statistics, in fp32; weights are rounded to f16 after that, relative to the row's largest. Scales outside
+ * [2^-60, 2^60] count as the nearest of the two, NaN as 2^-60. Base and strides of the pool: multiples of 16 bytes.
+ * Workspace: tq_attention_workspace_bytes(q, kv). */
+tq_status tq_paged_attention8(const tq_queries* q, tq_dtype q_dtype, const tq_kv* kv, const tq_scales* scales,
+                              const int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride,
+                              const int32_t* d_seq_ids, const int32_t* d_kv_lens, int causal, void* d_workspace,
+                              size_t workspace_bytes, uint32_t* d_status, tq_stream_t stream);
+
+/* tq_cross_attention: attention as tq_paged_attention's over an encoder's states, of another length than the queries, every state visible.
  * Packed (kv->outer = 1, d_kv_starts[batch + 1] given): request b has rows [kv_starts[b], kv_starts[b + 1]).
  * Padded (d_kv_starts NULL, kv->outer = batch, d_kv_lens[batch] given): request b has its first kv_lens[b] rows.
  * No state gives zeros. States past a request's own may hold anything. */

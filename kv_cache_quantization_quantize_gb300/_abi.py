@@ -8,7 +8,7 @@ LIB_PATH = os.path.join(_PKG, "libtq.so")
 HEADER = os.path.join(os.path.dirname(_PKG), "include", "tq.h")
 
 TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CAPACITY, TQ_ERR_CUDA, TQ_ERR_DEVICE = range(6)
-TQ_BF16, TQ_F32, TQ_F16 = 0, 1, 2
+TQ_BF16, TQ_F32, TQ_F16, TQ_E4M3 = 0, 1, 2, 3
 TQ_CODEC_FP16, TQ_CODEC_KIVI2, TQ_CODEC_BONSAI1, TQ_CODEC_TQ_K3V2, TQ_CODEC_TQ_K3V4 = range(5)
 TQ_DEV_ERR_CAPACITY, TQ_DEV_ERR_SEQ_ID, TQ_DEV_ERR_SPLITS, TQ_DEV_ERR_TIMEOUT, TQ_DEV_ERR_BLOCK = 0x1, 0x2, 0x4, 0x8, 0x10
 TQ_DEV_ERR_POOL, TQ_DEV_ERR_LENGTH = 0x20, 0x40
@@ -74,9 +74,13 @@ _SIGS = {
     "tq_blocks_map": (c_int, [c_void_p, c_int, c_int, ctypes.c_int64, c_void_p, c_int] + [c_void_p] * 4 + [c_int] + [c_void_p] * 3
                       + [c_int, c_void_p, c_void_p]),
     "tq_paged_append": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p]),
+    "tq_rotate": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p]),
+    "tq_paged_extend": (c_int, [c_void_p] * 5 + [c_int, c_int, ctypes.c_int64] + [c_void_p] * 3 + [c_int, c_void_p, c_void_p]),
     "tq_attention_workspace_bytes": (c_size_t, [c_void_p, c_void_p]),
     "tq_paged_attention": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, ctypes.c_int64, c_void_p, c_void_p, c_int, c_void_p,
                                    c_size_t, c_void_p, c_void_p]),
+    "tq_paged_attention8": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, ctypes.c_int64, c_void_p, c_void_p, c_int,
+                                    c_void_p, c_size_t, c_void_p, c_void_p]),
     "tq_cross_attention": (c_int, [c_void_p] * 5 + [c_size_t, c_void_p, c_void_p]),
     "tq_codec_kv_bytes": (c_size_t, [c_int, c_int, c_int, c_int, ctypes.c_int64]),
 }

@@ -44,6 +44,8 @@ struct AttnArgs {
   int slope, shift;          // cost that each tile of a causal request has over the one before, and the scale of costs
                              // (tq_attention_line.cuh)
   int mode, causal;
+  const float *k_scale, *v_scale;  // a cache of 8 bits: entry (block, KV head) at block * ks_block + head
+  int64_t ks_block, vs_block;
   int max_rows;              // rows (query, head of the group) of a request and KV head at most
 };
 
@@ -107,6 +109,47 @@ __device__ __forceinline__ int tile_kv(const AttnArgs& a, const Request& r, int 
   return last < 0 ? 0 : seen(a, r, a.div_g(last));
 }
 
+// The scales of a unit of tokens in a cache of 8 bits: of its keys; of its values their logarithm and inverse.
+struct UnitScale {
+  float k, log_v, inv_v;
+};
+__device__ __forceinline__ float clamp_scale(float s) {
+  constexpr float kLo = 8.67361737988403547205962240695953369140625e-19f;  // 2^-60
+  return fminf(fmaxf(s, kLo), 1.f / kLo);  // NaN: kLo
+}
+__device__ __forceinline__ UnitScale unit_scale(const AttnArgs& a, int block, int head) {
+  UnitScale r = {1.f, 0.f, 1.f};
+  if (block < a.outer) {
+    r.k = clamp_scale(a.k_scale[block * a.ks_block + head]);
+    const float v = clamp_scale(a.v_scale[block * a.vs_block + head]);
+    const uint32_t u = __float_as_uint(v);
+    r.log_v = u & 0x7fffffu ? log2f(v) : (float)((int)(u >> 23) - 127);
+    r.inv_v = 1.f / v;
+  }
+  return r;
+}
+// Two e4m3 numbers, which f16 holds exactly: the low half's and the high half's of a word.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t x) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(x));
+  return r;
+}
+// The power of two that takes a bf16 row to f16 with its largest value in [2^7, 2^8), by the bits of that value (sign
+// off): bf16 numbers stay exact down to 2^-25 of it. And its inverse.
+__device__ __forceinline__ float to_f16_by(uint32_t top) { return __uint_as_float((261u - max(top >> 7, 8u)) << 23); }
+__device__ __forceinline__ float to_f16_back(uint32_t top) { return __uint_as_float((max(top >> 7, 8u) - 7u) << 23); }
+// Two bf16 values times `by`, in f16.
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t x, float by) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(__uint_as_float(x & 0xffff0000u) * by), "f"(__uint_as_float(x << 16) * by));
+  return r;
+}
+
 // 2^x as the special function unit gives it (relative error about 2^-22, 0 for -inf).
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -151,6 +194,9 @@ struct AttnMaps {
 // Tensor map of K or V for boxes of 64 channels x box_tokens tokens of one head, 128-byte swizzle: dimensions
 // {head_dim, tokens, heads, outer}.
 cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtensorMap* m);
+// Of a pool of 8 bits, for boxes of `channels` bytes x box_tokens tokens of one head: 128-byte swizzle (64-byte at head_dim
+// 64) or none.
+cudaError_t attn_tensor_map8(const tq_kv& kv, bool values, int channels, int box_tokens, bool swizzle, CUtensorMap* m);
 // Tensor map of the queries for boxes of 64 channels x the G heads of a group x 128 / G queries: 128 rows of a tile.
 cudaError_t query_tensor_map(const tq_queries& q, int head_dim, int dtype, int G, CUtensorMap* m);
 // A kernel's tiles and launch: rows (query, head of the group) of a tile, tokens of a unit, CTAs at most, bytes of
@@ -167,7 +213,10 @@ struct AttnPlan : AttnShape {
 };
 AttnShape attn_rows_shape(int d, int64_t rows, int sms);
 AttnShape attn_tc_shape(int d, int sms);
+AttnShape attn8_rows_shape(int d, int64_t rows, int sms);
 cudaError_t launch_attn_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
+// Over a pool of 8 bits; dtype: of the queries.
+cudaError_t launch_attn8_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 
 }  // namespace tq

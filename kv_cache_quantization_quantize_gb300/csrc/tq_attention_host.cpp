@@ -50,6 +50,21 @@ cudaError_t attn_tensor_map(const tq_kv& kv, bool values, int box_tokens, CUtens
   return encode_map(m, kv.dtype, 4, base, dims, strides, box);
 }
 
+cudaError_t attn_tensor_map8(const tq_kv& kv, bool values, int channels, int box_tokens, bool swizzle, CUtensorMap* m) {
+  const auto encode = encoder();
+  if (!encode) return cudaErrorNotSupported;
+  const int64_t* st = values ? kv.v_strides : kv.k_strides;
+  const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, (cuuint64_t)kv.tokens, (cuuint64_t)kv.n_kv_heads, (cuuint64_t)kv.outer};
+  auto bytes = [&](cuuint64_t n, int64_t stride) { return n > 1 ? (cuuint64_t)stride : dims[0]; };  // a stride that is never taken: any
+  const cuuint64_t strides[3] = {bytes(dims[1], st[1]), bytes(dims[2], st[2]), bytes(dims[3], st[0])};
+  const cuuint32_t box[4] = {(cuuint32_t)channels, (cuuint32_t)box_tokens, 1, 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, values ? kv.v : kv.k, dims, strides, box, estr,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : channels == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t query_tensor_map(const tq_queries& q, int head_dim, int dtype, int G, CUtensorMap* m) {
   const cuuint64_t d = (cuuint64_t)head_dim;
   const cuuint64_t dims[3] = {d, (cuuint64_t)q.n_q_heads, (cuuint64_t)q.n_rows};
@@ -103,11 +118,13 @@ tq_status check_map(const int32_t* table, int max_seqs, int max_pages, int64_t s
   return TQ_OK;
 }
 
-tq_status check_kv(const tq_kv* kv, bool map) {
+// `scaled`: a pool of 8 bits.
+tq_status check_kv(const tq_kv* kv, bool map, bool scaled = false) {
   if (!kv) return fail(TQ_ERR_INVALID_ARG, "kv is NULL");
   if (kv->head_dim != 64 && kv->head_dim != 128 && kv->head_dim != 256)
     return fail(TQ_ERR_UNSUPPORTED, "head_dim %d: supported 64, 128, 256", kv->head_dim);
-  if (kv->dtype != TQ_BF16 && kv->dtype != TQ_F16) return fail(TQ_ERR_UNSUPPORTED, "cache type %d: bf16 or f16", kv->dtype);
+  if (scaled && kv->dtype != TQ_E4M3) return fail(TQ_ERR_UNSUPPORTED, "cache type %d: with scales, e4m3", kv->dtype);
+  if (!scaled && kv->dtype != TQ_BF16 && kv->dtype != TQ_F16) return fail(TQ_ERR_UNSUPPORTED, "cache type %d: bf16 or f16", kv->dtype);
   if (kv->n_kv_heads < 1 || kv->n_kv_heads > 65535 || kv->outer < 0 || kv->tokens < 0)
     return fail(TQ_ERR_INVALID_ARG, "n_kv_heads %d, outer %d, tokens %d", kv->n_kv_heads, kv->outer, kv->tokens);
   if (!kv->outer || !kv->tokens) return TQ_OK;  // no element
@@ -117,10 +134,50 @@ tq_status check_kv(const tq_kv* kv, bool map) {
   const int size[3] = {kv->outer, kv->tokens, kv->n_kv_heads};
   for (int i = 0; i < 3; ++i)
     for (const int64_t st : {kv->k_strides[i], kv->v_strides[i]})
-      if (size[i] > 1 && (st < 1 || st % 8 || st >= (int64_t)1 << 38))
-        return fail(TQ_ERR_INVALID_ARG, "stride %lld of k or v: a positive multiple of 8 elements", (long long)st);
+      if (size[i] > 1 && (st < 1 || st % (scaled ? 16 : 8) || st >= (int64_t)1 << 38))
+        return fail(TQ_ERR_INVALID_ARG, "stride %lld of k or v: a positive multiple of %d elements", (long long)st, scaled ? 16 : 8);
   return TQ_OK;
 }
+
+tq_status check_scales(const tq_scales* s, const tq_kv* kv) {
+  if (!s || !s->k || !s->v || !aligned(s->k, 4) || !aligned(s->v, 4))
+    return fail(TQ_ERR_INVALID_ARG, "scales of k and v: two arrays of floats");
+  if (kv->outer > 1 && (s->k_block < kv->n_kv_heads || s->v_block < kv->n_kv_heads))
+    return fail(TQ_ERR_INVALID_ARG, "scales: %lld and %lld entries from block to block for %d heads", (long long)s->k_block,
+                (long long)s->v_block, kv->n_kv_heads);
+  return TQ_OK;
+}
+
+tq_status check_pool(const tq_kv* kv) {
+  if (kv->tokens != tq::kPage || kv->outer < 1 || kv->outer > (1 << 24) - 1)
+    return fail(TQ_ERR_INVALID_ARG, "a pool has 1 to 2^24 - 1 blocks of 128 tokens (got %d of %d)", kv->outer, kv->tokens);
+  return TQ_OK;
+}
+
+tq_status check_table(int max_seqs, int max_pages, int64_t stride) {
+  if (max_seqs < 1 || max_pages < 1 || max_pages > (1 << 20) || stride < max_pages)
+    return fail(TQ_ERR_INVALID_ARG, "max_seqs %d, max_pages %d (at most 2^20), table_stride %lld", max_seqs, max_pages,
+                (long long)stride);
+  return TQ_OK;
+}
+
+// rot as the kernels take it (NULL: none), for heads of head_dim channels.
+tq_status check_rotary(const tq_rotary* rot, int head_dim, tq::Rotation* r) {
+  *r = {};
+  if (!rot) return TQ_OK;
+  if (rot->rotary_dim < 8 || rot->rotary_dim % 8 || rot->rotary_dim > head_dim)
+    return fail(TQ_ERR_UNSUPPORTED, "rotary_dim %d: a multiple of 8, at most head_dim %d", rot->rotary_dim, head_dim);
+  if (rot->interleaved != 0 && rot->interleaved != 1) return fail(TQ_ERR_INVALID_ARG, "interleaved %d: 0 or 1", rot->interleaved);
+  if (!std::isfinite(rot->factor)) return fail(TQ_ERR_INVALID_ARG, "factor is not finite");
+  if (!rot->d_turns || !aligned(rot->d_turns, 8)) return fail(TQ_ERR_INVALID_ARG, "d_turns: 8-byte aligned device memory");
+  r->turns = rot->d_turns;
+  r->pairs = rot->rotary_dim / 2;
+  r->interleaved = rot->interleaved;
+  r->factor = rot->factor;
+  return TQ_OK;
+}
+
+bool known_type(int dt) { return dt == TQ_BF16 || dt == TQ_F16 || dt == TQ_F32; }
 
 tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
   if (!q) return fail(TQ_ERR_INVALID_ARG, "queries are NULL");
@@ -153,8 +210,10 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
 tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   tq::AttnPlan p;
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * (q.n_q_heads / kv.n_kv_heads);
-  const bool tc = rows > 32;
-  static_cast<tq::AttnShape&>(p) = tc ? tq::attn_tc_shape(kv.head_dim, sms) : tq::attn_rows_shape(kv.head_dim, rows, sms);
+  const bool tc = rows > 32 && kv.dtype != TQ_E4M3;
+  static_cast<tq::AttnShape&>(p) = tc                      ? tq::attn_tc_shape(kv.head_dim, sms)
+                                   : kv.dtype == TQ_E4M3 ? tq::attn8_rows_shape(kv.head_dim, rows, sms)
+                                                         : tq::attn_rows_shape(kv.head_dim, rows, sms);
   p.tc = tc;
   p.max_rows = rows;
   p.ctas = std::min(p.ctas, tq::kMaxAttnCtas);
@@ -167,7 +226,8 @@ tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   return p;
 }
 
-tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void* ws, size_t ws_bytes,
+// q_dtype: of queries and outputs; the cache's own, unless that has 8 bits.
+tq_status attend(const tq_queries* q, int q_dtype, const tq_kv* kv_in, tq::AttnArgs& a, void* ws, size_t ws_bytes,
                  uint32_t* status, tq_stream_t stream) {
   if (!q->batch || !q->n_rows) return tq::set_error(TQ_OK, "");
   int sms = 0;
@@ -214,6 +274,13 @@ tq_status attend(const tq_queries* q, const tq_kv* kv_in, tq::AttnArgs& a, void*
     return fail(TQ_ERR_UNSUPPORTED, "batch x heads x rows: too many tiles for one launch");
   a.slope = (int)slope >> a.shift;
   tq::AttnMaps m = {};
+  if (kv.dtype == TQ_E4M3) {
+    const int channels = std::min(kv.head_dim, 128);
+    e = tq::attn_tensor_map8(kv, false, channels, p.unit, true, &m.k);
+    if (e == cudaSuccess) e = tq::attn_tensor_map8(kv, true, channels, p.unit, true, &m.v);
+    if (e == cudaSuccess) e = tq::launch_attn8_rows(a, m, p, kv.head_dim, q_dtype, (cudaStream_t)stream);
+    return done(e, "attention launch");
+  }
   e = tq::attn_tensor_map(kv, false, p.unit, &m.k);
   if (e == cudaSuccess) e = tq::attn_tensor_map(kv, true, p.unit, &m.v);
   // Queries by TMA: a tile's 128 rows are whole queries where the group's size divides 128, with strides that TMA takes.
@@ -292,9 +359,8 @@ tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dt
   const tq::NvtxRange nvtx_range("tq_paged_append");
   const tq_status st = check_kv(pool, false);
   if (st != TQ_OK) return st;
-  if (pool->tokens != tq::kPage || pool->outer < 1 || pool->outer > (1 << 24) - 1)
-    return fail(TQ_ERR_INVALID_ARG, "a pool has 1 to 2^24 - 1 blocks of 128 tokens (got %d of %d)", pool->outer, pool->tokens);
-  if (dt != TQ_BF16 && dt != TQ_F16 && dt != TQ_F32) return fail(TQ_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (check_pool(pool) != TQ_OK) return TQ_ERR_INVALID_ARG;
+  if (!known_type(dt)) return fail(TQ_ERR_INVALID_ARG, "dtype %d", (int)dt);
   if (n_tokens < 0) return fail(TQ_ERR_INVALID_ARG, "n_tokens %d < 0", n_tokens);
   if (!n_tokens) return tq::set_error(TQ_OK, "");
   if (!k || !v || !k_strides || !v_strides || !d_slots) return fail(TQ_ERR_INVALID_ARG, "NULL array");
@@ -309,27 +375,84 @@ tq_status tq_paged_append(const tq_kv* pool, const void* k, const void* v, tq_dt
               "tq_paged_append");
 }
 
+tq_status tq_rotate(const tq_rotary* rot, const void* x, void* out, tq_dtype dt, const int64_t* x_strides,
+                    const int64_t* out_strides, const int32_t* d_positions, int n_tokens, int n_heads, int head_dim,
+                    int inverse, tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_rotate");
+  if (!rot) return fail(TQ_ERR_INVALID_ARG, "rot is NULL");
+  if (head_dim < 8 || head_dim % 8 || head_dim > 1024)
+    return fail(TQ_ERR_UNSUPPORTED, "head_dim %d: a multiple of 8, at most 1024", head_dim);
+  tq::Rotation r;
+  const tq_status st = check_rotary(rot, head_dim, &r);
+  if (st != TQ_OK) return st;
+  if (!known_type(dt)) return fail(TQ_ERR_INVALID_ARG, "dtype %d", (int)dt);
+  if (inverse != 0 && inverse != 1) return fail(TQ_ERR_INVALID_ARG, "inverse %d: 0 or 1", inverse);
+  if (n_tokens < 0 || n_heads < 0) return fail(TQ_ERR_INVALID_ARG, "n_tokens %d, n_heads %d: none below 0", n_tokens, n_heads);
+  if (!n_tokens || !n_heads) return tq::set_error(TQ_OK, "");
+  if (!x || !out || !x_strides || !out_strides || !d_positions) return fail(TQ_ERR_INVALID_ARG, "NULL array");
+  const size_t esz = dt == TQ_F32 ? 4 : 2;
+  if (!aligned(x, esz) || !aligned(out, esz)) return fail(TQ_ERR_INVALID_ARG, "an address is not a multiple of its element's size");
+  r.inverse = inverse;
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return done(e, "device");
+  return done(tq::launch_rotate(r, x, out, (int)dt, x_strides, out_strides, d_positions, n_tokens, n_heads, head_dim, sms,
+                                (cudaStream_t)stream),
+              "tq_rotate");
+}
+
+tq_status tq_paged_extend(const tq_kv* pool, const tq_scales* scales, const tq_new_rows* rows, const tq_rotary* rot,
+                          const int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride,
+                          const int32_t* d_seq_ids, const int32_t* d_starts, const int32_t* d_totals, int batch,
+                          uint32_t* d_status, tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_paged_extend");
+  tq_status st = check_kv(pool, scales != nullptr, scales != nullptr);
+  if (st == TQ_OK) st = check_pool(pool);
+  if (st == TQ_OK && scales) st = check_scales(scales, pool);
+  tq::Rotation r;
+  if (st == TQ_OK) st = check_rotary(rot, pool->head_dim, &r);
+  if (st == TQ_OK) st = check_table(max_seqs, max_pages, table_stride);
+  if (st != TQ_OK) return st;
+  if (!rows) return fail(TQ_ERR_INVALID_ARG, "rows are NULL");
+  if (!known_type(rows->dtype)) return fail(TQ_ERR_INVALID_ARG, "dtype %d", rows->dtype);
+  if (rows->n_rows < 0 || batch < 0 || rows->n_q_heads < 0 || rows->n_q_heads > 65535)
+    return fail(TQ_ERR_INVALID_ARG, "n_rows %d, batch %d, n_q_heads %d (at most 65535): none below 0", rows->n_rows, batch, rows->n_q_heads);
+  if (batch > 65535) return fail(TQ_ERR_UNSUPPORTED, "batch %d: at most 65535", batch);
+  if (rows->q && !rot) return fail(TQ_ERR_INVALID_ARG, "q without rot: nothing to do");
+  if (!batch || !rows->n_rows) return tq::set_error(TQ_OK, "");
+  const bool queries = rows->q && rows->n_q_heads;
+  if (!rows->k || !rows->v || (queries && !rows->q_out) || !d_table || !d_starts || !d_totals)
+    return fail(TQ_ERR_INVALID_ARG, "NULL array");
+  if (!d_seq_ids && batch > max_seqs) return fail(TQ_ERR_INVALID_ARG, "batch %d above max_seqs %d", batch, max_seqs);
+  const size_t esz = rows->dtype == TQ_F32 ? 4 : 2;
+  if (!aligned(rows->k, esz) || !aligned(rows->v, esz) || (queries && (!aligned(rows->q, esz) || !aligned(rows->q_out, esz))) ||
+      !aligned(pool->k, 2) || !aligned(pool->v, 2))
+    return fail(TQ_ERR_INVALID_ARG, "an address is not a multiple of its element's size");
+  tq::StepMap m = {d_table, table_stride, d_seq_ids, d_starts, d_totals, max_seqs, max_pages, batch, rows->n_rows};
+  tq_new_rows n = *rows;
+  if (!queries) n.q = nullptr;
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return done(e, "device");
+  return done(tq::launch_paged_extend(*pool, scales, n, r, m, d_status, sms, (cudaStream_t)stream), "tq_paged_extend");
+}
+
 size_t tq_attention_workspace_bytes(const tq_queries* q, const tq_kv* kv) {
   int sms = 0;
-  if (check_kv(kv, false) != TQ_OK || !q || q->batch < 1 || q->n_rows < 1 || q->max_q < 0 || q->n_q_heads < 1 ||
+  if (!kv || check_kv(kv, false, kv->dtype == TQ_E4M3) != TQ_OK || !q || q->batch < 1 || q->n_rows < 1 || q->max_q < 0 || q->n_q_heads < 1 ||
       q->n_q_heads % kv->n_kv_heads || sm_count(&sms) != cudaSuccess)
     return 0;
   return plan_of(*q, *kv, sms).bytes;
 }
 
-tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_table, int max_seqs,
-                             int max_pages, int64_t table_stride, const int32_t* d_seq_ids, const int32_t* d_kv_lens,
-                             int causal, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
-                             tq_stream_t stream) {
-  const tq::NvtxRange nvtx_range("tq_paged_attention");
-  tq_status st = check_kv(kv, true);
-  if (st == TQ_OK) st = check_queries(q, kv);
+// tq_paged_attention, and with scales tq_paged_attention8
+static tq_status paged_attention(const tq_queries* q, int q_dtype, const tq_kv* kv, const tq_scales* scales, const int32_t* d_table,
+                                 int max_seqs, int max_pages, int64_t table_stride, const int32_t* d_seq_ids,
+                                 const int32_t* d_kv_lens, int causal, void* d_workspace, size_t workspace_bytes,
+                                 uint32_t* d_status, tq_stream_t stream) {
+  tq_status st = check_queries(q, kv);
   if (st != TQ_OK) return st;
-  if (kv->tokens != tq::kPage || kv->outer < 1 || kv->outer > (1 << 24) - 1)
-    return fail(TQ_ERR_INVALID_ARG, "a pool has 1 to 2^24 - 1 blocks of 128 tokens (got %d of %d)", kv->outer, kv->tokens);
-  if (max_seqs < 1 || max_pages < 1 || max_pages > (1 << 20) || table_stride < max_pages)
-    return fail(TQ_ERR_INVALID_ARG, "max_seqs %d, max_pages %d (at most 2^20), table_stride %lld", max_seqs, max_pages,
-                (long long)table_stride);
+  if (check_pool(kv) != TQ_OK || check_table(max_seqs, max_pages, table_stride) != TQ_OK) return TQ_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return fail(TQ_ERR_INVALID_ARG, "causal %d: 0 or 1", causal);
   if (q->batch && q->n_rows && (!d_table || !d_kv_lens)) return fail(TQ_ERR_INVALID_ARG, "d_table or d_kv_lens is NULL");
   if (!d_seq_ids && q->batch > max_seqs) return fail(TQ_ERR_INVALID_ARG, "batch %d above max_seqs %d", q->batch, max_seqs);
@@ -342,7 +465,37 @@ tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t
   a.table_stride = table_stride;
   a.max_seqs = max_seqs;
   a.most_kv = max_pages * tq::kPage;
-  return attend(q, kv, a, d_workspace, workspace_bytes, d_status, stream);
+  if (scales) {
+    a.k_scale = scales->k;
+    a.v_scale = scales->v;
+    a.ks_block = scales->k_block;
+    a.vs_block = scales->v_block;
+  }
+  return attend(q, q_dtype, kv, a, d_workspace, workspace_bytes, d_status, stream);
+}
+
+tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_table, int max_seqs,
+                             int max_pages, int64_t table_stride, const int32_t* d_seq_ids, const int32_t* d_kv_lens,
+                             int causal, void* d_workspace, size_t workspace_bytes, uint32_t* d_status,
+                             tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_paged_attention");
+  const tq_status st = check_kv(kv, true);
+  if (st != TQ_OK) return st;
+  return paged_attention(q, kv->dtype, kv, nullptr, d_table, max_seqs, max_pages, table_stride, d_seq_ids, d_kv_lens, causal,
+                         d_workspace, workspace_bytes, d_status, stream);
+}
+
+tq_status tq_paged_attention8(const tq_queries* q, tq_dtype q_dtype, const tq_kv* kv, const tq_scales* scales,
+                              const int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride,
+                              const int32_t* d_seq_ids, const int32_t* d_kv_lens, int causal, void* d_workspace,
+                              size_t workspace_bytes, uint32_t* d_status, tq_stream_t stream) {
+  const tq::NvtxRange nvtx_range("tq_paged_attention8");
+  tq_status st = check_kv(kv, true, true);
+  if (st == TQ_OK) st = check_scales(scales, kv);
+  if (st != TQ_OK) return st;
+  if (q_dtype != TQ_BF16 && q_dtype != TQ_F16) return fail(TQ_ERR_UNSUPPORTED, "queries of type %d: bf16 or f16", (int)q_dtype);
+  return paged_attention(q, q_dtype, kv, scales, d_table, max_seqs, max_pages, table_stride, d_seq_ids, d_kv_lens, causal,
+                         d_workspace, workspace_bytes, d_status, stream);
 }
 
 tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t* d_kv_starts,
@@ -362,7 +515,7 @@ tq_status tq_cross_attention(const tq_queries* q, const tq_kv* kv, const int32_t
   a.kv_starts = d_kv_starts;
   a.max_seqs = kv->outer;
   a.most_kv = kv->tokens;  // packed: the most that one request can have
-  return attend(q, kv, a, d_workspace, workspace_bytes, d_status, stream);
+  return attend(q, kv->dtype, kv, a, d_workspace, workspace_bytes, d_status, stream);
 }
 
 }  // extern "C"

@@ -285,4 +285,22 @@ cudaError_t launch_paged_append(const tq_kv& pool, const void* k, const void* v,
                                 const int64_t* v_strides, const int32_t* slots, int n_tokens, uint32_t* status,
                                 int sms, cudaStream_t s);
 
+// Rotary positions and rotated appends (tq_extend.cu). What a tq_rotary is to the kernels; pairs 0: no rotation.
+struct Rotation {
+  const uint64_t* turns;
+  int pairs, interleaved, inverse;
+  float factor;
+};
+// Where a step's rows go.
+struct StepMap {
+  const int32_t* table;
+  int64_t stride;
+  const int32_t *ids, *starts, *totals;
+  int max_seqs, max_pages, batch, n_rows;
+};
+cudaError_t launch_rotate(const Rotation& r, const void* x, void* out, int dt, const int64_t* xs, const int64_t* os,
+                          const int32_t* positions, int n_tokens, int heads, int d, int sms, cudaStream_t s);
+cudaError_t launch_paged_extend(const tq_kv& pool, const tq_scales* scales, const tq_new_rows& rows, const Rotation& r,
+                                const StepMap& m, uint32_t* status, int sms, cudaStream_t s);
+
 }  // namespace tq

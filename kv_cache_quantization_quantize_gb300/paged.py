@@ -1,7 +1,8 @@
-"""Exact paged cache: block maps, appends and attention of new tokens, and cross attention to an encoder's states.
+"""Paged caches of 16 and 8 bits: block maps, appends, rotary positions and attention of new tokens, and cross attention to an
+encoder's states.
 
-Python binding of tq_blocks_map, tq_blocks_release, tq_paged_append, tq_paged_attention and tq_cross_attention
-(include/tq.h has the operations). Argument checks and marshalling only: the work runs in libtq's kernels; there is
+Python binding of tq_blocks_map, tq_blocks_release, tq_paged_append, tq_rotate, tq_paged_extend, tq_paged_attention,
+tq_paged_attention8 and tq_cross_attention (include/tq.h has the operations). Argument checks and marshalling only: the work runs in libtq's kernels; there is
 no fallback. No call reads a length, id or start on the host, so every one of them can be captured into a graph.
 
 A page is 128 tokens, the packed cache's page: one block table serves a paged TurboQuantCache (its `block_pool`) and
@@ -16,17 +17,24 @@ One serving step:
     out = cache.attention(layer, q, seq_ids, starts, totals, max_q=..., max_kv=...)
     ...
     pool.release(seq_ids_of_finished_requests)               # keep=lengths: back to these, without packed layers
+
+With rotary positions, and in a cache of 8 bits (dtype=torch.float8_e4m3fn) in any case, extend takes append's place:
+
+    rotary = Rotary(head_dim, base=500000.0)
+    q = cache.extend(layer, k, v, seq_ids, starts, totals, rotary=rotary, q=q)   # K rotated on the way, q in the same launch
 """
 import ctypes
+import math
 import struct
+from fractions import Fraction
 
 import torch
 
-from ._abi import (TQ_BF16, TQ_DEV_ERR_BLOCK, TQ_DEV_ERR_LENGTH, TQ_DEV_ERR_POOL, TQ_DEV_ERR_SEQ_ID,
+from ._abi import (TQ_BF16, TQ_E4M3, TQ_DEV_ERR_BLOCK, TQ_DEV_ERR_LENGTH, TQ_DEV_ERR_POOL, TQ_DEV_ERR_SEQ_ID,
                    TQ_DEV_ERR_SPLITS, TQ_DEV_ERR_TIMEOUT, TQ_F16, TQ_F32, check, load)
 
-__all__ = ["PAGE", "BlockPool", "PagedCache", "map_blocks", "release_blocks", "append", "attention", "cross_attention",
-           "attention_workspace_bytes", "TQ_DEV_ERR_BLOCK", "TQ_DEV_ERR_LENGTH", "TQ_DEV_ERR_POOL", "TQ_DEV_ERR_SEQ_ID",
+__all__ = ["PAGE", "BlockPool", "PagedCache", "Rotary", "map_blocks", "release_blocks", "append", "rotate", "extend", "attention",
+           "cross_attention", "attention_workspace_bytes", "TQ_DEV_ERR_BLOCK", "TQ_DEV_ERR_LENGTH", "TQ_DEV_ERR_POOL", "TQ_DEV_ERR_SEQ_ID",
            "TQ_DEV_ERR_SPLITS", "TQ_DEV_ERR_TIMEOUT"]
 
 PAGE = 128
@@ -34,10 +42,14 @@ _DTYPES = {torch.bfloat16: TQ_BF16, torch.float16: TQ_F16, torch.float32: TQ_F32
 _KV = struct.Struct("@PP6q5i4x")     # tq_kv
 _QUERIES = struct.Struct("@PP4qP5if")  # tq_queries
 _STRIDES = struct.Struct("@2q")
+_ROTARY = struct.Struct("@P2if4x")     # tq_rotary
+_SCALES = struct.Struct("@PP2q")       # tq_scales
+_NEW_ROWS = struct.Struct("@4P8qP3i4x")  # tq_new_rows
 
 
 _I32 = torch.int32
 _HALVES = (torch.bfloat16, torch.float16)
+_E4M3 = torch.float8_e4m3fn
 _raw_memory = None  # see _raw_allocator
 
 
@@ -161,21 +173,188 @@ def release_blocks(table, free, n_free, seq_ids, keep=None, status=None, stream=
 
 
 def _kv(k, v, outer, tokens, heads, d, k_strides, v_strides):
-    return _KV.pack(k.data_ptr(), v.data_ptr(), *k_strides, *v_strides, outer, tokens, heads, d, _DTYPES[k.dtype])
+    return _KV.pack(k.data_ptr(), v.data_ptr(), *k_strides, *v_strides, outer, tokens, heads, d, TQ_E4M3 if k.dtype is _E4M3 else _DTYPES[k.dtype])
 
 
-def _pools(k_pool, v_pool):
-    """(device index, tq_kv, head_dim, heads, type) of a pool."""
+def _pools(k_pool, v_pool, scaled=False):
+    """(device index, tq_kv, head_dim, heads, type) of a pool, of one of e4m3 if `scaled`."""
     shape, dtype, index = k_pool.shape, k_pool.dtype, k_pool.get_device()
     if index < 0:
         raise ValueError("k_pool: expected a CUDA tensor")
-    if (len(shape) != 4 or shape[1] != PAGE or not shape[2] or shape != v_pool.shape or dtype is not v_pool.dtype or dtype not in _HALVES
-            or v_pool.get_device() != index):
-        raise ValueError("k_pool, v_pool: expected two bf16 or f16 tensors [n_blocks, 128, n_kv_heads, head_dim] on one device")
+    if (len(shape) != 4 or shape[1] != PAGE or not shape[2] or shape != v_pool.shape or dtype is not v_pool.dtype or v_pool.get_device() != index
+            or (dtype is not _E4M3 if scaled else dtype not in _HALVES)):
+        raise ValueError(f"k_pool, v_pool: expected two {'e4m3' if scaled else 'bf16 or f16'} tensors [n_blocks, 128, n_kv_heads, head_dim] on one "
+                         f"device (e4m3 ones go with k_scale and v_scale)")
     ks, vs = k_pool.stride(), v_pool.stride()
     if ks[3] != 1 or vs[3] != 1:
         raise ValueError("k_pool, v_pool: the channels of a head have to be contiguous")
     return index, _kv(k_pool, v_pool, shape[0], PAGE, shape[2], shape[3], ks[:3], vs[:3]), shape[3], shape[2], dtype
+
+
+def _scales(k_scale, v_scale, index, blocks, heads):
+    """tq_scales, or None where both are None."""
+    if k_scale is None and v_scale is None:
+        return None
+    for t in (k_scale, v_scale):
+        if (t is None or t.dtype is not torch.float32 or t.get_device() != index or t.shape != (blocks, heads) or (heads > 1 and t.stride(1) != 1)
+                or (blocks > 1 and t.stride(0) < heads)):
+            raise ValueError(f"k_scale, v_scale: expected two float32 tensors [{blocks}, {heads}] with contiguous rows on cuda:{index}")
+    return _SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr(), max(k_scale.stride(0), heads), max(v_scale.stride(0), heads))
+
+
+class Rotary:
+    """Angles of rotary positions: pair i of the first rotary_dim channels of a head turns by steps[i] radians per position.
+
+    The pairs are channels (i, i + rotary_dim / 2), or with `interleaved` (2 i, 2 i + 1). Without scaling, steps[i] =
+    base^(-2 i / rotary_dim). Scalings to contexts that are `factor` times longer than the `first` tokens of training:
+      "linear"  every step divided by factor
+      "base"    base * factor^(rotary_dim / (rotary_dim - 2)): the fastest pair stays, the slowest is divided by factor
+      "bands"   by how often a pair turns over `first` tokens: `high` times and more stays, `low` times and less is
+                divided by factor, between them in proportion
+      "ramp"    in proportion over the pairs between those that turn `fast` and `slow` times over `first` tokens; cosines and sines
+                are multiplied by `times`, by default 0.1 ln(factor) + 1
+    `times` multiplies cosines and sines with any scaling. Angles of other rules: Rotary.of(steps)."""
+
+    def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling=None, factor=1.0, first=0, low=1.0, high=4.0, fast=32.0, slow=1.0,
+                 times=None, device="cuda"):
+        if rotary_dim < 8 or rotary_dim % 8:
+            raise ValueError(f"rotary_dim {rotary_dim}: a multiple of 8")
+        if not base > 1 or not math.isfinite(base) or not factor > 0 or not math.isfinite(factor):
+            raise ValueError(f"base {base}, factor {factor}: a finite base above 1 and a finite factor above 0")
+        if scaling not in (None, "linear", "base", "bands", "ramp"):
+            raise ValueError(f"scaling {scaling!r}: None, 'linear', 'base', 'bands' or 'ramp'")
+        if scaling in ("bands", "ramp") and not first > 0:
+            raise ValueError(f"scaling {scaling!r} needs first, the tokens of the context that it starts from")
+        if scaling == "bands" and not high > low or scaling == "ramp" and not fast > slow > 0:
+            raise ValueError("high has to be above low, fast above slow and slow above 0")
+        if scaling == "base":
+            base *= factor ** (rotary_dim / (rotary_dim - 2))
+        steps = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+        if scaling == "linear":
+            steps = [t / factor for t in steps]
+        elif scaling == "bands":
+            keep = [min(1.0, max(0.0, (t * first / (2 * math.pi) - low) / (high - low))) for t in steps]
+            steps = [t * x + t / factor * (1.0 - x) for t, x in zip(steps, keep)]
+        elif scaling == "ramp":
+            lo, hi = (rotary_dim * math.log(first / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow))
+            lo, hi = max(math.floor(lo), 0), min(math.ceil(hi), rotary_dim - 1)
+            slowed = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(rotary_dim // 2)]
+            steps = [t / factor * x + t * (1.0 - x) for t, x in zip(steps, slowed)]
+            times = 0.1 * math.log(factor) + 1.0 if times is None else times
+        self._set(steps, interleaved, 1.0 if times is None else times, device)
+
+    @classmethod
+    def of(cls, steps, interleaved=False, times=1.0, device="cuda"):
+        """Angles of rotary_dim / 2 given steps, in radians per position."""
+        self = cls.__new__(cls)
+        self._set([float(t) for t in steps], interleaved, times, device)
+        return self
+
+    def _set(self, steps, interleaved, times, device):
+        if len(steps) < 4 or len(steps) % 4 or not all(map(math.isfinite, steps)) or not math.isfinite(times):
+            raise ValueError("steps: a multiple of 4 finite numbers, and a finite times")
+        self.rotary_dim, self.steps, self.interleaved, self.times = 2 * len(steps), tuple(steps), bool(interleaved), float(times)
+        # in 2^-64 of a whole turn, modulo 1
+        two_pi = 2 * Fraction(314159265358979323846264338327950288419716939937511, 10 ** 50)
+        turns = [round(Fraction(t) / two_pi * 2 ** 64) % 2 ** 64 for t in steps]
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        self._packed = None
+
+    def _pack(self, index):
+        if self._packed is None:
+            self._packed = (self.turns.get_device(), _ROTARY.pack(self.turns.data_ptr(), self.rotary_dim, self.interleaved, self.times))
+        if self._packed[0] != index:
+            raise ValueError(f"rotary: its angles are on {self.turns.device}, the others on cuda:{index}")
+        return self._packed[1]
+
+
+def rotate(x, positions, rotary, out=None, inverse=False, stream=None):
+    """x [tokens, heads, head_dim] (bf16, f16 or f32, any strides with contiguous channels) rotated to `positions` [tokens]
+    (int32) by a Rotary (tq_rotate). inverse: the transposed rotation, which takes a gradient of the result to that of x. out: the
+    tensor to write, which may be x. Returns out."""
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    if len(shape) != 3 or dtype not in _DTYPES or index < 0:
+        raise ValueError("x: expected a bf16, f16 or f32 CUDA tensor [tokens, heads, head_dim]")
+    place = _ints("positions", positions, index, shape[0])
+    rot = rotary._pack(index)
+    raw, on = _here(index, stream, (x, positions, rotary.turns, out))
+    if on is not None:
+        with on:
+            return _rotate(x, shape, dtype, index, place, rot, out, inverse, raw)
+    return _rotate(x, shape, dtype, index, place, rot, out, inverse, raw)
+
+
+def _rotate(x, shape, dtype, index, place, rot, out, inverse, raw):
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=x.device)
+    elif out.shape != shape or out.dtype is not dtype or out.get_device() != index:
+        raise ValueError("out: expected a tensor of x's shape, type and device")
+    xs, os = x.stride(), out.stride()
+    if xs[2] != 1 or os[2] != 1:
+        raise ValueError("x, out: the channels of a head have to be contiguous")
+    check(load().tq_rotate(rot, x.data_ptr(), out.data_ptr(), _DTYPES[dtype], _STRIDES.pack(xs[0], xs[1]), _STRIDES.pack(os[0], os[1]), place,
+                           shape[0], shape[1], shape[2], 1 if inverse else 0, raw))
+    return out
+
+
+def extend(k, v, k_pool, v_pool, table, seq_ids, starts, totals, rotary=None, positions=None, q=None, q_out=None, k_scale=None, v_scale=None,
+           status=None, stream=None):
+    """Writes a step's new tokens into the pools, K rotated on the way (tq_paged_extend).
+
+    k, v: [rows, n_kv_heads, head_dim] (bf16, f16 or f32, any strides with contiguous channels); request b's new rows are
+    [starts[b], starts[b + 1]), the last of its totals[b] tokens in the pages of table row seq_ids[b] (None: row b), as
+    map_blocks gives them. rotary: a Rotary (None: K is written as it is); positions: int32 [rows] to rotate by instead of
+    the tokens' places. q: [rows, n_q_heads, head_dim] of k's type, rotated into q_out (which may be q; None: a new
+    tensor, whose rows of no request are not written). k_scale, v_scale: float32 [n_blocks, n_kv_heads] of pools of
+    torch.float8_e4m3fn, which are kept up with the tokens. Returns q_out."""
+    scaled = k_scale is not None or v_scale is not None
+    index, pool, d, heads, _ = _pools(k_pool, v_pool, scaled)
+    scales = _scales(k_scale, v_scale, index, k_pool.shape[0], heads)
+    shape, dtype = k.shape, k.dtype
+    if (len(shape) != 3 or shape != v.shape or dtype is not v.dtype or dtype not in _DTYPES or k.get_device() != index
+            or v.get_device() != index or shape[1] != heads or shape[2] != d):
+        raise ValueError("k, v: expected two tensors [rows, n_kv_heads, head_dim] of one type that fit the pools")
+    ks, vs = k.stride(), v.stride()
+    if ks[2] != 1 or vs[2] != 1:
+        raise ValueError("k, v: the channels of a head have to be contiguous")
+    n, batch = shape[0], starts.shape[0] - 1
+    if batch < 0:
+        raise ValueError("starts: expected [batch + 1] entries")
+    args = (_table(table, index), None if seq_ids is None else _ints("seq_ids", seq_ids, index, batch), _ints("starts", starts, index),
+            _ints("totals", totals, index, batch), batch, None if status is None else _ints("status", status, index, 1))
+    places = 0 if positions is None else _ints("positions", positions, index, n)
+    if rotary is None and (q is not None or positions is not None):
+        raise ValueError("q and positions go with a rotary")
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
+    rot = None if rotary is None else rotary._pack(index)
+    if q is not None and (q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.dtype is not dtype or q.get_device() != index):
+        raise ValueError(f"q: expected a {dtype} tensor [{n}, n_q_heads, {d}] on cuda:{index}")
+    raw, on = _here(index, stream, (k, v, k_pool, v_pool, table, seq_ids, starts, totals, positions, q, q_out, k_scale, v_scale, status,
+                                    None if rotary is None else rotary.turns))
+    if on is not None:
+        with on:
+            return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, raw)
+    return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, raw)
+
+
+def _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, raw):
+    if q is None:
+        queries = (0, 0, 0, 0, 0, 0, 0)
+    else:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype is not dtype or q_out.device != q.device:
+            raise ValueError("q_out: expected a tensor of q's shape, type and device")
+        qs, os = q.stride(), q_out.stride()
+        if qs[2] != 1 or os[2] != 1:
+            raise ValueError("q, q_out: the channels of a head have to be contiguous")
+        queries = (q.data_ptr(), q_out.data_ptr(), qs[0], qs[1], os[0], os[1], q.shape[1])
+    rows = _NEW_ROWS.pack(k.data_ptr(), v.data_ptr(), queries[0], queries[1], ks[0], ks[1], vs[0], vs[1], *queries[2:6], places, n, queries[6],
+                          _DTYPES[dtype])
+    table, seq_ids, starts, totals, batch, word = args
+    check(load().tq_paged_extend(pool, scales, rows, rot, *table, seq_ids, starts, totals, batch, word, raw))
+    return q_out
 
 
 def append(k, v, k_pool, v_pool, slots, status=None, stream=None):
@@ -258,17 +437,31 @@ def attention_workspace_bytes(q, k, max_q=0, max_kv=0, batch=1):
 
 
 def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True, softmax_scale=0.0, max_q=0, max_kv=0, out=None,
-              workspace=None, status=None, stream=None):
-    """Attention of each request's new tokens over the paged cache that already holds them (tq_paged_attention).
+              workspace=None, status=None, stream=None, k_scale=None, v_scale=None):
+    """Attention of each request's new tokens over the paged cache that already holds them (tq_paged_attention; with k_scale and
+    v_scale, float32 [n_blocks, n_kv_heads], over pools of torch.float8_e4m3fn: tq_paged_attention8).
 
-    q: [rows, n_q_heads, head_dim] of the pools' type, request b's rows at [q_starts[b], q_starts[b + 1]); kv_lens[b]: its
+    q: [rows, n_q_heads, head_dim] of the pools' type (bf16 or f16 where they are e4m3), request b's rows at [q_starts[b], q_starts[b + 1]); kv_lens[b]: its
     tokens with the new ones, in the pages of table row seq_ids[b] (None: row b). max_q: no request has more rows (0:
     unknown; few rows take a kernel of their own); max_kv: no request has more tokens (0: unknown; short calls launch fewer
     CTAs). Returns out, of q's shape; rows of no request stay as they are. What the cache holds behind a request's
     tokens does not matter; a token that any of its queries sees has to be finite."""
-    index, kv, d, heads, dtype = _pools(k_pool, v_pool)
+    scaled = k_scale is not None or v_scale is not None
+    index, kv, d, heads, dtype = _pools(k_pool, v_pool, scaled)
     pages = _table(table, index)
     word = None if status is None else _ints("status", status, index, 1)
+    if scaled:
+        scales = _scales(k_scale, v_scale, index, k_pool.shape[0], heads)
+        dtype = q.dtype
+        if dtype not in _HALVES:
+            raise ValueError("q: expected a bf16 or f16 tensor")
+
+        def call8(queries, kv, batch, ws, size, raw):
+            return load().tq_paged_attention8(queries, _DTYPES[dtype], kv, scales, *pages, None if seq_ids is None else _ints("seq_ids", seq_ids, index, batch),
+                                              _ints("kv_lens", kv_lens, index, batch), 1 if causal else 0, ws, size, word, raw)
+
+        return _attend(q, dtype, heads, d, index, q_starts, max_q, max_kv, softmax_scale, out, workspace, kv, stream,
+                       (k_pool, v_pool, k_scale, v_scale, table, seq_ids, kv_lens, status), call8)
 
     def call(queries, kv, batch, ws, size, raw):
         return load().tq_paged_attention(queries, kv, *pages, None if seq_ids is None else _ints("seq_ids", seq_ids, index, batch),
@@ -343,21 +536,33 @@ class BlockPool:
 
 
 class PagedCache:
-    """Exact K and V of n_layers layers in 16 bits, in the blocks of a BlockPool (which other caches may share)."""
+    """K and V of n_layers layers in the blocks of a BlockPool (which other caches may share): exact in 16 bits, or in 8 bits
+    (torch.float8_e4m3fn) with a scale for each block and head, `scales` [n_layers, 2, n_blocks, n_kv_heads]."""
 
     def __init__(self, n_layers, pool, n_kv_heads, head_dim, dtype=torch.bfloat16):
-        if dtype not in (torch.bfloat16, torch.float16):
-            raise ValueError("dtype: bf16 or f16")
+        if dtype not in (torch.bfloat16, torch.float16, _E4M3):
+            raise ValueError("dtype: bf16, f16 or float8_e4m3fn")
         self.pool = pool
         self.kv = torch.empty((n_layers, 2, pool.n_blocks, PAGE, n_kv_heads, head_dim), dtype=dtype, device=pool.device)
+        self.scales = torch.ones((n_layers, 2, pool.n_blocks, n_kv_heads), device=pool.device) if dtype is _E4M3 else None
+
+    def _scales(self, layer):
+        return {} if self.scales is None else {"k_scale": self.scales[layer, 0], "v_scale": self.scales[layer, 1]}
 
     def append(self, layer, k, v, slots, stream=None):
-        """Writes the step's k, v [tokens, n_kv_heads, head_dim] of one layer at the slots of pool.map."""
+        """Writes the step's k, v [tokens, n_kv_heads, head_dim] of one layer at the slots of pool.map (16 bits: a cache of 8 bits
+        takes extend, whose scales need to know which tokens a block holds)."""
         append(k, v, self.kv[layer, 0], self.kv[layer, 1], slots, self.pool.status, stream)
+
+    def extend(self, layer, k, v, seq_ids, starts, totals, rotary=None, positions=None, q=None, q_out=None, stream=None):
+        """Writes the step's k, v [tokens, n_kv_heads, head_dim] of one layer, K rotated by a Rotary, and returns q [tokens,
+        n_q_heads, head_dim] rotated; starts and totals are those of pool.map. See extend()."""
+        return extend(k, v, self.kv[layer, 0], self.kv[layer, 1], self.pool.table, seq_ids, starts, totals, rotary, positions, q, q_out,
+                      status=self.pool.status, stream=stream, **self._scales(layer))
 
     def attention(self, layer, q, seq_ids, q_starts, kv_lens, causal=True, softmax_scale=0.0, max_q=0, max_kv=0, out=None,
                   workspace=None, stream=None):
         """Attention of the step's q [tokens, n_q_heads, head_dim] over one layer; q_starts and kv_lens are the starts and totals
         of pool.map. See attention()."""
         return attention(q, self.kv[layer, 0], self.kv[layer, 1], self.pool.table, seq_ids, q_starts, kv_lens, causal, softmax_scale, max_q,
-                         max_kv, out, workspace, self.pool.status, stream)
+                         max_kv, out, workspace, self.pool.status, stream, **self._scales(layer))
