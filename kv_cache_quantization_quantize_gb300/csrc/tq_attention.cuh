@@ -214,9 +214,11 @@ struct AttnPlan : AttnShape {
 AttnShape attn_rows_shape(int d, int64_t rows, int sms);
 AttnShape attn_tc_shape(int d, int sms);
 AttnShape attn8_rows_shape(int d, int64_t rows, int sms);
+AttnShape attn8_tc_shape(int d, int sms);
 cudaError_t launch_attn_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 cudaError_t launch_attn_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 // Over a pool of 8 bits; dtype: of the queries.
 cudaError_t launch_attn8_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
+cudaError_t launch_attn8_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s);
 
 }  // namespace tq

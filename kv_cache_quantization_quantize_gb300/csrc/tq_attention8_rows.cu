@@ -12,7 +12,7 @@ namespace {
 //     free, as long as the queries' fragments have the same.
 //   - V: ldmatrix moves pairs of neighbouring channels as one 16-bit element, transposed; a byte permutation then parts
 //     the even channels from the odd ones, which go to products of their own.
-// Scales: with p = 2^(s + log2 vs - m), where m is a maximum of s + log2 vs, the sums are of p times the number and the statistic
+// Scales: with p = 2^(s - m + log2 vs - m'), where m + m' is a maximum of s + log2 vs, the sums are of p times the number and the statistic
 // is of p / vs, so scales cost nothing per element but an addition, and weights are rounded to f16 relative to what they are
 // multiplied with, however far apart the scales of pages are.
 // =============================================================================================
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
         if (consumers_any(!ok)) break;
       }
     }
-    float o[MT][2 * NC][4], m[MT][2], l[MT][2], back[MT][2];
+    float o[MT][2 * NC][4], m[MT][2], mv[MT][2], l[MT][2], back[MT][2];  // m, mv: of scores, of values' scales
     int lim[MT][2];
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
       for (int i = 0; i < 2 * NC; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        l[t][x] = 0.f;
+        l[t][x] = mv[t][x] = 0.f;
         const int row = t * 16 + g8 + x * 8, f = g.f0 + row;
         lim[t][x] = f < g.rows ? seen(a, r, a.div_g(f)) : 0;
         m[t][x] = f < g.rows ? -INFINITY : INFINITY;  // a row past the last, of any scores, never outgrows its maximum
@@ -327,23 +327,22 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
             if (base + U > lim_all) x = t0 + n * 8 + (i & 1 ? tk1 : tk0) < lim[t][i >> 1] ? x : -INFINITY;
             top[t][i >> 1] = fmaxf(top[t][i >> 1], x);
           }
-        top[t][0] += us.log_v;
-        top[t][1] += us.log_v;
-        need |= top[t][0] > m[t][0] + kLazy || top[t][1] > m[t][1] + kLazy;
+        // (apart: far scores have no room for the logarithm)
+        need |= (top[t][0] - m[t][0]) + (us.log_v - mv[t][0]) > kLazy || (top[t][1] - m[t][1]) + (us.log_v - mv[t][1]) > kLazy;
       }
       float sum[MT][2];
       for (;;) {  // twice where a maximum outgrew its range: the code is not doubled, since a cold path costs its fetches
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
+          const float above[2] = {us.log_v - mv[t][0], us.log_v - mv[t][1]};
           sum[t][0] = sum[t][1] = 0.f;
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              // the difference first: far scores have no room for the logarithm
-              w[i] = exp2_fast((s[t][n][i] - mu[i >> 1]) + us.log_v);
+              w[i] = exp2_fast((s[t][n][i] - mu[i >> 1]) + above[i >> 1]);
               sum[t][i >> 1] += w[i];
             }
 #pragma unroll
@@ -375,10 +374,15 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = t * 16 + g8 + x * 8;
-            const float mn = fmaxf(m[t][x], fmaxf(fmaxf(sx[0][row], sx[1][row]), fmaxf(sx[2][row], sx[3][row])));
-            alpha[x] = mn == -INFINITY ? 1.f : exp2_fast(m[t][x] - mn);
-            m[t][x] = mn;
-            l[t][x] *= alpha[x];
+            const float mx = fmaxf(fmaxf(sx[0][row], sx[1][row]), fmaxf(sx[2][row], sx[3][row]));
+            alpha[x] = 1.f;
+            const float by = (m[t][x] - mx) + (mv[t][x] - us.log_v);
+            if (by < 0.f) {
+              alpha[x] = exp2_fast(by);
+              m[t][x] = mx;
+              mv[t][x] = us.log_v;
+              l[t][x] *= alpha[x];
+            }
           }
           if (k > 0) {
 #pragma unroll
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
         const int row = t * 16 + g8 + x * 8, f = g.f0 + row;
         if (f >= g.rows) continue;
         const float sum = sx[0][row] + sx[1][row] + sx[2][row] + sx[3][row];
+        const float part = exp2_fast(mv[t][x]);  // parts of a tile go to the join relative to m alone
         const int ch = warp * (D / 4) + j4 * 4;  // channels 4 j .. 4 j + 3 of each chunk: even, odd, even, odd
         if (g.direct) {
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -501,9 +506,9 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
 #pragma unroll
           for (int c = 0; c < NC; ++c)
             *reinterpret_cast<float4*>(po + c * 16) =
-                make_float4(o[t][2 * c][2 * x], o[t][2 * c + 1][2 * x], o[t][2 * c][2 * x + 1], o[t][2 * c + 1][2 * x + 1]);
+                make_float4(o[t][2 * c][2 * x] * part, o[t][2 * c + 1][2 * x] * part, o[t][2 * c][2 * x + 1] * part, o[t][2 * c + 1][2 * x + 1] * part);
           if (warp == 0 && (lane & 3) == 0)
-            cut_ml<R>(a, gridDim.x, blockIdx.x, g.slot)[row] = make_float2(m[t][x], sum);
+            cut_ml<R>(a, gridDim.x, blockIdx.x, g.slot)[row] = make_float2(m[t][x], sum * part);
         }
       }
   }

@@ -210,10 +210,9 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
 tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   tq::AttnPlan p;
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * (q.n_q_heads / kv.n_kv_heads);
-  const bool tc = rows > 32 && kv.dtype != TQ_E4M3;
-  static_cast<tq::AttnShape&>(p) = tc                      ? tq::attn_tc_shape(kv.head_dim, sms)
-                                   : kv.dtype == TQ_E4M3 ? tq::attn8_rows_shape(kv.head_dim, rows, sms)
-                                                         : tq::attn_rows_shape(kv.head_dim, rows, sms);
+  const bool tc = rows > 32, e4m3 = kv.dtype == TQ_E4M3;
+  static_cast<tq::AttnShape&>(p) = tc ? (e4m3 ? tq::attn8_tc_shape(kv.head_dim, sms) : tq::attn_tc_shape(kv.head_dim, sms))
+                                      : (e4m3 ? tq::attn8_rows_shape : tq::attn_rows_shape)(kv.head_dim, rows, sms);
   p.tc = tc;
   p.max_rows = rows;
   p.ctas = std::min(p.ctas, tq::kMaxAttnCtas);
@@ -275,10 +274,11 @@ tq_status attend(const tq_queries* q, int q_dtype, const tq_kv* kv_in, tq::AttnA
   a.slope = (int)slope >> a.shift;
   tq::AttnMaps m = {};
   if (kv.dtype == TQ_E4M3) {
-    const int channels = std::min(kv.head_dim, 128);
-    e = tq::attn_tensor_map8(kv, false, channels, p.unit, true, &m.k);
-    if (e == cudaSuccess) e = tq::attn_tensor_map8(kv, true, channels, p.unit, true, &m.v);
-    if (e == cudaSuccess) e = tq::launch_attn8_rows(a, m, p, kv.head_dim, q_dtype, (cudaStream_t)stream);
+    const int channels = p.tc ? kv.head_dim : std::min(kv.head_dim, 128);  // the rows kernel reads what TMA wrote, in the swizzle
+    e = tq::attn_tensor_map8(kv, false, channels, p.unit, !p.tc, &m.k);
+    if (e == cudaSuccess) e = tq::attn_tensor_map8(kv, true, channels, p.unit, !p.tc, &m.v);
+    if (e == cudaSuccess)
+      e = (p.tc ? tq::launch_attn8_tc : tq::launch_attn8_rows)(a, m, p, kv.head_dim, q_dtype, (cudaStream_t)stream);
     return done(e, "attention launch");
   }
   e = tq::attn_tensor_map(kv, false, p.unit, &m.k);

@@ -540,6 +540,32 @@ def test_queries_of_any_size(d, n):
                     check_attended(out[i:i + 1, h:h + 1], one, kk, ks[:, h // 2:h // 2 + 1], vv, vs[:, h // 2:h // 2 + 1], table, slot, [1], [300 - n + i + 1], scale=scale)
 
 
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("size,sign", [(2.0 ** 12, 1), (2.0 ** 12, -1), (2.0 ** 15, 1)])
+def test_scores_far_from_zero_pick_one_token(dtype, d, n, size, sign):
+    """Scores around 2^20 to 2^40, of which one is the largest by far, over pages whose values' scales are far apart: the result is that
+    token's values, exact but for the result's rounding."""
+    m, hkv = 700, 2
+    table, slot, blocks = place_requests([n], [m], 3)
+    gen = torch.Generator().manual_seed(d + n)
+    k = torch.full((blocks, 128, hkv, d), 256.0)
+    pick = 200
+    k[int(table[slot[0], pick // 128]), pick % 128] = 256.0 + 32.0 * sign  # the neighbouring number of e4m3
+    k = k.to(E4M3).to(DEV)
+    v = torch.randn((blocks, 128, hkv, d), generator=gen).to(E4M3).to(DEV)
+    ks = torch.full((blocks, hkv), 2.0 ** 4, device=DEV)
+    most = 40 if dtype == torch.bfloat16 else 5
+    vs = torch.exp2(torch.randint(-most, most, (blocks, hkv), generator=gen).float()).to(DEV)
+    q = torch.full((n, 4, d), size * sign, dtype=dtype, device=DEV)
+    for scale in (1.0, 2.0 ** -6):
+        out = paged.attention(q, k, v, table, i32(slot), i32([0, n]), i32([m]), softmax_scale=scale, k_scale=ks, v_scale=vs)
+        block = int(table[slot[0], pick // 128])
+        want = (v[block, pick % 128].float().double() * vs[block].double()[:, None]).repeat_interleave(2, 0)[None].expand(n, 4, d)
+        assert bool(((out.double() - want).abs() <= ref.rounding(want, dtype) + want.abs() * 2.0 ** -20).all())
+
+
 def test_attention_over_8_bits_options():
     nq, kv = [3, 50], [200, 260]
     for nq in ([3, 1], [3, 50]):
@@ -714,13 +740,17 @@ def test_calls_on_another_stream():
     assert all(same(a, b) for a, b in zip(*pools)) and all(torch.equal(a, b) for a, b in zip(*scale))
 
 
-def test_results_repeat_bit_for_bit():
-    for n in (1, 33):
-        q, k, ks, v, vs, table, slot = attend_inputs([n] * 3, [3000, 100, 900], 8, 2, 128, torch.bfloat16, False, 30)
-        args = (table, i32(slot), i32([0, n, 2 * n, 3 * n]), i32([3000, 100, 900]))
-        first = paged.attention(q, k, v, *args, k_scale=ks, v_scale=vs)
-        for _ in range(20):
-            assert torch.equal(first, paged.attention(q, k, v, *args, k_scale=ks, v_scale=vs))
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads,nq,kv", [((8, 2), [1, 1, 1], [3000, 100, 900]), ((8, 2), [33, 33, 33], [3000, 100, 900]), ((6, 2), [257], [900]),
+                                         ((8, 2), [256], [1024]), ((6, 2), [100, 1, 33], [500, 130, 33])])
+def test_results_repeat_bit_for_bit(d, heads, nq, kv):
+    """Tiles cut between CTAs at many places, whose loads, conversions and products run ahead of one another differently each time."""
+    q, k, ks, v, vs, table, slot = attend_inputs(nq, kv, *heads, d, torch.bfloat16, False, 30)
+    args = (table, i32(slot), i32(starts_of(nq)), i32(kv))
+    first = paged.attention(q, k, v, *args, k_scale=ks, v_scale=vs)
+    check_attended(first, q, k, ks, v, vs, table, slot, nq, kv)
+    differ = sum(not torch.equal(first, paged.attention(q, k, v, *args, k_scale=ks, v_scale=vs)) for _ in range(300))
+    assert differ == 0
 
 
 def test_offsets_past_32_bits():
