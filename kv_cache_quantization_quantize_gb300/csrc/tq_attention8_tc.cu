@@ -160,10 +160,10 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
     ++at;
     return g.n_all >= 0;
   };
-  // The softmax threads hold half a row of scores: they take registers from the other warps (256 x 168 + 256 x 88 = 512 x
-  // 128, what the block was launched with).
+  // The softmax threads hold a row of scores: they take registers from the other warps (256 x 208 + 256 x 48 = 512 x 128,
+  // what the block was launched with).
   if (warp >= kMmaWarp) {
-    set_regs_dec<88>();
+    set_regs_dec<48>();
     if (warp == kTmaWarp) {
       // ---- K and V tiles as they lie: for every unit, ring entry e holds K and entry e + 1 its V ----
       int e = 0, issued = 0;
@@ -310,8 +310,12 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
       if (!ok && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
     } else if (warp >= kConvert) {
       // ---- e4m3 to f16: a thread takes 16 channels of a token at a time ----
-      constexpr int kPer = D / 16, kTake = Sh::kRaw / 16 / 128;
-      const int id = threadIdx.x - kConvert * 32;
+      constexpr int kPer = D / 16, kTake = Sh::kRaw / 16 / 128, kRows = 128 / kPer;  // rows of one step of all threads
+      const int id = threadIdx.x - kConvert * 32, c = id % kPer;
+      const int to = (c >> 2) * (BN * 128) + id / kPer * 128;  // steps are multiples of 8 rows: one place in the swizzle
+      // lanes of every second 64 channels write their second half first: no bank conflicts
+      const bool odd = (c >> 2) & 1;
+      const uint32_t x_at = ((((c & 3) * 2 + odd) ^ (id / kPer)) & 7) << 4;
       int e = 0;
       Part g;
       while (ok && take(g)) {
@@ -323,22 +327,26 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
             ok = warp_wait(&raw_full[rs], (e / SR) & 1);
             if (ok && e >= ST) ok = warp_wait(&empty[fs], (e / ST - 1) & 1);
             if (!ok) break;
-            const uint4* src = reinterpret_cast<const uint4*>(sraw + rs * Sh::kRaw) + id;
-            uint4 v[kTake];
+            const uint8_t* src = sraw + rs * Sh::kRaw + id * 16;
+            uint8_t* dst = skv + fs * kTile + to;
 #pragma unroll
-            for (int i = 0; i < kTake; ++i) v[i] = src[128 * i];
-            uint8_t* dst = skv + fs * kTile;
+            for (int i0 = 0; i0 < kTake; i0 += 4) {  // loads in flight
+              uint4 v[4];
 #pragma unroll
-            for (int i = 0; i < kTake; ++i) {
-              const int at = id + 128 * i, row = at / kPer, c = at % kPer;
-              if (which && row >= valid) v[i] = make_uint4(0, 0, 0, 0);  // 0 x NaN is NaN
-              const uint4 lo = make_uint4(e4m3_lo(v[i].x), e4m3_hi(v[i].x), e4m3_lo(v[i].y), e4m3_hi(v[i].y));
-              const uint4 hi = make_uint4(e4m3_lo(v[i].z), e4m3_hi(v[i].z), e4m3_lo(v[i].w), e4m3_hi(v[i].w));
-              // lanes of the second 64 channels begin with their second half: no bank conflicts
-              const int odd = (c >> 2) & 1;
-              uint8_t* p = dst + (c >> 2) * (BN * 128) + row * 128;
-              *reinterpret_cast<uint4*>(p + ((((c & 3) * 2 + odd) ^ (row & 7)) << 4)) = odd ? hi : lo;
-              *reinterpret_cast<uint4*>(p + ((((c & 3) * 2 + 1 - odd) ^ (row & 7)) << 4)) = odd ? lo : hi;
+              for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(src + (i0 + i) * 2048);
+              if (which && valid < BN) {  // rows behind the sequence: 0 x NaN is NaN
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (id / kPer + (i0 + i) * kRows >= valid) v[i] = make_uint4(0, 0, 0, 0);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t x0 = odd ? v[i].z : v[i].x, x1 = odd ? v[i].w : v[i].y;
+                const uint32_t y0 = odd ? v[i].x : v[i].z, y1 = odd ? v[i].y : v[i].w;
+                uint8_t* p = dst + (i0 + i) * (kRows * 128);
+                *reinterpret_cast<uint4*>(p + x_at) = make_uint4(e4m3_lo(x0), e4m3_hi(x0), e4m3_lo(x1), e4m3_hi(x1));
+                *reinterpret_cast<uint4*>(p + (x_at ^ 16)) = make_uint4(e4m3_lo(y0), e4m3_hi(y0), e4m3_lo(y1), e4m3_hi(y1));
+              }
             }
             fence_async_smem();
             __syncwarp();
@@ -354,7 +362,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
       if (!ok && lane == 0 && a.status) atomicOr(a.status, TQ_DEV_ERR_TIMEOUT);
     }
   } else {
-    set_regs_inc<168>();
+    set_regs_inc<208>();
     // ---- softmax of tile t: a thread per row (kPair: of every other unit) ----
     constexpr bool kPair = Sh::kPair;
     const int wg = warp >> 2, t = kPair ? 0 : wg, row_t = threadIdx.x & 127;
@@ -458,31 +466,31 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           ok = warp_wait(&turn[t], (t == 1 ? turns : turns - 1) & 1);
           if (!ok) break;
         }
-        // 64 scores at a time in registers: the upper half of 128 is read for the maximum and again for its weights
-        constexpr int kHalf = 64;
-        float s[kHalf], top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        const int base = (u0 + k) * BN, left = base + BN > lim_all ? lim - base : BN;
-        const bool masked = base + BN > lim_all;
-        auto read = [&](int c0) {
+        float s[BN];
 #pragma unroll
-          for (int c = 0; c < kHalf; c += 32) tmem_ld32_async(ts + buf_of(j) * Sh::kBuf + c0 + c, s + c);
-          tmem_wait_ld();
-          tie32(s);
-          tie32(s + 32);
-          if (masked) {
+        for (int c = 0; c < BN; c += 32) tmem_ld32_async(ts + buf_of(j) * Sh::kBuf + c, s + c);
+        tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < kHalf; ++c) s[c] = c0 + c < left ? s[c] : -INFINITY;
-          }
-        };
-#pragma unroll
-        for (int c0 = BN - kHalf; c0 >= 0; c0 -= kHalf) {
-          read(c0);
-#pragma unroll
-          for (int c = 0; c < kHalf; c += 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[c + i], s[c + 4 + i]);
-          }
+        for (int c = 0; c < BN; c += 32) tie32(s + c);
+        if constexpr (Sh::kOwnP) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[bi]);
         }
+        const int base = (u0 + k) * BN;
+        if (base + BN > lim_all) {
+          const int left = lim - base;
+#pragma unroll
+          for (int c = 0; c < BN; ++c) s[c] = c < left ? s[c] : -INFINITY;
+        }
+        float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < BN - 4; c += 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top[i] = max3(top[i], s[c + i], s[c + 4 + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], s[BN - 4 + i]);
         const float mx = fmaxf(max3(top[0], top[1], top[2]), top[3]) * scale;
         if (kPair && k > 0) {
           ok = warp_wait(&m_full[other8], turn_of(j - 1));
@@ -529,11 +537,10 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
         // s * scale - mu in one rounding is off by what mu was rounded by, the same for all tokens of the row. Past kFar it would
         // leave the weights' range: there the scores are rounded as mu was, and then taken from it.
         const bool by_steps = special && __any_sync(0xffffffffu, far);
-        auto take_steps = [&] {
+        if (by_steps) {
 #pragma unroll
-          for (int c = 0; c < kHalf; ++c) s[c] = __fsub_rn(__fmul_rn(s[c], scale), mu) + above;
-        };
-        if (by_steps) take_steps();
+          for (int c = 0; c < BN; ++c) s[c] = __fsub_rn(__fmul_rn(s[c], scale), mu) + above;
+        }
         m = mn;
         mv = mvn;
         const float from = by_steps ? 0.f : above - mu;
@@ -542,28 +549,18 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // the product with the first half of V starts while the second is made
-          if (BN > kHalf && half == 1) {
-            read(kHalf);
-            if constexpr (Sh::kOwnP) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&s_free[bi]);
-            }
-            if (by_steps) take_steps();
-          }
-          const int at = BN > kHalf ? 0 : half * (BN / 2);  // of this half in s
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 32) {
+          for (int c = half * (BN / 2); c < (half + 1) * (BN / 2); c += 32) {
             uint32_t p[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              float2 y = fma2(make_float2(s[at + c + 2 * i], s[at + c + 2 * i + 1]), sc, off);
+              float2 y = fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), sc, off);
               y.x = exp2_fast(y.x);
               y.y = exp2_fast(y.y);
               sum[i & 1] = add2(sum[i & 1], y);
               p[i] = pack2<false>(y.x, y.y);
             }
-            tmem_st16(tp + buf_of(j) * Sh::kBuf + (half * (BN / 2) + c) / 2, p);
+            tmem_st16(tp + buf_of(j) * Sh::kBuf + c / 2, p);
           }
           tmem_wait_st();
           tc_fence_before();
