@@ -1,6 +1,7 @@
 // Rotary positions, and a step's new tokens rotated on their way into a paged cache of 16 or 8 bits: tq_rotate,
 // tq_paged_extend.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "tq_device.cuh"
@@ -12,22 +13,58 @@ __device__ __forceinline__ void report(uint32_t* status, uint32_t bits) {
   if (bits && status) atomicOr(status, bits);
 }
 
+// Two floats at a time.
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float flip(float x, uint32_t sign) { return __uint_as_float(__float_as_uint(x) ^ sign); }
+
 // ---- rotation ----
 
-// Cosine and sine of position * turns (turns in 2^-64 of a whole turn), times factor. The product modulo 2^64 is the angle
-// modulo a turn without error; its upper 32 bits are taken to the nearest quarter turn before they become a float, so
-// that the rest, at most an eighth of a turn, is rounded to 2^-25 of itself.
-__device__ __forceinline__ void turn(int position, uint64_t turns, float factor, float& c, float& s) {
-  const uint32_t f = (uint32_t)(((uint64_t)(int64_t)position * turns) >> 32);
-  const uint32_t q = (f + (1u << 29)) >> 30;
-  const float x = (float)(int32_t)(f - (q << 30)) * 4.656612873077392578125e-10f;  // 2^-31: in half turns
-  float cx, sx;
-  sincospif(x, &sx, &cx);
-  cx *= factor;
-  sx *= factor;
-  const float a = q & 1 ? sx : cx, b = q & 1 ? cx : sx;
-  c = (q + 1) & 2 ? -a : a;
-  s = q & 2 ? -b : b;
+// Cosines and sines of position * turns (in 2^-64 of a whole turn) of two pairs, times factor, the sines with the sign bit
+// `inverse` flipped. The product modulo 2^64 is the angle modulo a turn without error; its upper 32 bits are taken to the
+// nearest quarter turn before they become a float, so that the rest x, at most a quarter of a half turn, is rounded to
+// 2^-25 of itself. There sin(pi x) and cos(pi x) are their Taylor series to x^9 and x^10, whose next terms are below
+// 2e-9: two pairs at a time these are half the instructions of the library's functions (65536 tokens x 8 heads into 8
+// bits: 109 us with those).
+__device__ __forceinline__ void turn2(int position, const uint64_t* turns, float factor, uint32_t inverse, float2& c, float2& s) {
+  float x[2];
+  uint32_t q[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t f = (uint32_t)(((uint64_t)(int64_t)position * turns[i]) >> 32);
+    q[i] = (f + (1u << 29)) >> 30;
+    x[i] = (float)(int32_t)(f - (q[i] << 30));  // in 2^-31 of a half turn
+  }
+  const float2 y = mul2(make_float2(x[0], x[1]), both(4.656612873077392578125e-10f)), t = mul2(y, y);
+  float2 sn = fma2(t, both(0.08214588661112823f), both(-0.5992645293207921f));  // pi^9 / 9!, -pi^7 / 7!
+  sn = fma2(t, sn, both(2.550164039877345f));
+  sn = fma2(t, sn, both(-5.16771278004997f));
+  sn = fma2(t, sn, both(3.141592653589793f));
+  sn = mul2(sn, y);
+  float2 cs = fma2(t, both(-0.02580689139001406f), both(0.2353306303588935f));  // -pi^10 / 10!, pi^8 / 8!
+  cs = fma2(t, cs, both(-1.335262768854589f));
+  cs = fma2(t, cs, both(4.058712126416768f));
+  cs = fma2(t, cs, both(-4.934802200544679f));
+  cs = fma2(t, cs, both(1.f));
+  sn = mul2(sn, both(factor));
+  cs = mul2(cs, both(factor));
+  c = make_float2(flip(q[0] & 1 ? sn.x : cs.x, (q[0] + 1) << 30 & 0x80000000u), flip(q[1] & 1 ? sn.y : cs.y, (q[1] + 1) << 30 & 0x80000000u));
+  s = make_float2(flip(q[0] & 1 ? cs.x : sn.x, (q[0] << 30 & 0x80000000u) ^ inverse),
+                  flip(q[1] & 1 ? cs.y : sn.y, (q[1] << 30 & 0x80000000u) ^ inverse));
 }
 
 // A thread's 2 CH channels of a head: CH from lo and CH from hi on; its pairs are CH j .. CH j + CH - 1.
@@ -43,30 +80,28 @@ struct Place {
   }
 };
 
+// Cosines and sines of a thread's pairs, two and two.
 template <int CH>
 struct Turned {
-  float c[CH], s[CH];
+  float2 c[CH / 2], s[CH / 2];
   __device__ __forceinline__ void at(const Rotation& r, const uint64_t (&turns)[CH], int position) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      turn(position, turns[i], r.factor, c[i], s[i]);
-      if (r.inverse) s[i] = -s[i];
-    }
+    for (int i = 0; i < CH / 2; ++i) turn2(position, turns + 2 * i, r.factor, (uint32_t)r.inverse << 31, c[i], s[i]);
   }
   __device__ __forceinline__ void apply(const Rotation& r, float (&x)[2 * CH]) const {
     if (r.interleaved) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * c[i] - b * s[i];
-        x[2 * i + 1] = b * c[i] + a * s[i];
+        const float a = x[2 * i], b = x[2 * i + 1], ci = i & 1 ? c[i / 2].y : c[i / 2].x, si = i & 1 ? s[i / 2].y : s[i / 2].x;
+        x[2 * i] = a * ci - b * si;
+        x[2 * i + 1] = b * ci + a * si;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const float a = x[i], b = x[CH + i];
-        x[i] = a * c[i] - b * s[i];
-        x[CH + i] = b * c[i] + a * s[i];
+      for (int i = 0; i < CH / 2; ++i) {
+        const float2 a = make_float2(x[2 * i], x[2 * i + 1]), b = make_float2(x[CH + 2 * i], x[CH + 2 * i + 1]);
+        const float2 y = fma2(b, make_float2(-s[i].x, -s[i].y), mul2(a, c[i])), z = fma2(a, s[i], mul2(b, c[i]));
+        x[2 * i] = y.x, x[2 * i + 1] = y.y, x[CH + 2 * i] = z.x, x[CH + 2 * i + 1] = z.y;
       }
     }
   }
@@ -80,56 +115,89 @@ __device__ __forceinline__ void load_turns(const Rotation& r, int j, uint64_t (&
 
 // ---- rows ----
 
-template <typename T>
-__device__ __forceinline__ float as_float(T x) {
-  return static_cast<float>(x);
+// Two values of 16 bits in a word, the first in the low half.
+__device__ __forceinline__ float2 unpack(uint32_t x, __nv_bfloat16) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack(uint32_t x, __half) { return __half22float2(*reinterpret_cast<__half2*>(&x)); }
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __nv_bfloat16) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// CH elements at each of two places. VEC: 16-byte aligned.
+// CH elements at each of two places, as words. VEC: 16-byte aligned.
 template <typename T, int CH, bool VEC>
 struct Pieces {
-  alignas(16) T lo[CH], hi[CH];
-  __device__ __forceinline__ void load(const T* p, const Place<CH>& at) {
+  static constexpr int kWords = CH * (int)sizeof(T) / 4;
+  uint32_t lo[kWords], hi[kWords];
+  __device__ __forceinline__ static void load_at(const T* p, uint32_t (&w)[kWords]) {
     if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < (int)(CH * sizeof(T) / 16); ++i) {
-        reinterpret_cast<uint4*>(lo)[i] = *(reinterpret_cast<const uint4*>(p + at.lo) + i);
-        reinterpret_cast<uint4*>(hi)[i] = *(reinterpret_cast<const uint4*>(p + at.hi) + i);
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p + i * (4 / sizeof(T)));
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
       }
-    } else {
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        lo[i] = p[at.lo + i];
-        hi[i] = p[at.hi + i];
+      for (int i = 0; i < kWords; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+    } else {
+      const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
+    }
+  }
+  __device__ __forceinline__ static void store_at(T* p, const uint32_t (&w)[kWords]) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4*>(p + i * (4 / sizeof(T))) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) reinterpret_cast<uint32_t*>(p)[i] = w[i];
+    } else {
+      uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        q[2 * i] = (uint16_t)w[i];
+        q[2 * i + 1] = (uint16_t)(w[i] >> 16);
       }
     }
   }
+  __device__ __forceinline__ void load(const T* p, const Place<CH>& at) {
+    load_at(p + at.lo, lo);
+    load_at(p + at.hi, hi);
+  }
+  __device__ __forceinline__ void store(T* p, const Place<CH>& at) const {
+    store_at(p + at.lo, lo);
+    store_at(p + at.hi, hi);
+  }
   __device__ __forceinline__ void floats(float (&x)[2 * CH]) const {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      x[i] = as_float(lo[i]);
-      x[CH + i] = as_float(hi[i]);
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        x[i] = __uint_as_float(lo[i]);
+        x[CH + i] = __uint_as_float(hi[i]);
+      } else {
+        const float2 a = unpack(lo[i], T()), b = unpack(hi[i], T());
+        x[2 * i] = a.x, x[2 * i + 1] = a.y, x[CH + 2 * i] = b.x, x[CH + 2 * i + 1] = b.y;
+      }
     }
   }
   __device__ __forceinline__ void round(const float (&x)[2 * CH]) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      lo[i] = T(x[i]);
-      hi[i] = T(x[CH + i]);
-    }
-  }
-  __device__ __forceinline__ void store(T* p, const Place<CH>& at) const {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < (int)(CH * sizeof(T) / 16); ++i) {
-        *(reinterpret_cast<uint4*>(p + at.lo) + i) = reinterpret_cast<const uint4*>(lo)[i];
-        *(reinterpret_cast<uint4*>(p + at.hi) + i) = reinterpret_cast<const uint4*>(hi)[i];
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        p[at.lo + i] = lo[i];
-        p[at.hi + i] = hi[i];
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 4) {
+        lo[i] = __float_as_uint(x[i]);
+        hi[i] = __float_as_uint(x[CH + i]);
+      } else {
+        lo[i] = pack(x[2 * i], x[2 * i + 1], T());
+        hi[i] = pack(x[CH + 2 * i], x[CH + 2 * i + 1], T());
       }
     }
   }
@@ -292,8 +360,10 @@ int rows_ctas(RowsArgs& a, int ch, int sms) {
 
 // =============================================================================================
 // Into pages of 8 bits. A CTA takes one page of one request and every Y-th of its 2 x n_kv_heads items (keys or values
-// of a head). Runs of up to kShort new tokens take a warp per item, longer ones the CTA; the rotated values stay in registers
-// between the largest of them and their rounding, so that everything is read once.
+// of a head). Runs of up to kShort new tokens take a warp per item, longer ones the CTA. The rows stay in registers, as they
+// came, between the largest of them and their rounding, so that everything is read once; K is rotated twice for that, with
+// cosines and sines that a thread makes once for all heads and keeps in shared memory of its own (4 x 8 pairs: registers
+// would leave one CTA to an SM).
 // Page j of request b has number starts[b] / 128 + 2 b + j: n new tokens touch at most n / 128 + 2 pages, so numbers
 // never meet, and a CTA finds its request from starts alone.
 // =============================================================================================
@@ -305,10 +375,12 @@ struct PagesArgs {
 constexpr int kShort = 8;
 constexpr int kLeast = -60, kMost = 60;
 
-// Two numbers of e4m3, to nearest even, at most 448.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+// Four numbers of e4m3, to nearest even, at most 448; and two as floats.
+__device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
 __device__ __forceinline__ float2 e4m3x2_floats(uint32_t x) {
@@ -339,12 +411,26 @@ __device__ __forceinline__ float largest(const float (&x)[N], float top) {
   return top;
 }
 
+// The largest of x and top, infinite where one is (NaN does not count).
+template <int N>
+__device__ __forceinline__ float largest_any(const float (&x)[N], float top) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(fabsf(x[i])), "f"(fabsf(x[i + 1])));
+    top = r;
+  }
+  return top;
+}
+
 template <int CH>
 __device__ __forceinline__ void store8(uint8_t* p, const Place<CH>& at, const float (&x)[2 * CH], float by) {
   uint32_t w[CH / 2];
 #pragma unroll
-  for (int i = 0; i < CH / 2; ++i)
-    w[i] = e4m3x2(x[4 * i] * by, x[4 * i + 1] * by) | e4m3x2(x[4 * i + 2] * by, x[4 * i + 3] * by) << 16;
+  for (int i = 0; i < CH / 2; ++i) {
+    const float2 a = mul2(make_float2(x[4 * i], x[4 * i + 1]), both(by)), b = mul2(make_float2(x[4 * i + 2], x[4 * i + 3]), both(by));
+    w[i] = e4m3x4(a, b);
+  }
   if constexpr (CH == 8) {
     *reinterpret_cast<uint2*>(p + at.lo) = make_uint2(w[0], w[1]);
     *reinterpret_cast<uint2*>(p + at.hi) = make_uint2(w[2], w[3]);
@@ -373,25 +459,28 @@ __device__ __forceinline__ void rescale(uint8_t* page, int64_t row, int n, float
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float2 x = e4m3x2_floats(w[q] & 0xffffu), y = e4m3x2_floats(w[q] >> 16);
-        w[q] = e4m3x2(x.x * by, x.y * by) | e4m3x2(y.x * by, y.y * by) << 16;
+        w[q] = e4m3x4(mul2(x, both(by)), mul2(y, both(by)));
       }
       *reinterpret_cast<uint4*>(page + (int64_t)(i / kPer) * row + (i % kPer) * 16) = v[k];
     }
   }
 }
 
-template <int D>
+template <int D, int CH>
 struct PagesShape {
   static constexpr int kThreads = D == 256 ? 512 : 256;
+  static constexpr int kHead = D / (2 * CH);  // threads of a token's head
+  static constexpr int kRun = kThreads / kHead;  // tokens that the CTA has in one pass
+  static constexpr int kPasses = (kPage + kRun - 1) / kRun;
+  static constexpr int kSmem = kPasses * kThreads * CH * 8;  // cosines and sines
 };
 
 template <typename T, int D, int CH, bool VEC>
 __device__ void pages_part(const PagesArgs& p) {
-  constexpr int kThreads = PagesShape<D>::kThreads, kWarps = kThreads / 32;
-  constexpr int kHead = D / (2 * CH);           // threads of a token's head
-  constexpr int kRun = kThreads / kHead;        // tokens that the CTA has in one pass
-  constexpr int kPasses = (kPage + kRun - 1) / kRun;
+  using Sh = PagesShape<D, CH>;
+  constexpr int kThreads = Sh::kThreads, kWarps = kThreads / 32, kHead = Sh::kHead, kRun = Sh::kRun, kPasses = Sh::kPasses;
   constexpr int kWarpRun = 32 / kHead, kWarpPasses = kShort / kWarpRun;
+  extern __shared__ float4 angles[];  // [pass][CH / 2][thread]: cosines and sines of two pairs
   __shared__ float tops[2][kWarps];
   const RowsArgs& a = p.rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -415,22 +504,18 @@ __device__ void pages_part(const PagesArgs& p) {
     return;
   }
   const int hkv = a.heads[1], items = 2 * hkv;
-  float* const scales[2] = {p.scales.k + (int64_t)block * p.scales.k_block, p.scales.v + (int64_t)block * p.scales.v_block};
+  auto scale_at = [&](int w, int h) {
+    return (w ? p.scales.v + (int64_t)block * p.scales.v_block : p.scales.k + (int64_t)block * p.scales.k_block) + h;
+  };
   const bool alone = n <= kShort;
   const int id = alone ? lane : threadIdx.x, j = id % kHead, run0 = id / kHead;
   const Place<CH> at(a.rot, j);
   uint64_t turns[CH];
   if (at.turned) load_turns<CH>(a.rot, j, turns);
-  auto load = [&](int w, int h, int i, float (&x)[2 * CH]) {  // new token i of the page, rotated
-    Pieces<T, CH, VEC> in;
+  auto load = [&](int w, int h, int i, Pieces<T, CH, VEC>& in) {  // new token i of the page
     in.load(static_cast<const T*>(a.x[1 + w]) + (int64_t)(row0 + i) * a.x_row[1 + w] + (int64_t)h * a.x_head[1 + w], at);
-    in.floats(x);
-    if (w == 0 && at.turned) {
-      Turned<CH> t;
-      t.at(a.rot, turns, a.positions ? a.positions[row0 + i] : lo + i);
-      t.apply(a.rot, x);
-    }
   };
+  auto turn_to = [&](int i, Turned<CH>& t) { t.at(a.rot, turns, a.positions ? a.positions[row0 + i] : lo + i); };
   if (alone) {
     for (int item = y + p.y * warp; item < items; item += p.y * kWarps) {
       const int w = item >= hkv, h = item - w * hkv;
@@ -440,11 +525,18 @@ __device__ void pages_part(const PagesArgs& p) {
       for (int k = 0; k < kWarpPasses; ++k) {
         const int i = k * kWarpRun + run0;
         if (i < n) {
-          load(w, h, i, x[k]);
+          Pieces<T, CH, VEC> in;
+          load(w, h, i, in);
+          in.floats(x[k]);
+          if (w == 0 && at.turned) {
+            Turned<CH> t;
+            turn_to(i, t);
+            t.apply(a.rot, x[k]);
+          }
           top = largest<2 * CH>(x[k], top);
         }
       }
-      const float held = at0 ? held_scale(scales[w][h]) : 0.f;
+      const float held = at0 ? held_scale(*scale_at(w, h)) : 0.f;
       const float scale = fmaxf(held, scale_of(warp_max(top))), by = 1.f / scale;
       if (at0 && scale > held) rescale<D>(to, a.o_row[1 + w], at0, held / scale, lane, 32);
 #pragma unroll
@@ -452,46 +544,101 @@ __device__ void pages_part(const PagesArgs& p) {
         const int i = k * kWarpRun + run0;
         if (i < n) store8<CH>(to + (int64_t)(at0 + i) * a.o_row[1 + w], at, x[k], by);
       }
-      if (lane == 0) scales[w][h] = scale;
+      if (lane == 0) *scale_at(w, h) = scale;
     }
     return;
   }
+  float4* const mine = angles + threadIdx.x;
+  if (at.turned && y < hkv) {
+#pragma unroll 1
+    for (int k = 0; k < kPasses; ++k) {
+      if (k * kRun + run0 >= n) break;
+      Turned<CH> t;
+      turn_to(k * kRun + run0, t);
+#pragma unroll
+      for (int i = 0; i < CH / 2; ++i)
+        mine[(k * (CH / 2) + i) * kThreads] = make_float4(t.c[i].x, t.c[i].y, t.s[i].x, t.s[i].y);
+    }
+  }
   int buf = 0;
-  for (int item = y; item < items; item += p.y, buf ^= 1) {
+  for (int item = y; item < items; item += p.y) {
     const int w = item >= hkv, h = item - w * hkv;
     uint8_t* const to = static_cast<uint8_t*>(a.out[1 + w]) + (int64_t)block * a.o_block[1 + w] + (int64_t)h * a.o_head[1 + w];
-    float x[kPasses][2 * CH], top = 0.f;
+    Pieces<T, CH, VEC> in[kPasses];
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k) {
-      const int i = k * kRun + run0;
-      if (i < n) {
-        load(w, h, i, x[k]);
-        top = largest<2 * CH>(x[k], top);
+    for (int k = 0; k < kPasses; ++k)
+      if (k * kRun + run0 < n) load(w, h, k * kRun + run0, in[k]);
+    auto values = [&](int k, float (&x)[2 * CH]) {
+      in[k].floats(x);
+      if (w == 0 && at.turned) {
+        Turned<CH> t;
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          const float4 v = mine[(k * (CH / 2) + i) * kThreads];
+          t.c[i] = make_float2(v.x, v.y);
+          t.s[i] = make_float2(v.z, v.w);
+        }
+        t.apply(a.rot, x);
       }
-    }
-    const float held = at0 ? held_scale(scales[w][h]) : 0.f;
-    top = warp_max(top);
-    if (lane == 0) tops[buf][warp] = top;
-    __syncthreads();
+    };
+    auto top_of = [&](auto largest_of) {  // over the CTA
+      float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, tops[buf][i]);
+      for (int k = 0; k < kPasses; ++k) {
+        if (k * kRun + run0 < n) {
+          float x[2 * CH];
+          values(k, x);
+          top = largest_of(x, top);
+        }
+      }
+      top = warp_max(top);
+      if (lane == 0) tops[buf][warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) top = fmaxf(top, tops[buf][i]);
+      buf ^= 1;
+      return top;
+    };
+    const float held = at0 ? held_scale(*scale_at(w, h)) : 0.f;
+    float top = top_of([](const float (&x)[2 * CH], float t) { return largest_any<2 * CH>(x, t); });
+    if (top == INFINITY) top = top_of([](const float (&x)[2 * CH], float t) { return largest<2 * CH>(x, t); });
     const float scale = fmaxf(held, scale_of(top)), by = 1.f / scale;
     if (at0 && scale > held) rescale<D>(to, a.o_row[1 + w], at0, held / scale, threadIdx.x, kThreads);
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {
       const int i = k * kRun + run0;
-      if (i < n) store8<CH>(to + (int64_t)(at0 + i) * a.o_row[1 + w], at, x[k], by);
+      if (i < n) {
+        float x[2 * CH];
+        values(k, x);
+        store8<CH>(to + (int64_t)(at0 + i) * a.o_row[1 + w], at, x, by);
+      }
     }
-    if (threadIdx.x == 0) scales[w][h] = scale;
+    if (threadIdx.x == 0) *scale_at(w, h) = scale;
   }
 }
 
 template <typename T, int D, int CH, bool VEC>
-__global__ void __launch_bounds__(PagesShape<D>::kThreads) k_extend_pages(const __grid_constant__ PagesArgs p) {
+__global__ void __launch_bounds__(PagesShape<D, CH>::kThreads, D == 256 ? 1 : 2) k_extend_pages(const __grid_constant__ PagesArgs p) {
   pdl_wait();
   const int queries = p.pages * p.y;
   if ((int)blockIdx.x < queries) pages_part<T, D, CH, VEC>(p);
   else if (threadIdx.x < kRowsThreads) rows_part<T, CH, VEC>(p.rows, blockIdx.x - queries);
+}
+
+template <typename T, int D, int CH, bool VEC>
+cudaError_t launch_pages_as(const PagesArgs& p, unsigned grid, cudaStream_t s) {
+  using Sh = PagesShape<D, CH>;
+  static std::atomic<uint64_t> known{0};  // devices whose kernel may use kSmem
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (e == cudaSuccess && !(known.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(k_extend_pages<T, D, CH, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+    if (e == cudaSuccess) known.fetch_or(bit, std::memory_order_relaxed);
+  }
+  if (e != cudaSuccess) return e;
+  // without a run that the CTA takes together nothing is kept
+  return launch_pdl(k_extend_pages<T, D, CH, VEC>, dim3(grid), dim3(Sh::kThreads), p.rows.n_rows > kShort ? Sh::kSmem : 0, s, p);
 }
 
 template <typename T, int CH, bool VEC>
@@ -502,9 +649,9 @@ cudaError_t launch_pages_d(PagesArgs& p, int sms, cudaStream_t s) {
   a.per = q.per;
   const int64_t grid = (int64_t)p.pages * p.y + query_ctas;
   if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  if (a.d == 64) return launch_pdl(k_extend_pages<T, 64, CH, VEC>, dim3((unsigned)grid), dim3(PagesShape<64>::kThreads), 0, s, p);
-  if (a.d == 128) return launch_pdl(k_extend_pages<T, 128, CH, VEC>, dim3((unsigned)grid), dim3(PagesShape<128>::kThreads), 0, s, p);
-  return launch_pdl(k_extend_pages<T, 256, CH, VEC>, dim3((unsigned)grid), dim3(PagesShape<256>::kThreads), 0, s, p);
+  if (a.d == 64) return launch_pages_as<T, 64, CH, VEC>(p, (unsigned)grid, s);
+  if (a.d == 128) return launch_pages_as<T, 128, CH, VEC>(p, (unsigned)grid, s);
+  return launch_pages_as<T, 256, CH, VEC>(p, (unsigned)grid, s);
 }
 
 template <typename T>
@@ -593,7 +740,7 @@ cudaError_t launch_paged_extend(const tq_kv& pool, const tq_scales* scales, cons
   // items per CTA: all warps busy in short runs, and enough CTAs for the SMs to take turns in long ones
   const int likely = std::max(1, n.n_rows / kPage + m.batch);
   const int most = n.n_rows / std::max(1, m.batch) > kShort ? items : (items + warps - 1) / warps;
-  p.y = std::min(most, std::max(1, (16 * sms + likely - 1) / likely));
+  p.y = std::min(most, std::max(1, (8 * sms + likely - 1) / likely));
   if (n.dtype == TQ_BF16) return launch_pages<__nv_bfloat16>(p, vec, sms, s);
   if (n.dtype == TQ_F16) return launch_pages<__half>(p, vec, sms, s);
   return launch_pages<float>(p, vec, sms, s);
