@@ -16,13 +16,16 @@ namespace {
 // is of p / vs, so scales cost nothing per element but an addition, and weights are rounded to f16 relative to what they are
 // multiplied with, however far apart the scales of pages are.
 // =============================================================================================
+constexpr int k8TileCost = 64;   // start and end of a tile, as one unit
+constexpr int k8MinPart = 64;    // no CTA gets less than that (2 requests of 100 to 1000 tokens: 15.2 us with 128, 10.9 so)
+
 template <int D, int MT>
 struct Rows8Shape {
   static constexpr int R = 16 * MT;
-  static constexpr int U = D == 64 ? 128 : 64;  // tokens of a unit
+  static constexpr int U = kPage;  // tokens of a unit: a page, which has one scale
   static constexpr int kEntry = U * D;          // bytes of K or V of one unit
   static constexpr int kCtas = D == 256 ? 1 : D == 64 && MT == 1 ? 3 : 2;  // CTAs per SM
-  static constexpr int kEntries = D == 64 ? 6 : 8;                         // bytes in flight: as k_attn_rows
+  static constexpr int kEntries = D == 64 ? 6 : 4;
   static constexpr int kQRow = D * 2 + 16;  // bytes of a query row
   static constexpr int kQ = R * kQRow;
   static constexpr int kP = R * U * 2;  // weights of one unit
@@ -48,7 +51,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
     k_attn8_rows(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v) {
   using Sh = Rows8Shape<D, MT>;
-  using W = Walk<Sh::R, Sh::U, kTileCost, 0>;
+  using W = Walk<Sh::R, Sh::U, k8TileCost, 0>;
   constexpr int U = Sh::U, TW = U / 4, NS = TW / 8;  // tokens of a warp, tiles of 8 of them
   constexpr int R = Sh::R, ST = Sh::kEntries, KS = D / 16, NC = D / 64;  // NC: 16-channel chunks of a warp
   extern __shared__ uint8_t smem_raw[];
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
   __shared__ LineStart first;
   __shared__ int warp_sums[kRowsThreads / 32];
   __shared__ float sx[4][R];  // row maxima or sums of each warp
-  __shared__ UnitScale scales[ST / 2];
+  __shared__ UnitScale scales[ST];  // of unit e / 2
   __shared__ float q_back[2][R];  // what a row's scores are multiplied with
   __shared__ int gave_up;
 
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
   }
   pdl_wait();
   pdl_launch();  // the join may be scheduled; it waits for this kernel's end
-  find_start<W, kRowsThreads>(a, kMinPart, first, warp_sums);
+  find_start<W, kRowsThreads>(a, k8MinPart, first, warp_sums);
   bool ok = true;
 
   if (warp == 4) {
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
             const int st = (e + which) % ST;
             if (ok && e + which >= ST) ok = mbar_wait(&empty[st], ((e + which) / ST - 1) & 1);
             if (!ok) break;
-            if (which == 0) scales[st / 2] = u1;  // read by all before they give the entry back
+            if (which == 0) scales[e / 2 % ST] = u1;  // read by all before they give the entry back
             uint8_t* dst = smem + st * Sh::kEntry;
             mbar_expect_tx(&full[st], Sh::kEntry);
 #pragma unroll
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
         for (int t = 0; t < MT; ++t)
 #pragma unroll
           for (int n = 0; n < NS; ++n) s[t][n][0] = s[t][n][1] = s[t][n][2] = s[t][n][3] = 0.f;
-        if (ok) us = scales[st / 2];
+        if (ok) us = scales[e / 2 % ST];
         if (ok && t0 < g.kv) {
           // at 16 tokens per warp the odd steps have sums of their own: half the chain of dependent products
           constexpr int kChains = NS == 2 ? 2 : 1;
@@ -535,10 +538,18 @@ cudaError_t launch_type(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p,
 
 }  // namespace
 
+namespace {
+template <int D, int MT>
+AttnShape rows8_shape(int sms) {
+  using Sh = Rows8Shape<D, MT>;
+  return {Sh::R, Sh::U, sms * Sh::kCtas, cta_bytes(Sh::R, D), k8TileCost, k8MinPart};
+}
+}  // namespace
+
 AttnShape attn8_rows_shape(int d, int64_t rows, int sms) {
-  const int tile = rows <= 16 ? 16 : 32;
-  const int ctas = sms * (d == 256 ? Rows8Shape<256, 1>::kCtas : d == 64 && tile == 16 ? Rows8Shape<64, 1>::kCtas : 2);
-  return {tile, d == 64 ? Rows8Shape<64, 1>::U : Rows8Shape<128, 1>::U, ctas, cta_bytes(tile, d), kTileCost, kMinPart};
+  if (d == 64) return rows <= 16 ? rows8_shape<64, 1>(sms) : rows8_shape<64, 2>(sms);
+  if (d == 128) return rows <= 16 ? rows8_shape<128, 1>(sms) : rows8_shape<128, 2>(sms);
+  return rows <= 16 ? rows8_shape<256, 1>(sms) : rows8_shape<256, 2>(sms);
 }
 cudaError_t launch_attn8_rows(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {
   return dtype == TQ_BF16 ? launch_type<true>(a, m, p, d, s) : launch_type<false>(a, m, p, d, s);

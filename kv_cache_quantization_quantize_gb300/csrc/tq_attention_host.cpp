@@ -58,10 +58,13 @@ cudaError_t attn_tensor_map8(const tq_kv& kv, bool values, int channels, int box
   auto bytes = [&](cuuint64_t n, int64_t stride) { return n > 1 ? (cuuint64_t)stride : dims[0]; };  // a stride that is never taken: any
   const cuuint64_t strides[3] = {bytes(dims[1], st[1]), bytes(dims[2], st[2]), bytes(dims[3], st[0])};
   const cuuint32_t box[4] = {(cuuint32_t)channels, (cuuint32_t)box_tokens, 1, 1}, estr[4] = {1, 1, 1, 1};
+  // L2 fetches what a token's head has and not the next head's: 32 requests of 4096 to 8192 tokens of 8 heads of 128, heads
+  // of a token together, 75.5 us against 87 with 256 bytes
   const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, values ? kv.v : kv.k, dims, strides, box, estr,
                             CU_TENSOR_MAP_INTERLEAVE_NONE,
                             !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : channels == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            kv.head_dim == 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -26,7 +26,6 @@ With rotary positions, and in a cache of 8 bits (dtype=torch.float8_e4m3fn) in a
 import ctypes
 import math
 import struct
-from fractions import Fraction
 
 import torch
 
@@ -48,6 +47,7 @@ _NEW_ROWS = struct.Struct("@4P8qP3i4x")  # tq_new_rows
 
 
 _I32 = torch.int32
+_F32 = torch.float32
 _HALVES = (torch.bfloat16, torch.float16)
 _E4M3 = torch.float8_e4m3fn
 _raw_memory = None  # see _raw_allocator
@@ -195,11 +195,15 @@ def _scales(k_scale, v_scale, index, blocks, heads):
     """tq_scales, or None where both are None."""
     if k_scale is None and v_scale is None:
         return None
-    for t in (k_scale, v_scale):
-        if (t is None or t.dtype is not torch.float32 or t.get_device() != index or t.shape != (blocks, heads) or (heads > 1 and t.stride(1) != 1)
-                or (blocks > 1 and t.stride(0) < heads)):
-            raise ValueError(f"k_scale, v_scale: expected two float32 tensors [{blocks}, {heads}] with contiguous rows on cuda:{index}")
-    return _SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr(), max(k_scale.stride(0), heads), max(v_scale.stride(0), heads))
+    if k_scale is not None and v_scale is not None and k_scale.dtype is _F32 and v_scale.dtype is _F32 and k_scale.get_device() == index:
+        ks, vs = k_scale.stride(), v_scale.stride()
+        if (v_scale.get_device() == index and k_scale.shape == (blocks, heads) and v_scale.shape == (blocks, heads)
+                and (heads == 1 or ks[1] == 1 and vs[1] == 1) and (blocks == 1 or ks[0] >= heads and vs[0] >= heads)):
+            return _SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr(), max(ks[0], heads), max(vs[0], heads))
+    raise ValueError(f"k_scale, v_scale: expected two float32 tensors [{blocks}, {heads}] with contiguous rows on cuda:{index}")
+
+
+_TURN = 5 * 10 ** 49 * 2 ** 160 // 314159265358979323846264338327950288419716939937511  # 2^160 / (2 pi)
 
 
 class Rotary:
@@ -255,8 +259,8 @@ class Rotary:
             raise ValueError("steps: a multiple of 4 finite numbers, and a finite times")
         self.rotary_dim, self.steps, self.interleaved, self.times = 2 * len(steps), tuple(steps), bool(interleaved), float(times)
         # in 2^-64 of a whole turn, modulo 1
-        two_pi = 2 * Fraction(314159265358979323846264338327950288419716939937511, 10 ** 50)
-        turns = [round(Fraction(t) / two_pi * 2 ** 64) % 2 ** 64 for t in steps]
+        ratios = [t.as_integer_ratio() for t in steps]
+        turns = [((2 * n * _TURN // d >> 96) + 1 >> 1) % 2 ** 64 for n, d in ratios]  # rounded to the nearest
         self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
         self._packed = None
 
@@ -330,6 +334,8 @@ def extend(k, v, k_pool, v_pool, table, seq_ids, starts, totals, rotary=None, po
     rot = None if rotary is None else rotary._pack(index)
     if q is not None and (q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.dtype is not dtype or q.get_device() != index):
         raise ValueError(f"q: expected a {dtype} tensor [{n}, n_q_heads, {d}] on cuda:{index}")
+    if stream is None and torch._C._cuda_getDevice() == index:
+        return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, torch._C._cuda_getCurrentRawStream(index))
     raw, on = _here(index, stream, (k, v, k_pool, v_pool, table, seq_ids, starts, totals, positions, q, q_out, k_scale, v_scale, status,
                                     None if rotary is None else rotary.turns))
     if on is not None:
@@ -543,7 +549,10 @@ class PagedCache:
         if dtype not in (torch.bfloat16, torch.float16, _E4M3):
             raise ValueError("dtype: bf16, f16 or float8_e4m3fn")
         self.pool = pool
-        self.kv = torch.empty((n_layers, 2, pool.n_blocks, PAGE, n_kv_heads, head_dim), dtype=dtype, device=pool.device)
+        if dtype is _E4M3:  # the tokens of a head together: appends and attention take them so, and a row is 64 to 256 bytes
+            self.kv = torch.empty((n_layers, 2, pool.n_blocks, n_kv_heads, PAGE, head_dim), dtype=dtype, device=pool.device).transpose(3, 4)
+        else:
+            self.kv = torch.empty((n_layers, 2, pool.n_blocks, PAGE, n_kv_heads, head_dim), dtype=dtype, device=pool.device)
         self.scales = torch.ones((n_layers, 2, pool.n_blocks, n_kv_heads), device=pool.device) if dtype is _E4M3 else None
 
     def _scales(self, layer):
