@@ -39,6 +39,13 @@ __device__ __forceinline__ uint32_t raw_off(int row, int chunk) {
   if constexpr (D == 64) return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
   else return (uint32_t)((chunk >> 3) * (U * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
+// The product of k_attn_rows, kept in its place: a ring entry is given back behind it, so what it was read from has arrived.
+__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 // Token that column (or row) x of a group of 8 stands for: with rows of 128 bytes, neighbours are four apart, so that the loads of K,
 // of two tokens by eight lanes, meet no bank conflict.
 template <int D>
@@ -297,8 +304,8 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
                 const uint32_t b0 = e4m3_lo(w), b1 = e4m3_hi(w);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                  if constexpr (kChains == 2) mma16816<false>(x & 1 ? s2[t][n] : s[t][n], af[t], b0, b1);
-                  else mma16816<false>(s[t][n], af[t], b0, b1);
+                  if constexpr (kChains == 2) mma8(x & 1 ? s2[t][n] : s[t][n], af[t], b0, b1);
+                  else mma8(s[t][n], af[t], b0, b1);
                 }
               }
             }
@@ -458,8 +465,8 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
                 const uint32_t x0 = e4m3_lo(x), y0 = e4m3_lo(y), x1 = e4m3_hi(x), y1 = e4m3_hi(y);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                  mma16816<false>(o[t][2 * c], ap[j][t], x0, y0);
-                  mma16816<false>(o[t][2 * c + 1], ap[j][t], x1, y1);
+                  mma8(o[t][2 * c], ap[j][t], x0, y0);
+                  mma8(o[t][2 * c + 1], ap[j][t], x1, y1);
                 }
               }
           }
