@@ -22,6 +22,10 @@ constexpr int k8MinPart = 64;    // no CTA gets less than that (2 requests of 10
 template <int D, int MT>
 struct Rows8Shape {
   static constexpr int R = 16 * MT;
+  // Consumers: for the sums each has D / kWarps channels, 16 at least. With 8 at head_dim 128 two CTAs leave 96 registers (32
+  // requests of 4096 to 8192 tokens 93 us, with 4 72); at 256 8 are faster (16 requests of 8 drafts each 62.7 against 68.5).
+  static constexpr int kWarps = D == 256 ? 8 : 4;
+  static constexpr int kThreads = 32 * kWarps + 32;
   static constexpr int U = kPage;  // tokens of a unit: a page, which has one scale
   static constexpr int kEntry = U * D;          // bytes of K or V of one unit
   static constexpr int kCtas = D == 256 ? 1 : D == 64 && MT == 1 ? 3 : 2;  // CTAs per SM
@@ -39,6 +43,17 @@ __device__ __forceinline__ uint32_t raw_off(int row, int chunk) {
   if constexpr (D == 64) return (uint32_t)(row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4));
   else return (uint32_t)((chunk >> 3) * (U * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
 }
+// Barrier over the consumer warps; true for all where the predicate is true for one.
+template <int WARPS>
+__device__ __forceinline__ bool any_of(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)x), "n"(32 * WARPS)
+      : "memory");
+  return r != 0;
+}
 // The product of k_attn_rows, kept in its place: a ring entry is given back behind it, so what it was read from has arrived.
 __device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -54,13 +69,13 @@ __device__ __forceinline__ int tok8(int x) {
 }
 
 template <int D, int MT, bool BF16>
-__global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
+__global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>::kCtas)
     k_attn8_rows(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v) {
   using Sh = Rows8Shape<D, MT>;
   using W = Walk<Sh::R, Sh::U, k8TileCost, 0>;
-  constexpr int U = Sh::U, TW = U / 4, NS = TW / 8;  // tokens of a warp, tiles of 8 of them
-  constexpr int R = Sh::R, ST = Sh::kEntries, KS = D / 16, NC = D / 64;  // NC: 16-channel chunks of a warp
+  constexpr int NW = Sh::kWarps, U = Sh::U, TW = U / NW, NS = TW / 8;  // tokens of a warp, tiles of 8 of them
+  constexpr int R = Sh::R, ST = Sh::kEntries, KS = D / 16, NC = D / (16 * NW);  // NC: 16-channel chunks of a warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint8_t* sp = smem + ST * Sh::kEntry;
@@ -68,8 +83,8 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
   __shared__ alignas(8) uint64_t full[ST], empty[ST], q_full[2], q_empty[2], part_full[kParts], part_empty[kParts];
   __shared__ Part parts[kParts];
   __shared__ LineStart first;
-  __shared__ int warp_sums[kRowsThreads / 32];
-  __shared__ float sx[4][R];  // row maxima or sums of each warp
+  __shared__ int warp_sums[Sh::kThreads / 32];
+  __shared__ float sx[NW][R];  // row maxima or sums of each warp
   __shared__ UnitScale scales[ST];  // of unit e / 2
   __shared__ float q_back[2][R];  // what a row's scores are multiplied with
   __shared__ int gave_up;
@@ -83,24 +98,24 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
     gave_up = 0;
     for (int i = 0; i < ST; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 4);
+      mbar_init(&empty[i], NW);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 4);
+      mbar_init(&q_empty[i], NW);
     }
     for (int i = 0; i < kParts; ++i) {
       mbar_init(&part_full[i], 1);
-      mbar_init(&part_empty[i], 4);
+      mbar_init(&part_empty[i], NW);
     }
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   pdl_wait();
   pdl_launch();  // the join may be scheduled; it waits for this kernel's end
-  find_start<W, kRowsThreads>(a, k8MinPart, first, warp_sums);
+  find_start<W, Sh::kThreads>(a, k8MinPart, first, warp_sums);
   bool ok = true;
 
-  if (warp == 4) {
+  if (warp == NW) {
     // ---- producer: the parts, their queries, and for every unit ring entry e with K and entry e + 1 with V ----
     W w;
     w.start(a, first);
@@ -177,7 +192,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
     return;
   }
 
-  // ---- consumers. A wait that gives up is made known at the next barrier, where all four warps leave together ----
+  // ---- consumers. A wait that gives up is made known at the next barrier, where all of them leave together ----
   const int g8 = lane >> 2, j4 = lane & 3, mi = lane >> 3, ri = lane & 7;
   const int tk0 = tok8<D>(2 * j4), tk1 = tok8<D>(2 * j4 + 1);  // tokens of this thread's two columns of a group of 8
   const uint32_t ring = smem_u32(smem), pbase = smem_u32(sp);
@@ -191,7 +206,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
     Part g = {};
     if (ok) g = parts[pi];
     give_up();
-    if (consumers_any(!ok)) break;
+    if (any_of<NW>(!ok)) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(&part_empty[pi]);
     if (g.n_all < 0) break;
@@ -204,7 +219,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
       if constexpr (BF16) {  // the queries to f16, each row by a power of two
         if (ok) {
           constexpr int kWords = D / 64;
-          for (int row = warp; row < min(R, g.rows - g.f0); row += 4) {
+          for (int row = warp; row < min(R, g.rows - g.f0); row += NW) {
             uint32_t* p = reinterpret_cast<uint32_t*>(sq + qbuf * Sh::kQ + row * Sh::kQRow) + lane;
             uint32_t v[kWords], top = 0;
 #pragma unroll
@@ -221,7 +236,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
           asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");  // the buffer's next queries come by bulk copies
         }
         give_up();
-        if (consumers_any(!ok)) break;
+        if (any_of<NW>(!ok)) break;
       }
     }
     float o[MT][2 * NC][4], m[MT][2], mv[MT][2], l[MT][2], back[MT][2];  // m, mv: of scores, of values' scales
@@ -363,12 +378,12 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
           }
         }
         give_up();
-        if (!consumers_any(need || !ok)) break;
+        if (!any_of<NW>(need || !ok)) break;
         if (*(volatile int*)&gave_up) {
           left = true;
           break;
         }
-        // new maxima for all rows, from all four warps
+        // new maxima for all rows, from all warps
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -377,14 +392,16 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
             top[t][x] = fmaxf(top[t][x], __shfl_xor_sync(0xffffffffu, top[t][x], 2));
             if ((lane & 3) == 0) sx[warp][t * 16 + g8 + x * 8] = top[t][x];
           }
-        consumers_any(false);
+        any_of<NW>(false);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           float alpha[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int row = t * 16 + g8 + x * 8;
-            const float mx = fmaxf(fmaxf(sx[0][row], sx[1][row]), fmaxf(sx[2][row], sx[3][row]));
+            float mx = sx[0][row];
+#pragma unroll
+            for (int i = 1; i < NW; ++i) mx = fmaxf(mx, sx[i][row]);
             alpha[x] = 1.f;
             const float by = (m[t][x] - mx) + (mv[t][x] - us.log_v);
             if (by < 0.f) {
@@ -412,7 +429,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
         l[t][0] += sum[t][0] * us.inv_v;
         l[t][1] += sum[t][1] * us.inv_v;
       }
-      // sums of D / 4 channels over all tokens of the unit
+      // sums of D / NW channels over all tokens of the unit
       {
         const int st = (e + 1) % ST;
         ok = warp_wait(&full[st], ((e + 1) / ST) & 1);
@@ -481,7 +498,7 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
       if (lane == 0) mbar_arrive(&q_empty[q_used & 1]);
       ++q_used;
     }
-    // the row sums of the four warps
+    // the row sums of the warps
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -492,16 +509,18 @@ __global__ void __launch_bounds__(kRowsThreads, Rows8Shape<D, MT>::kCtas)
         if ((lane & 3) == 0) sx[warp][t * 16 + g8 + x * 8] = v;
       }
     give_up();
-    if (consumers_any(!ok)) break;
+    if (any_of<NW>(!ok)) break;
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int row = t * 16 + g8 + x * 8, f = g.f0 + row;
         if (f >= g.rows) continue;
-        const float sum = sx[0][row] + sx[1][row] + sx[2][row] + sx[3][row];
+        float sum = sx[0][row];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) sum += sx[i][row];
         const float part = exp2_fast(mv[t][x]);  // parts of a tile go to the join relative to m alone
-        const int ch = warp * (D / 4) + j4 * 4;  // channels 4 j .. 4 j + 3 of each chunk: even, odd, even, odd
+        const int ch = warp * (D / NW) + j4 * 4;  // channels 4 j .. 4 j + 3 of each chunk: even, odd, even, odd
         if (g.direct) {
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
           const int qi = a.div_g(f), head = g.h * a.G + f - qi * a.G;
@@ -531,7 +550,7 @@ cudaError_t launch_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, c
   static std::atomic<uint64_t> known{0};
   cudaError_t e = allow_smem(k_attn8_rows<D, MT, BF16>, Sh::kSmem, known);
   if (e == cudaSuccess)
-    e = launch_pdl(k_attn8_rows<D, MT, BF16>, dim3(p.ctas), dim3(kRowsThreads), Sh::kSmem, s, a, m.k, m.v);
+    e = launch_pdl(k_attn8_rows<D, MT, BF16>, dim3(p.ctas), dim3(Sh::kThreads), Sh::kSmem, s, a, m.k, m.v);
   if (e != cudaSuccess) return e;
   return launch_join<D, Sh::R, BF16>(a, p.ctas, p.max_rows, s);
 }
