@@ -375,6 +375,10 @@ struct PagesArgs {
 constexpr int kShort = 8;
 constexpr int kLeast = -60, kMost = 60;
 
+// 16 bytes to shared memory, not waited for.
+__device__ __forceinline__ void copy_async(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
 // Four numbers of e4m3, to nearest even, at most 448; and two as floats.
 __device__ __forceinline__ uint32_t e4m3x4(float2 a, float2 b) {
   uint32_t r;
@@ -466,18 +470,21 @@ __device__ __forceinline__ void rescale(uint8_t* page, int64_t row, int n, float
   }
 }
 
-template <int D, int CH>
+template <int D, int CH, int SIZE>
 struct PagesShape {
   static constexpr int kThreads = D == 256 ? 512 : 256;
   static constexpr int kHead = D / (2 * CH);  // threads of a token's head
   static constexpr int kRun = kThreads / kHead;  // tokens that the CTA has in one pass
   static constexpr int kPasses = (kPage + kRun - 1) / kRun;
-  static constexpr int kSmem = kPasses * kThreads * CH * 8;  // cosines and sines
+  // Rows of 16 bits in pieces of 16 bytes are fetched an item ahead, into shared memory that is each thread's own.
+  static constexpr bool kAhead = CH == 8 && SIZE == 2;
+  static constexpr int kAngles = kPasses * kThreads * CH * 8;  // bytes of cosines and sines
+  static constexpr int kSmem = kAngles + (kAhead ? kPasses * kThreads * 32 : 0);
 };
 
 template <typename T, int D, int CH, bool VEC>
 __device__ void pages_part(const PagesArgs& p) {
-  using Sh = PagesShape<D, CH>;
+  using Sh = PagesShape<D, CH, sizeof(T)>;
   constexpr int kThreads = Sh::kThreads, kWarps = kThreads / 32, kHead = Sh::kHead, kRun = Sh::kRun, kPasses = Sh::kPasses;
   constexpr int kWarpRun = 32 / kHead, kWarpPasses = kShort / kWarpRun;
   extern __shared__ float4 angles[];  // [pass][CH / 2][thread]: cosines and sines of two pairs
@@ -549,6 +556,19 @@ __device__ void pages_part(const PagesArgs& p) {
     return;
   }
   float4* const mine = angles + threadIdx.x;
+  uint4* const ahead = reinterpret_cast<uint4*>(angles) + Sh::kAngles / 16 + threadIdx.x;  // [pass][lo, hi][thread]
+  auto fetch = [&](int item) {
+    const int w = item >= hkv, h = item - w * hkv;
+    const T* p = static_cast<const T*>(a.x[1 + w]) + (int64_t)(row0 + run0) * a.x_row[1 + w] + (int64_t)h * a.x_head[1 + w];
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k, p += kRun * a.x_row[1 + w]) {
+      if (k * kRun + run0 >= n) break;
+      copy_async(ahead + 2 * k * kThreads, p + at.lo);
+      copy_async(ahead + (2 * k + 1) * kThreads, p + at.hi);
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  if (Sh::kAhead && y < items) fetch(y);
   if (at.turned && y < hkv) {
 #pragma unroll 1
     for (int k = 0; k < kPasses; ++k) {
@@ -565,9 +585,18 @@ __device__ void pages_part(const PagesArgs& p) {
     const int w = item >= hkv, h = item - w * hkv;
     uint8_t* const to = static_cast<uint8_t*>(a.out[1 + w]) + (int64_t)block * a.o_block[1 + w] + (int64_t)h * a.o_head[1 + w];
     Pieces<T, CH, VEC> in[kPasses];
+    if constexpr (Sh::kAhead) asm volatile("cp.async.wait_group 0;\n" ::: "memory");
 #pragma unroll
-    for (int k = 0; k < kPasses; ++k)
-      if (k * kRun + run0 < n) load(w, h, k * kRun + run0, in[k]);
+    for (int k = 0; k < kPasses; ++k) {
+      if (k * kRun + run0 >= n) continue;
+      if constexpr (Sh::kAhead) {
+        const uint4 l = ahead[2 * k * kThreads], u = ahead[(2 * k + 1) * kThreads];
+        in[k].lo[0] = l.x, in[k].lo[1] = l.y, in[k].lo[2] = l.z, in[k].lo[3] = l.w;
+        in[k].hi[0] = u.x, in[k].hi[1] = u.y, in[k].hi[2] = u.z, in[k].hi[3] = u.w;
+      } else {
+        load(w, h, k * kRun + run0, in[k]);
+      }
+    }
     auto values = [&](int k, float (&x)[2 * CH]) {
       in[k].floats(x);
       if (w == 0 && at.turned) {
@@ -581,7 +610,7 @@ __device__ void pages_part(const PagesArgs& p) {
         t.apply(a.rot, x);
       }
     };
-    auto top_of = [&](auto largest_of) {  // over the CTA
+    auto top_of = [&](auto largest_of, bool first) {  // over the CTA
       float top = 0.f;
 #pragma unroll
       for (int k = 0; k < kPasses; ++k) {
@@ -592,6 +621,7 @@ __device__ void pages_part(const PagesArgs& p) {
         }
       }
       top = warp_max(top);
+      if (Sh::kAhead && first && item + p.y < items) fetch(item + p.y);  // behind the last use of what it replaces
       if (lane == 0) tops[buf][warp] = top;
       __syncthreads();
 #pragma unroll
@@ -600,8 +630,8 @@ __device__ void pages_part(const PagesArgs& p) {
       return top;
     };
     const float held = at0 ? held_scale(*scale_at(w, h)) : 0.f;
-    float top = top_of([](const float (&x)[2 * CH], float t) { return largest_any<2 * CH>(x, t); });
-    if (top == INFINITY) top = top_of([](const float (&x)[2 * CH], float t) { return largest<2 * CH>(x, t); });
+    float top = top_of([](const float (&x)[2 * CH], float t) { return largest_any<2 * CH>(x, t); }, true);
+    if (top == INFINITY) top = top_of([](const float (&x)[2 * CH], float t) { return largest<2 * CH>(x, t); }, false);
     const float scale = fmaxf(held, scale_of(top)), by = 1.f / scale;
     if (at0 && scale > held) rescale<D>(to, a.o_row[1 + w], at0, held / scale, threadIdx.x, kThreads);
 #pragma unroll
@@ -618,7 +648,7 @@ __device__ void pages_part(const PagesArgs& p) {
 }
 
 template <typename T, int D, int CH, bool VEC>
-__global__ void __launch_bounds__(PagesShape<D, CH>::kThreads, D == 256 ? 1 : 2) k_extend_pages(const __grid_constant__ PagesArgs p) {
+__global__ void __launch_bounds__(PagesShape<D, CH, sizeof(T)>::kThreads, D == 256 ? 1 : 2) k_extend_pages(const __grid_constant__ PagesArgs p) {
   pdl_wait();
   const int queries = p.pages * p.y;
   if ((int)blockIdx.x < queries) pages_part<T, D, CH, VEC>(p);
@@ -627,7 +657,7 @@ __global__ void __launch_bounds__(PagesShape<D, CH>::kThreads, D == 256 ? 1 : 2)
 
 template <typename T, int D, int CH, bool VEC>
 cudaError_t launch_pages_as(const PagesArgs& p, unsigned grid, cudaStream_t s) {
-  using Sh = PagesShape<D, CH>;
+  using Sh = PagesShape<D, CH, sizeof(T)>;
   static std::atomic<uint64_t> known{0};  // devices whose kernel may use kSmem
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
