@@ -563,7 +563,7 @@ typedef struct tq_new_rows {
  *     scale that the block has, if it holds earlier tokens of the request (its first new token is not its first); then the
  *     numbers of those are brought to the new scale. Values are rounded to nearest even; one past 448 scales becomes
  *     that, NaN stays NaN. A block's scale is that of the tokens in it, so two requests must not extend one block.
- *     Base and strides of the pool: multiples of 16. One launch.
+ *     Base and strides of the pool: multiples of 16. One launch, or two where there are many queries.
  *   - Not served, with a status bit: ids outside [0, max_seqs) (TQ_DEV_ERR_SEQ_ID); starts that fall or pass n_rows, a
  *     total below the number of new rows or past max_pages pages (TQ_DEV_ERR_LENGTH); pages without a block in the
  *     pool (TQ_DEV_ERR_BLOCK: the page's tokens alone).

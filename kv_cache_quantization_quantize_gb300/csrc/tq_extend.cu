@@ -131,13 +131,16 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi, __half) {
   return r;
 }
 
-// CH elements at each of two places, as words. VEC: 16-byte aligned.
+// CH elements at each of two places, as words. VEC: aligned to their size, up to 16 bytes.
 template <typename T, int CH, bool VEC>
 struct Pieces {
   static constexpr int kWords = CH * (int)sizeof(T) / 4;
   uint32_t lo[kWords], hi[kWords];
   __device__ __forceinline__ static void load_at(const T* p, uint32_t (&w)[kWords]) {
-    if constexpr (VEC) {
+    if constexpr (VEC && kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4) {
         const uint4 v = *reinterpret_cast<const uint4*>(p + i * (4 / sizeof(T)));
@@ -153,7 +156,9 @@ struct Pieces {
     }
   }
   __device__ __forceinline__ static void store_at(T* p, const uint32_t (&w)[kWords]) {
-    if constexpr (VEC) {
+    if constexpr (VEC && kWords == 2) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else if constexpr (VEC) {
 #pragma unroll
       for (int i = 0; i < kWords; i += 4)
         *reinterpret_cast<uint4*>(p + i * (4 / sizeof(T))) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
@@ -254,7 +259,7 @@ struct RowsArgs {
 };
 
 constexpr int kRowsThreads = 256;
-constexpr int kMostPer = 8;
+constexpr int kMostPer = 32;
 
 template <typename T, int CH, bool VEC>
 __device__ void rows_part(const RowsArgs& a, int cta) {
@@ -353,8 +358,11 @@ __global__ void __launch_bounds__(kRowsThreads, 3) k_rotate_rows(const __grid_co
 
 int rows_ctas(RowsArgs& a, int ch, int sms) {
   const int groups = kRowsThreads / (a.d / (2 * ch));
-  a.per = 1;  // up to 8 tokens of a CTA, where there are enough for 8 CTAs on each SM
-  while (a.per < kMostPer && 2 * a.per <= groups && a.n_rows / (2 * a.per) >= 8 * sms) a.per *= 2;
+  // Up to 8 tokens of a CTA, where there are enough for a CTA on each SM: a thread makes its angles for more heads (2048 tokens of
+  // 32 heads of 128: 15.4 us with 8 CTAs on each SM, 9.2 so). More where a token has fewer heads than threads.
+  a.per = 1;
+  while (a.per < kMostPer && 2 * a.per <= groups && a.n_rows / (2 * a.per) >= sms && (a.per < 8 || groups / a.per > a.all))
+    a.per *= 2;
   return (a.n_rows + a.per - 1) / a.per;
 }
 
@@ -689,18 +697,31 @@ cudaError_t launch_pages(PagesArgs& p, bool vec, int sms, cudaStream_t s) {
   return vec ? launch_pages_d<T, 8, true>(p, sms, s) : launch_pages_d<T, 4, false>(p, sms, s);
 }
 
-template <typename T>
-cudaError_t launch_rows(RowsArgs& a, bool vec, int sms, cudaStream_t s) {
-  const int ctas = rows_ctas(a, vec ? 8 : 4, sms);
-  return vec ? launch_pdl(k_rotate_rows<T, 8, true>, dim3(ctas), dim3(kRowsThreads), 0, s, a)
-             : launch_pdl(k_rotate_rows<T, 4, false>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
+// Vectors that addresses, strides and the channels' cut allow: 8 pairs of a thread in 16 bytes (2 of them in fp32), 4 pairs in
+// vectors of half that, or 4 pairs one by one.
+enum Width { kOneByOne, kFour, kEight };
+constexpr int64_t kManyQueries = 8 << 20;  // elements
+
+Width width_of(const Rotation& r, int d) { return r.pairs % 8 == 0 && d % 16 == 0 ? kEight : kFour; }
+Width width_of(Width w, const void* p, int64_t row, int64_t head, int size) {
+  while (w != kOneByOne) {
+    const int bytes = w == kEight ? 16 : 4 * size;
+    if ((uintptr_t)p % bytes == 0 && row * size % bytes == 0 && head * size % bytes == 0) break;
+    w = (Width)(w - 1);
+  }
+  return w;
 }
 
-// 16-byte vectors of 8 pairs fit: addresses, strides and the channels' cut.
-bool vectors(const void* p, int64_t row, int64_t head, int size) {
-  return (uintptr_t)p % 16 == 0 && row * size % 16 == 0 && head * size % 16 == 0;
+template <typename T>
+cudaError_t launch_rows(RowsArgs& a, Width w, int sms, cudaStream_t s) {
+  // 4 pairs also where a thread's angles serve few heads (65536 tokens of 2 heads of 256: 43 us, with 8 pairs 63; 16384 of 32
+  // heads of 128 53.8 and 49.4), and in fp32, whose vectors are 16 bytes all the same (rows into bf16 50.7 and 53.3)
+  if (w == kEight && (sizeof(T) == 4 || a.all <= 4)) w = kFour;
+  const int ctas = rows_ctas(a, w == kEight ? 8 : 4, sms);
+  if (w == kEight) return launch_pdl(k_rotate_rows<T, 8, true>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
+  if (w == kFour) return launch_pdl(k_rotate_rows<T, 4, true>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
+  return launch_pdl(k_rotate_rows<T, 4, false>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
 }
-bool vectors(const Rotation& r, int d) { return r.pairs % 8 == 0 && d % 16 == 0; }
 
 }  // namespace
 
@@ -719,7 +740,7 @@ cudaError_t launch_rotate(const Rotation& r, const void* x, void* out, int dt, c
   a.d = d;
   a.n_rows = n_tokens;
   const int size = dt == TQ_F32 ? 4 : 2;
-  const bool vec = vectors(r, d) && vectors(x, xs[0], xs[1], size) && vectors(out, os[0], os[1], size);
+  const Width vec = width_of(width_of(width_of(r, d), x, xs[0], xs[1], size), out, os[0], os[1], size);
   if (dt == TQ_BF16) return launch_rows<__nv_bfloat16>(a, vec, sms, s);
   if (dt == TQ_F16) return launch_rows<__half>(a, vec, sms, s);
   return launch_rows<float>(a, vec, sms, s);
@@ -743,7 +764,7 @@ cudaError_t launch_paged_extend(const tq_kv& pool, const tq_scales* scales, cons
   void* out[3] = {n.q_out, pool.k, pool.v};
   const int64_t* xs[3] = {n.q_strides, n.k_strides, n.v_strides};
   const int64_t* os[3] = {n.q_out_strides, pool.k_strides, pool.v_strides};
-  bool vec = vectors(r, a.d);
+  Width vec = width_of(r, a.d);
   for (int w = 0; w < 3; ++w) {
     a.heads[w] = w == 0 ? (n.q ? n.n_q_heads : 0) : pool.n_kv_heads;
     if (!a.heads[w]) continue;
@@ -754,9 +775,9 @@ cudaError_t launch_paged_extend(const tq_kv& pool, const tq_scales* scales, cons
     if (w > 0) a.o_block[w] = os[w][0];
     a.o_row[w] = os[w][w > 0];
     a.o_head[w] = os[w][1 + (w > 0)];
-    vec = vec && vectors(x[w], a.x_row[w], a.x_head[w], size);
+    vec = width_of(vec, x[w], a.x_row[w], a.x_head[w], size);
     // pages of 8 bits have their alignment checked
-    if (w == 0 || !scales) vec = vec && vectors(out[w], a.o_row[w], a.o_head[w], w == 0 ? size : 2) && a.o_block[w] % 8 == 0;
+    if (w == 0 || !scales) vec = width_of(width_of(vec, out[w], a.o_row[w], a.o_head[w], w == 0 ? size : 2), nullptr, a.o_block[w], 0, 2);
   }
   a.all = a.heads[0] + (scales ? 0 : a.heads[1] + a.heads[2]);
   if (!scales) {
@@ -765,15 +786,28 @@ cudaError_t launch_paged_extend(const tq_kv& pool, const tq_scales* scales, cons
     return launch_rows<float>(a, vec, sms, s);
   }
   p.scales = *scales;
+  // Many queries take a launch of their own, whose CTAs leave each other more room (37000 tokens of 4 heads and 16 query heads of
+  // 64: 72.6 us in one launch, 65.1 in two; 8 requests of 128 tokens, 8 and 32 heads of 128, 13.1 and 16.6).
+  if (a.heads[0] && (int64_t)n.n_rows * a.heads[0] * a.d >= kManyQueries) {
+    RowsArgs q = a;
+    const Width w = width_of(width_of(width_of(r, a.d), x[0], a.x_row[0], a.x_head[0], size), out[0], a.o_row[0], a.o_head[0], size);
+    const cudaError_t e = n.dtype == TQ_BF16  ? launch_rows<__nv_bfloat16>(q, w, sms, s)
+                          : n.dtype == TQ_F16 ? launch_rows<__half>(q, w, sms, s)
+                                              : launch_rows<float>(q, w, sms, s);
+    if (e != cudaSuccess) return e;
+    a.heads[0] = a.all = 0;
+  }
   p.pages = n.n_rows / kPage + 2 * m.batch;
   const int items = 2 * pool.n_kv_heads, warps = a.d == 256 ? 16 : 8;
-  // items per CTA: all warps busy in short runs, and enough CTAs for the SMs to take turns in long ones
+  // Items per CTA: all warps busy in short runs; in long ones as many as leave a CTA or two to each SM, for the angles are made once
+  // for all of a CTA's (37000 tokens of 4 heads of 256: 79 us with 8 CTAs to each SM, 49 with one).
   const int likely = std::max(1, n.n_rows / kPage + m.batch);
   const int most = n.n_rows / std::max(1, m.batch) > kShort ? items : (items + warps - 1) / warps;
-  p.y = std::min(most, std::max(1, (8 * sms + likely - 1) / likely));
-  if (n.dtype == TQ_BF16) return launch_pages<__nv_bfloat16>(p, vec, sms, s);
-  if (n.dtype == TQ_F16) return launch_pages<__half>(p, vec, sms, s);
-  return launch_pages<float>(p, vec, sms, s);
+  const int want = a.d == 256 ? sms : 2 * sms;
+  p.y = std::min(most, std::max(1, (want + likely - 1) / likely));
+  if (n.dtype == TQ_BF16) return launch_pages<__nv_bfloat16>(p, vec == kEight, sms, s);
+  if (n.dtype == TQ_F16) return launch_pages<__half>(p, vec == kEight, sms, s);
+  return launch_pages<float>(p, vec == kEight, sms, s);
 }
 
 }  // namespace tq

@@ -411,6 +411,39 @@ def test_extend_of_many_requests():
                 assert torch.equal(got, x.to(dtype))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,hq,hkv", [(128, 8, 4), (64, 20, 3), (256, 4, 2)])
+def test_extend_of_long_prompts(dtype, d, hq, hkv):
+    """Prompts whose queries take a launch of their own: what one call writes is what rotation, a call without queries and the
+    token's round trip say."""
+    nq = [(9 << 20) // (hq * d) - 200, 150, 1]
+    kv = [nq[0], 400, 129]
+    gen = torch.Generator().manual_seed(d)
+    rows = sum(nq) + 3
+    q, k, v = (normal(gen, (rows, h, d), dtype) for h in (hq, hkv, hkv))
+    table, slot, blocks = place_requests(nq, kv, 1)
+    args = (table, i32(slot), i32(starts_of(nq)), i32(kv))
+    r, at = paged.Rotary(d, base=500000.0), torch.cat([torch.arange(m - n, m) for n, m in zip(nq, kv)]).to(torch.int32).to(DEV)
+    results = []
+    for queries in (q, None):
+        pools = [torch.zeros(blocks, 128, hkv, d, dtype=torch.uint8, device=DEV).view(E4M3) for _ in range(2)]
+        scales = [torch.ones(blocks, hkv, device=DEV) for _ in range(2)]
+        out = None if queries is None else torch.full_like(q, 5.0)
+        paged.extend(k, v, *pools, *args, rotary=r, q=queries, q_out=out, k_scale=scales[0], v_scale=scales[1])
+        if out is not None:
+            assert torch.equal(out[:sum(nq)], paged.rotate(q[:sum(nq)], at, r)) and bool((out[sum(nq):] == 5.0).all())
+        results.append(pools + scales)
+    assert all(same(a, b) for a, b in zip(*results))
+    host = table.cpu()
+    slots = torch.tensor([int(host[slot[b], p // 128]) * 128 + p % 128 for b, (n, m) in enumerate(zip(nq, kv)) for p in range(m - n, m)], device=DEV).long()
+    want, size = ref.rotate(k[:sum(nq)], at, r.steps, r.times, False)
+    error = ref.rotation_error(size, at, r.steps)
+    for x, pool, scale, e in ((want, results[0][0], results[0][2], error), (v[:sum(nq)].double(), results[0][1], results[0][3], 0.0 * error)):
+        s = scale.double()[slots // 128][..., None]
+        got = values8(pool, scale).view(-1, hkv, d)[slots]
+        assert bool(((got - x).abs() <= s * ref.half_step8((x.abs() + e) / s) + e).all())
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
 def test_extend_refusals(dtype):
     k = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=DEV)
