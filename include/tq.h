@@ -521,7 +521,8 @@ typedef struct tq_rotary {
  * type dt (TQ_BF16, TQ_F16 or TQ_F32) at strides {row, head} in elements; row t has position d_positions[t]. The
  * arithmetic is fp32, the result is rounded once. inverse = 1 takes the angles with the other sign, still times factor:
  * the transposed map, which is the gradient's. out may be x itself (with its strides); it may not overlap it otherwise.
- * Any alignment is served; 16-byte aligned rows with rotary_dim and head_dim multiples of 16 are faster. One launch. */
+ * Any alignment is served; 16-byte aligned rows with rotary_dim and head_dim multiples of 16 are faster. At most 2^31 - 256
+ * rows and 65535 heads. One launch. */
 tq_status tq_rotate(const tq_rotary* rot, const void* x, void* out, tq_dtype dt, const int64_t* x_strides,
                     const int64_t* out_strides, const int32_t* d_positions, int n_tokens, int n_heads, int head_dim,
                     int inverse, tq_stream_t stream);
@@ -567,7 +568,7 @@ typedef struct tq_new_rows {
  *   - Not served, with a status bit: ids outside [0, max_seqs) (TQ_DEV_ERR_SEQ_ID); starts that fall or pass n_rows, a
  *     total below the number of new rows or past max_pages pages (TQ_DEV_ERR_LENGTH); pages without a block in the
  *     pool (TQ_DEV_ERR_BLOCK: the page's tokens alone).
- * batch in [0, 65535]. The host reads no array; calls can be captured. */
+ * batch in [0, 65535], at most 2^31 - 256 rows. The host reads no array; calls can be captured. */
 tq_status tq_paged_extend(const tq_kv* pool, const tq_scales* scales, const tq_new_rows* rows, const tq_rotary* rot,
                           const int32_t* d_table, int max_seqs, int max_pages, int64_t table_stride,
                           const int32_t* d_seq_ids, const int32_t* d_starts, const int32_t* d_totals, int batch,

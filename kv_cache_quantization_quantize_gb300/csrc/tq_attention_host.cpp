@@ -180,6 +180,8 @@ tq_status check_rotary(const tq_rotary* rot, int head_dim, tq::Rotation* r) {
   return TQ_OK;
 }
 
+constexpr int kMostRows = 0x7fffff00;  // of rotations and rotated appends: the last CTA counts some rows past them in 32 bits
+
 bool known_type(int dt) { return dt == TQ_BF16 || dt == TQ_F16 || dt == TQ_F32; }
 
 tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
@@ -391,6 +393,8 @@ tq_status tq_rotate(const tq_rotary* rot, const void* x, void* out, tq_dtype dt,
   if (!known_type(dt)) return fail(TQ_ERR_INVALID_ARG, "dtype %d", (int)dt);
   if (inverse != 0 && inverse != 1) return fail(TQ_ERR_INVALID_ARG, "inverse %d: 0 or 1", inverse);
   if (n_tokens < 0 || n_heads < 0) return fail(TQ_ERR_INVALID_ARG, "n_tokens %d, n_heads %d: none below 0", n_tokens, n_heads);
+  if (n_tokens > kMostRows || n_heads > 65535)
+    return fail(TQ_ERR_UNSUPPORTED, "n_tokens %d, n_heads %d: at most %d and 65535", n_tokens, n_heads, kMostRows);
   if (!n_tokens || !n_heads) return tq::set_error(TQ_OK, "");
   if (!x || !out || !x_strides || !out_strides || !d_positions) return fail(TQ_ERR_INVALID_ARG, "NULL array");
   const size_t esz = dt == TQ_F32 ? 4 : 2;
@@ -421,6 +425,7 @@ tq_status tq_paged_extend(const tq_kv* pool, const tq_scales* scales, const tq_n
   if (rows->n_rows < 0 || batch < 0 || rows->n_q_heads < 0 || rows->n_q_heads > 65535)
     return fail(TQ_ERR_INVALID_ARG, "n_rows %d, batch %d, n_q_heads %d (at most 65535): none below 0", rows->n_rows, batch, rows->n_q_heads);
   if (batch > 65535) return fail(TQ_ERR_UNSUPPORTED, "batch %d: at most 65535", batch);
+  if (rows->n_rows > kMostRows) return fail(TQ_ERR_UNSUPPORTED, "n_rows %d: at most %d", rows->n_rows, kMostRows);
   if (rows->q && !rot) return fail(TQ_ERR_INVALID_ARG, "q without rot: nothing to do");
   if (!batch || !rows->n_rows) return tq::set_error(TQ_OK, "");
   const bool queries = rows->q && rows->n_q_heads;

@@ -280,7 +280,7 @@ __device__ void rows_part(const RowsArgs& a, int cta) {
         uint32_t err = 0;
         const StepRequest r = step_request(a.map, b, err);
         if (r.n > 0 && row >= r.row0 && row < r.row0 + r.n) {
-          const int at = r.first + row - r.row0;
+          const int at = r.first + (row - r.row0);
           t.position = a.positions ? a.positions[row] : at;
           t.place = at % kPage;
           t.block = -1;

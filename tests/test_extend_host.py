@@ -128,6 +128,14 @@ def test_extend_refuses(over, status):
     assert extend(**{"scale": scales(), **over}) == status
 
 
+def test_rows_and_heads_that_32_bits_would_not_count_are_refused():
+    st = paged._STRIDES.pack(0, 0)
+    for n, h in [(2 ** 31 - 1, 1), (2 ** 31 - 255, 1), (1, 65536), (1, 2 ** 31 - 1)]:
+        assert _abi.load().tq_rotate(rot(), P, P, 0, st, st, P, n, h, 64, 0, None) == NOT
+    for n in (2 ** 31 - 1, 2 ** 31 - 255):
+        assert extend(scale=scales(), new=rows(n=n)) == extend(pool=kv(), new=rows(n=n)) == NOT
+
+
 def test_extend_of_nothing():
     assert extend(scale=scales(), batch=0) == extend(scale=scales(), new=rows(n=0)) == _abi.TQ_OK
     assert extend(pool=kv(), new=rows(n=0)) == _abi.TQ_OK
