@@ -24,13 +24,17 @@ struct Tc8Shape {
   static constexpr int kStages = D == 64 ? 6 : D == 128 ? 3 : 4;
   static constexpr int kRawStages = kStages;
   // One tile's softmax is shared by two warpgroups that take its units in turn, each with a buffer of S and P of its own:
-  // with one warp per scheduler it was the bound (2048 queries after 14336 tokens: 413 us, with two 376).
+  // with one warp per scheduler it would be the bound, as it is of the exact kernel (10 % there).
   static constexpr bool kPair = kNT == 1;
   static constexpr int kThreads = 512;
-  // Start and end of a tile, in 64ths of a unit: 3 units of 128 tokens, 5 of 64 (4096 x 4096 causal at D = 256: 138 us
-  // with 3 units, 123 with 5, 126 with 7). No CTA gets less than a tile of one unit costs: short work takes fewer CTAs.
-  static constexpr int kTileCost = D == 256 ? 320 : 192;
-  static constexpr int kMinPart = kTileCost + 64;
+  // Start and end of a tile, in 64ths of a unit: 7 units of 128 tokens, 10 of 64 (4096 x 4096 causal, 16 query heads on 4 at
+  // D = 256 218 us with 5 units, 191 with 7, 178 with 10, 179 with 13; 16 requests of up to 700 on up to 4000 tokens, 32 heads on
+  // 8 of 128, 244 with 3, 231 with 5, 212 with 7, 207 with 9, but 4096 x 4096 161 with 7 and 164 with 9).
+  static constexpr int kTileCost = D == 256 ? 640 : 448;
+  // No CTA gets less than this, or short work would be in more parts than it is worth joining (16 queries of a request of 8000
+  // tokens at D = 256: 46.2 us with 128, 39.9 so; at 64 38.2 and 24.9) or leave CTAs idle (4 requests of 16 to 64 on up to 1000 tokens
+  // at D = 128: 30.7 us with 384, 22.4 so).
+  static constexpr int kMinPart = D == 256 ? 384 : D == 128 ? 128 : 320;
   static constexpr int kQ = kPair ? 0 : 128 * D * 2;   // bytes of a tile's queries
   static constexpr int kOutRow = D == 64 ? 128 : 64;  // bytes of each row of results that pass shared memory at a time
   static constexpr int kStage = 32 * kOutRow;          // of a softmax warp, for its results on their way out
@@ -47,8 +51,8 @@ struct Tc8Shape {
   static constexpr uint32_t kBuf = 64;  // columns from one buffer of S and P to the next
   static constexpr uint32_t kO = D == 64 ? 384 : 256;
   // At D = 128 the tiles' softmaxes take turns: left alone they fall into step, share the special function units and
-  // then leave the tensor pipe idle together (2900 cycles per unit against 2500; the SMs differed by 30 %). At D = 64
-  // the softmax is the bound and turns only add waits (2290 cycles per unit without them, 2900 with).
+  // then leave the tensor pipe idle together (2048 queries after 14336 tokens, 32 heads on 8: 388 us, without turns 461).
+  // At D = 64 the softmax is the bound and turns only add waits (the same with 16 heads on 4: 148 us, with turns 182).
   static constexpr bool kTurns = D == 128;
 };
 
@@ -699,14 +703,15 @@ cudaError_t launch_tc8_as(const AttnArgs& a, const AttnMaps& m, const AttnPlan& 
   return launch_join<D, 128 * Sh::kNT, BF16>(a, p.ctas, p.max_rows, s);
 }
 
+template <int D>
+AttnShape tc8_shape(int sms) {
+  using Sh = Tc8Shape<D>;
+  return {128 * Sh::kNT, Sh::kBN, sms, cta_bytes(128 * Sh::kNT, D), Sh::kTileCost, Sh::kMinPart};
+}
+
 }  // namespace
 
-AttnShape attn8_tc_shape(int d, int sms) {
-  using Wide = Tc8Shape<256>;
-  using Other = Tc8Shape<128>;
-  if (d == 256) return {128 * Wide::kNT, Wide::kBN, sms, cta_bytes(128 * Wide::kNT, d), Wide::kTileCost, Wide::kMinPart};
-  return {128 * Other::kNT, Other::kBN, sms, cta_bytes(128 * Other::kNT, d), Other::kTileCost, Other::kMinPart};
-}
+AttnShape attn8_tc_shape(int d, int sms) { return d == 64 ? tc8_shape<64>(sms) : d == 128 ? tc8_shape<128>(sms) : tc8_shape<256>(sms); }
 
 cudaError_t launch_attn8_tc(const AttnArgs& a, const AttnMaps& m, const AttnPlan& p, int d, int dtype, cudaStream_t s) {
   if (dtype == TQ_BF16)
