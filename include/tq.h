@@ -588,7 +588,8 @@ typedef struct tq_queries {
   int32_t n_q_heads;
   int32_t batch;       /* <= 65535 */
   int32_t max_q;       /* no request has more rows (0: n_rows); one that has gets no output, TQ_DEV_ERR_SPLITS */
-  int32_t max_kv;      /* no request has more tokens to attend to (0: unknown); bounds the CTAs of short calls */
+  int32_t max_kv;      /* no request has more tokens to attend to (0: unknown); bounds the CTAs of short calls; over
+                        * 8 bits little work also takes the kernel for few rows */
   float softmax_scale; /* <= 0: 1 / sqrt(head_dim) */
 } tq_queries;
 

@@ -211,11 +211,24 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
 // Requests of up to 32 rows (queries x query heads per KV head) take the rows kernel, others the tensor cores. Measured
 // with 4 query heads per KV head, head_dim 128: 32 rows, rows kernel against tensor cores: 19.8 against 26.9 us over
 // 8192 tokens, 56 against 61 us over 65536; 64 rows, which would be two tiles: 22.8 against 27.0 us over 8192 tokens, but
-// 83 against 63 us over 65536, and 28 against 22 us for 16 requests of 512.
+// 83 against 63 us over 65536, and 28 against 22 us for 16 requests of 512. Over 8 bits 64 against 76 us for 16 requests of 8
+// drafts over 4096 to 8192; there the rows kernel, in tiles of 32 rows, is also the faster one for little work, which its many
+// small parts spread better: where the tensor cores' tiles would be few (kRowsEach rows for each SM; 32 heads on 8 of 128, 16 queries
+// over 1000 tokens 12.5 against 18.8 us, over 16000 32.6 against 38.9; 16 heads on 4 of 256 12.3 against 26.9 and 30.2 against
+// 43.9; but 8 requests of 128 34.8 against 19.5) and each CTA gets kUnitsEach units at most (120 queries over 4000 tokens, 13 units:
+// 46.8 against 40.3).
+constexpr int kRowsEach = 32, kUnitsEach = 8;
 tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   tq::AttnPlan p;
   const int64_t rows = (int64_t)(q.max_q > 0 ? std::min(q.max_q, q.n_rows) : q.n_rows) * (q.n_q_heads / kv.n_kv_heads);
-  const bool tc = rows > 32, e4m3 = kv.dtype == TQ_E4M3;
+  const bool e4m3 = kv.dtype == TQ_E4M3;
+  bool tc = rows > 32;
+  if (tc && e4m3 && q.max_kv > 0) {
+    auto tiles = [&](int of) { return (double)q.batch * kv.n_kv_heads * ((rows + of - 1) / of); };
+    const tq::AttnShape few = tq::attn8_rows_shape(kv.head_dim, rows, sms);
+    const int wide = tq::attn8_tc_shape(kv.head_dim, sms).tile_rows;
+    tc = tiles(wide) * wide > kRowsEach * (double)sms || tiles(few.tile_rows) * ((q.max_kv + few.unit - 1) / few.unit) > kUnitsEach * (double)few.ctas;
+  }
   static_cast<tq::AttnShape&>(p) = tc ? (e4m3 ? tq::attn8_tc_shape(kv.head_dim, sms) : tq::attn_tc_shape(kv.head_dim, sms))
                                       : (e4m3 ? tq::attn8_rows_shape : tq::attn_rows_shape)(kv.head_dim, rows, sms);
   p.tc = tc;

@@ -450,7 +450,7 @@ def attention(q, k_pool, v_pool, table, seq_ids, q_starts, kv_lens, causal=True,
     q: [rows, n_q_heads, head_dim] of the pools' type (bf16 or f16 where they are e4m3), request b's rows at [q_starts[b], q_starts[b + 1]); kv_lens[b]: its
     tokens with the new ones, in the pages of table row seq_ids[b] (None: row b). max_q: no request has more rows (0:
     unknown; few rows take a kernel of their own); max_kv: no request has more tokens (0: unknown; short calls launch fewer
-    CTAs). Returns out, of q's shape; rows of no request stay as they are. What the cache holds behind a request's
+    CTAs, and over e4m3 little work takes that kernel too). Returns out, of q's shape; rows of no request stay as they are. What the cache holds behind a request's
     tokens does not matter; a token that any of its queries sees has to be finite."""
     scaled = k_scale is not None or v_scale is not None
     index, kv, d, heads, dtype = _pools(k_pool, v_pool, scaled)

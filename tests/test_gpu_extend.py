@@ -530,6 +530,26 @@ def test_attention_over_8_bits(dtype, d, heads, case):
 
 
 @pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads,nq,kv", [((8, 2), [9], [9]), ((6, 2), [11, 0, 40], [700, 0, 131]), ((5, 1), [100, 1], [257, 2000]), ((32, 1), [2, 3], [1, 3]),
+                                         ((1, 1), [200, 33], [300, 33]), ((4, 4), [65], [1500]), ((8, 1), [128], [128]), ((2, 1), [17, 64], [6000, 64])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_short_work_with_and_without_hints(dtype, d, heads, nq, kv, causal):
+    """The most tokens of a request, where it is known, choose the kernel: either one has to be right, in either's workspace."""
+    hq, hkv = heads
+    q, k, ks, v, vs, table, slot = attend_inputs(nq, kv, hq, hkv, d, dtype, causal, d + hq + len(nq), tail=2)
+    room = torch.empty(paged.attention_workspace_bytes(q, k, max_q=max(nq), batch=len(nq)), dtype=torch.uint8, device=DEV)
+    least = paged.attention_workspace_bytes(q, k, max_q=max(nq), max_kv=max(kv), batch=len(nq))
+    assert least <= room.numel()
+    for hints, ws in [({}, room), ({"max_kv": max(kv)}, room), ({"max_kv": max(kv)}, room[:least]), ({"max_kv": 1 << 20}, room)]:
+        out, status = torch.full_like(q, 5.0), i32([0])
+        paged.attention(q, k, v, table, i32(slot), i32(starts_of(nq)), i32(kv), causal=causal, max_q=max(nq), out=out, workspace=ws, status=status,
+                        k_scale=ks, v_scale=vs, **hints)
+        assert status.item() == 0 and bool((out[sum(nq):] == 5.0).all())
+        check_attended(out, q, k, ks, v, vs, table, slot, nq, kv, causal)
+
+
+@pytest.mark.parametrize("dtype", HALVES)
 @pytest.mark.parametrize("d,nq,kv", [(128, [1], [20000]), (64, [2], [9000]), (256, [1], [5000]), (128, [70], [6000]), (256, [130], [3000]), (64, [300], [4000])])
 def test_attention_over_8_bits_of_split_sequences(dtype, d, nq, kv):
     q, k, ks, v, vs, table, slot = attend_inputs(nq, kv, 8, 2, d, dtype, False, 77)
