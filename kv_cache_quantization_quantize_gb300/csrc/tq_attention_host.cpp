@@ -227,7 +227,7 @@ tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
     auto tiles = [&](int of) { return (double)q.batch * kv.n_kv_heads * ((rows + of - 1) / of); };
     const tq::AttnShape few = tq::attn8_rows_shape(kv.head_dim, rows, sms);
     const int wide = tq::attn8_tc_shape(kv.head_dim, sms).tile_rows;
-    tc = tiles(wide) * wide > kRowsEach * (double)sms || tiles(few.tile_rows) * ((q.max_kv + few.unit - 1) / few.unit) > kUnitsEach * (double)few.ctas;
+    tc = tiles(wide) * wide > kRowsEach * (double)sms || tiles(few.tile_rows) * (((int64_t)q.max_kv + few.unit - 1) / few.unit) > kUnitsEach * (double)few.ctas;
   }
   static_cast<tq::AttnShape&>(p) = tc ? (e4m3 ? tq::attn8_tc_shape(kv.head_dim, sms) : tq::attn_tc_shape(kv.head_dim, sms))
                                       : (e4m3 ? tq::attn8_rows_shape : tq::attn_rows_shape)(kv.head_dim, rows, sms);

@@ -541,6 +541,7 @@ def test_short_work_with_and_without_hints(dtype, d, heads, nq, kv, causal):
     room = torch.empty(paged.attention_workspace_bytes(q, k, max_q=max(nq), batch=len(nq)), dtype=torch.uint8, device=DEV)
     least = paged.attention_workspace_bytes(q, k, max_q=max(nq), max_kv=max(kv), batch=len(nq))
     assert least <= room.numel()
+    assert paged.attention_workspace_bytes(q, k, max_q=max(nq), max_kv=2 ** 31 - 1, batch=len(nq)) == room.numel()  # as if it were unknown
     for hints, ws in [({}, room), ({"max_kv": max(kv)}, room), ({"max_kv": max(kv)}, room[:least]), ({"max_kv": 1 << 20}, room)]:
         out, status = torch.full_like(q, 5.0), i32([0])
         paged.attention(q, k, v, table, i32(slot), i32(starts_of(nq)), i32(kv), causal=causal, max_q=max(nq), out=out, workspace=ws, status=status,
