@@ -332,30 +332,31 @@ def extend(k, v, k_pool, v_pool, table, seq_ids, starts, totals, rotary=None, po
     if q is None and q_out is not None:
         raise ValueError("q_out goes with q")
     rot = None if rotary is None else rotary._pack(index)
-    if q is not None and (q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.dtype is not dtype or q.get_device() != index):
+    q_shape = None if q is None else q.shape
+    if q is not None and (len(q_shape) != 3 or q_shape[0] != n or q_shape[2] != d or q.dtype is not dtype or q.get_device() != index):
         raise ValueError(f"q: expected a {dtype} tensor [{n}, n_q_heads, {d}] on cuda:{index}")
     if stream is None and torch._C._cuda_getDevice() == index:
-        return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, torch._C._cuda_getCurrentRawStream(index))
+        return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_shape, q_out, args, torch._C._cuda_getCurrentRawStream(index))
     raw, on = _here(index, stream, (k, v, k_pool, v_pool, table, seq_ids, starts, totals, positions, q, q_out, k_scale, v_scale, status,
                                     None if rotary is None else rotary.turns))
     if on is not None:
         with on:
-            return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, raw)
-    return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, raw)
+            return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_shape, q_out, args, raw)
+    return _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_shape, q_out, args, raw)
 
 
-def _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_out, args, raw):
+def _extend(k, v, ks, vs, n, dtype, pool, scales, rot, places, q, q_shape, q_out, args, raw):
     if q is None:
         queries = (0, 0, 0, 0, 0, 0, 0)
     else:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype is not dtype or q_out.device != q.device:
+            q_out = torch.empty(q_shape, dtype=dtype, device=q.device)
+        elif q_out.shape != q_shape or q_out.dtype is not dtype or q_out.get_device() != q.get_device():
             raise ValueError("q_out: expected a tensor of q's shape, type and device")
         qs, os = q.stride(), q_out.stride()
         if qs[2] != 1 or os[2] != 1:
             raise ValueError("q, q_out: the channels of a head have to be contiguous")
-        queries = (q.data_ptr(), q_out.data_ptr(), qs[0], qs[1], os[0], os[1], q.shape[1])
+        queries = (q.data_ptr(), q_out.data_ptr(), qs[0], qs[1], os[0], os[1], q_shape[1])
     rows = _NEW_ROWS.pack(k.data_ptr(), v.data_ptr(), queries[0], queries[1], ks[0], ks[1], vs[0], vs[1], *queries[2:6], places, n, queries[6],
                           _DTYPES[dtype])
     table, seq_ids, starts, totals, batch, word = args
