@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
-          const float above[2] = {us.log_v - mv[t][0], us.log_v - mv[t][1]};
+          const float above[2] = {(us.log_v - mv[t][0]) + kLift, (us.log_v - mv[t][1]) + kLift};
           sum[t][0] = sum[t][1] = 0.f;
 #pragma unroll
           for (int n = 0; n < NS; ++n) {

@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           mlv = mvn;
         }
         const bool grew = more && m != -INFINITY;
-        const float mu = mn == -INFINITY ? 0.f : mn, above = us.log_v - mvn;
+        const float mu = mn == -INFINITY ? 0.f : mn, above = (us.log_v - mvn) + kLift;
         const bool far = fabsf(mu) > kFar;
         const bool special = __any_sync(0xffffffffu, grew || far);
         // O_t is whole before it is rescaled, and P_t has been used before it is written again

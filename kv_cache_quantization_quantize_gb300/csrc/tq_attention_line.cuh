@@ -392,6 +392,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // Rescale sums when a row's maximum grew by more than this (in powers of two): weights stay below 2^8, far inside
 // fp32 and f16, and the final division takes the factor out.
 constexpr float kLazy = 8.0f;
+// Weights that are rounded to f16 are 2^kLift times as large, sums and statistics with them: up to 2^15 where f16 ends at 65504.
+// f16 has nothing below 2^-25, so without it a weight of 2^-25 of the row's largest would be lost, which 2^15 tokens
+// behind a first one that takes nearly all of the weight have; so it is 2^-32.
+constexpr float kLift = 7.0f;
 
 }  // namespace
 }  // namespace tq

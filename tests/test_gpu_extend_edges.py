@@ -1,0 +1,70 @@
+"""GPU tests of rotary positions, rotated appends and the paged cache of 8 bits at the edges of what they take, against plain 64-bit references."""
+import math
+
+import pytest
+import torch
+
+from kv_cache_quantization_quantize_gb300 import paged
+from tests import extend_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+E4M3 = torch.float8_e4m3fn
+HALVES = [torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from kv_cache_quantization_quantize_gb300 import build
+    build.build()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def codes(x):
+    return x.to(E4M3).to(DEV)
+
+
+# ---- attention over 8 bits: weights far below a row's largest, scales at the ends of their range ----
+
+def attend_shared(q, k, v, ks, vs, batch, m, scale, word=None):
+    """q [n, hq, d] of each of `batch` requests, all on one sequence (so that few parts of it go to the join). Returns
+    [batch, n, hq, d]."""
+    n = q.shape[0]
+    table = torch.arange(k.shape[0], dtype=torch.int32, device=DEV)[None]
+    many = q[None].expand(batch, -1, -1, -1).reshape(batch * n, *q.shape[1:]).contiguous()
+    out = paged.attention(many, k, v, table, torch.zeros(batch, dtype=torch.int32, device=DEV), torch.arange(0, (batch + 1) * n, n, dtype=torch.int32, device=DEV),
+                          torch.full((batch,), m, dtype=torch.int32, device=DEV), causal=False, softmax_scale=scale, max_q=n, max_kv=m, status=word,
+                          **({} if ks is None else {"k_scale": ks, "v_scale": vs}))
+    return out.view(batch, *q.shape)
+
+
+def sink(m, d, hkv, below):
+    """Numbers of K and V of m tokens in pages: the first token's key scores `below` log2 above all others with a query of ones and the
+    returned softmax scale; its value is 0, the others' are positive."""
+    pages, gen = -(-m // 128), torch.Generator().manual_seed(m + d)
+    k, v = torch.zeros(pages * 128, hkv, d), torch.randint(1, 9, (pages * 128, hkv, d), generator=gen) / 4
+    k[0], v[0] = 1.0, 0.0
+    return k.view(pages, 128, hkv, d), v.view(pages, 128, hkv, d), below * math.log(2.0) / d
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 640), (6, 640), (40, 320)])
+def test_small_weights_beside_a_sink_are_kept_over_8_bits(dtype, d, n, batch):
+    """A first token that takes nearly all of the weight and has no value, before 32767 others: the result is the others' alone.
+
+    Weights are rounded to f16 as p = 2^(s - m + 7) with m at most the row's maximum: relative to 2^7 by 2^-11, or by half of f16's
+    least step, 2^-25 / 2^7, below 2^-14 / 2^7. So a result is off by 2^-11 of the sum of w |v| and 2^-32 of that of |v|, over that of w,
+    beside its own rounding; scores are 0 and `below` exactly, and fp32 sums of 2048 steps, of weights and of products, add 2^-13 each."""
+    m, below = 32768, 25.5
+    k, v, scale = sink(m, d, 1, below)
+    one = torch.ones(k.shape[0], 1, device=DEV)
+    out = attend_shared(torch.ones(n, 4, d, dtype=dtype, device=DEV), codes(k), codes(v), one, one, batch, m, scale)
+    w, total = 2.0 ** -below, 1.0 + (m - 1) * 2.0 ** -below
+    mass = v.double().sum((0, 1, 2)).to(DEV) / total  # of |v|
+    want = w * mass
+    bound = want * (torch.finfo(dtype).eps / 2 + 2.0 ** -11 + 2.0 ** -12) + 2.0 ** -32 * mass + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    assert bool(((out.double() - want).abs() <= bound).all())
