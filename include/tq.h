@@ -617,8 +617,9 @@ tq_status tq_paged_attention(const tq_queries* q, const tq_kv* kv, const int32_t
 /* tq_paged_attention8: the same over a pool of 8 bits (kv of type TQ_E4M3, with the scales that tq_paged_extend keeps) for queries
  * and outputs of type q_dtype, TQ_BF16 or TQ_F16. Numbers of e4m3 are exact in f16, in which the products run: queries in bf16 are
  * taken there by a power of two for each row and head. The scales of K multiply scores, those of V the weights' exponents and
- * the statistics, in fp32; weights are rounded to f16 after that, in steps of 2^-11 of themselves, or of 2^-31 of the row's
- * largest for those below 2^-21 of it. Scales outside
+ * the statistics, in fp32; weights are rounded to f16 after that, which takes up to 2^-11 of themselves, or 2^-32 of the row's
+ * largest from those below 2^-21 of it. Results in f16 past its largest number are infinite, but for those up to 2^-8 past it,
+ * where rounded weights may have taken them: they are that number. Scales outside
  * [2^-60, 2^60] count as the nearest of the two, NaN as 2^-60. Base and strides of the pool: multiples of 16 bytes.
  * Workspace: tq_attention_workspace_bytes(q, kv). */
 tq_status tq_paged_attention8(const tq_queries* q, tq_dtype q_dtype, const tq_kv* kv, const tq_scales* scales,

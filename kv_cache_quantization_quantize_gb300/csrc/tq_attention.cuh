@@ -166,14 +166,15 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// Two results in the cache's type. A result is an average of values, so a finite one past f16's largest number is there
-// by the rounding of weights alone (up to 2^-11 of it; the next number is already infinite): it is that number.
+// Two results in the queries' type. A result is an average of values, so over a cache of f16 a finite one past f16's largest
+// number is there by the rounding of weights alone (up to 2^-11 of it, and what the sums add; the next number is already
+// infinite): up to 2^-8 past it is that number. A cache of 8 bits can hold more, and results behind that are infinite.
 template <bool BF16>
 __device__ __forceinline__ uint32_t result2(float lo, float hi) {
   if constexpr (!BF16) {
-    constexpr float kMost = 65504.f;
-    if (fabsf(lo) > kMost && fabsf(lo) < INFINITY) lo = copysignf(kMost, lo);
-    if (fabsf(hi) > kMost && fabsf(hi) < INFINITY) hi = copysignf(kMost, hi);
+    constexpr float kMost = 65504.f, kNear = 65504.f * (1.f + 1.f / 256.f);
+    if (fabsf(lo) > kMost && fabsf(lo) <= kNear) lo = copysignf(kMost, lo);
+    if (fabsf(hi) > kMost && fabsf(hi) <= kNear) hi = copysignf(kMost, hi);
   }
   return pack2<BF16>(lo, hi);
 }

@@ -68,3 +68,23 @@ def test_small_weights_beside_a_sink_are_kept_over_8_bits(dtype, d, n, batch):
     want = w * mass
     bound = want * (torch.finfo(dtype).eps / 2 + 2.0 ** -11 + 2.0 ** -12) + 2.0 ** -32 * mass + (2.0 ** -25 if dtype == torch.float16 else 0.0)
     assert bool(((out.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 6, 40])
+@pytest.mark.parametrize("m", [70, 9000])
+def test_results_past_f16_are_infinite(d, n, m):
+    """All values of a request the same: the result is that, infinite where f16 has no number for it, and its largest number where
+    only rounded weights carry a result past it."""
+    pages, gen = -(-m // 128), torch.Generator().manual_seed(d + n)
+    k, q = codes(torch.randn((pages, 128, 2, d), generator=gen)), torch.randn((n, 4, d), generator=gen).half().to(DEV)
+    v, one = codes(torch.full((pages, 128, 2, d), 448.0)), torch.ones(pages, 2, device=DEV)
+    v.view(torch.uint8)[..., 1::2] = 0xFE  # -448
+    sign = torch.ones(d, device=DEV, dtype=torch.float64)
+    sign[1::2] = -1.0
+    args = (torch.arange(pages, dtype=torch.int32, device=DEV)[None], None, i32([0, n]), i32([m]))
+    for scale in (2.0 ** 8, 2.0 ** 60):  # 114688 and more
+        out = paged.attention(q, k, v, *args, causal=False, k_scale=one, v_scale=one * scale)
+        assert torch.equal(out.double(), (sign * math.inf).expand(n, 4, d))
+    out = paged.attention(q, k, v, *args, causal=False, k_scale=one, v_scale=one * (65504.0 / 448.0))
+    assert bool(out.isfinite().all()) and bool(((out.double() - sign * 65504.0).abs() <= 65504.0 * 2.0 ** -10).all())
