@@ -357,9 +357,10 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
           }
         // (apart: far scores have no room for the logarithm)
         need |= (top[t][0] - m[t][0]) + (us.log_v - mv[t][0]) > kLazy || (top[t][1] - m[t][1]) + (us.log_v - mv[t][1]) > kLazy;
+        need |= fmaxf(mv[t][0], mv[t][1]) - us.log_v > kApart;
       }
       float sum[MT][2];
-      for (;;) {  // twice where a maximum outgrew its range: the code is not doubled, since a cold path costs its fetches
+      for (;;) {  // twice where a maximum or a scale left its range: the code is not doubled, since a cold path costs its fetches
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
           left = true;
           break;
         }
-        // new maxima for all rows, from all warps
+        // new references for all rows, from all warps
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -406,11 +407,15 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
 #pragma unroll
             for (int i = 1; i < NW; ++i) mx = fmaxf(mx, sx[i][row]);
             alpha[x] = 1.f;
-            const float by = (m[t][x] - mx) + (mv[t][x] - us.log_v);
-            if (by < 0.f) {
+            const float by = (m[t][x] - mx) + (mv[t][x] - us.log_v), lower = fmaxf((mv[t][x] - us.log_v) - kApart, 0.f);
+            if (by < lower) {
               alpha[x] = exp2_fast(by);
               m[t][x] = mx;
               mv[t][x] = us.log_v;
+              l[t][x] *= alpha[x];
+            } else if (lower > 0.f) {
+              alpha[x] = exp2_fast(lower);
+              mv[t][x] -= lower;
               l[t][x] *= alpha[x];
             }
           }

@@ -505,8 +505,9 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           mv = m_other->y;
         }
         // the sum of both maxima's parts may outgrow theirs; far scores have no room for the logarithm, so it stays apart
-        const bool more = (mx - m) + (us.log_v - mv) > kLazy;  // also where m is -inf and mx is not
-        const float mn = more ? mx : m, mvn = more ? us.log_v : mv;
+        const float lower = fmaxf((mv - us.log_v) - kApart, 0.f);
+        const bool more = (mx - m) + (us.log_v - mv) > (lower > 0.f ? -lower : kLazy);  // also where m is -inf and mx is not
+        const float mn = more ? mx : m, mvn = more ? us.log_v : mv - lower;
         if constexpr (kPair) {
           *m_own = make_float2(mn, mvn);
           __syncwarp();
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           ml = mn;
           mlv = mvn;
         }
-        const bool grew = more && m != -INFINITY;
+        const bool grew = (more || lower > 0.f) && m != -INFINITY;  // or its scale was lowered
         const float mu = mn == -INFINITY ? 0.f : mn, above = (us.log_v - mvn) + kLift;
         const bool far = fabsf(mu) > kFar;
         const bool special = __any_sync(0xffffffffu, grew || far);

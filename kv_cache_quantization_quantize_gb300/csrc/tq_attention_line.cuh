@@ -396,6 +396,10 @@ constexpr float kLazy = 8.0f;
 // f16 has nothing below 2^-25, so without it a weight of 2^-25 of the row's largest would be lost, which 2^15 tokens
 // behind a first one that takes nearly all of the weight have; so it is 2^-32.
 constexpr float kLift = 7.0f;
+// Over 8 bits: the reference's scale is no more than 2^kApart above that of the unit at hand, or it is lowered, sums and statistic with it. Scales can be
+// 2^120 apart, and a weight below fp32's range (2^-126) would be lost to the statistic, which divides it by a scale that
+// small; and the statistic relative to a maximum's score alone, as the join takes it, could leave the range above.
+constexpr float kApart = 80.0f;
 
 }  // namespace
 }  // namespace tq

@@ -88,3 +88,35 @@ def test_results_past_f16_are_infinite(d, n, m):
         assert torch.equal(out.double(), (sign * math.inf).expand(n, 4, d))
     out = paged.attention(q, k, v, *args, causal=False, k_scale=one, v_scale=one * (65504.0 / 448.0))
     assert bool(out.isfinite().all()) and bool(((out.double() - sign * 65504.0).abs() <= 65504.0 * 2.0 ** -10).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 640), (6, 640), (40, 320), (1, 1), (40, 1)])
+def test_a_page_of_small_values_counts_beside_one_of_large_ones(d, n, batch):
+    """Scales 2^60 and 2^-60, the ends of their range: the tokens of the small one have 2^-9 of the others' weight each, and
+    together more than half of all."""
+    m, ratio = 128 * 400, 2.0 ** -9
+    k, v = torch.zeros(400, 128, 1, d), torch.full((400, 128, 1, d), 2.0)
+    k[0] = 1.0
+    vs = torch.full((400, 1), 2.0 ** -60, device=DEV)
+    vs[0] = 2.0 ** 60
+    out = attend_shared(torch.ones(n, 4, d, dtype=torch.bfloat16, device=DEV), codes(k), codes(v), torch.ones_like(vs), vs, batch, m, 9.0 * math.log(2.0) / d)
+    want = 2.0 ** 61 / (1.0 + 399 * ratio)  # the small values themselves are far below half a step of that
+    # the result's and a weight's rounding, fp32 sums of 3200 steps
+    assert bool(((out.double() / want - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -11).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 1), (6, 3), (40, 1), (1, 640), (40, 320)])
+def test_a_page_of_large_values_and_no_weight(d, n, batch):
+    """The first page's scale is 2^60 and all others' 2^-60, but these have 2^125 of its weight for each token: their values are the
+    result, with what the first's add."""
+    m, below = 128 * 200, 125.0
+    k, v = torch.zeros(200, 128, 1, d), torch.full((200, 128, 1, d), 3.0)
+    k[1:] = 1.0
+    vs = torch.full((200, 1), 2.0 ** -60, device=DEV)
+    vs[0] = 2.0 ** 60
+    out = attend_shared(torch.ones(n, 4, d, dtype=torch.bfloat16, device=DEV), codes(k), codes(v), torch.ones_like(vs), vs, batch, m, below * math.log(2.0) / d)
+    want = 3.0 * 2.0 ** -60 + 3.0 * 2.0 ** (60 - below) / 199
+    # beside both roundings: scores up to 87 from fp32 sums of d products, off by (d + 8) 2^-24 of that, and fp32 sums of 1600 steps
+    assert bool(((out.double() / want - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * 87 + 2.0 ** -12).all())
