@@ -562,7 +562,8 @@ typedef struct tq_new_rows {
  *   - A pool of TQ_E4M3: for each block and head that gets tokens, the scale is the smallest power of two in
  *     [2^-60, 2^60] with which the largest finite value of the new tokens is at most 448 scales, and no less than the
  *     scale that the block has, if it holds earlier tokens of the request (its first new token is not its first); then the
- *     numbers of those are brought to the new scale. Values are rounded to nearest even; one past 448 scales becomes
+ *     numbers of those are brought to the new scale. A scale that the call did not write itself counts as tq_paged_attention8
+ *     counts it, and is rounded up to a power of two. Values are rounded to nearest even; one past 448 scales becomes
  *     that, NaN stays NaN. A block's scale is that of the tokens in it, so two requests must not extend one block.
  *     Base and strides of the pool: multiples of 16. One launch, or two where there are many queries.
  *   - Not served, with a status bit: ids outside [0, max_seqs) (TQ_DEV_ERR_SEQ_ID); starts that fall or pass n_rows, a

@@ -113,10 +113,6 @@ __device__ __forceinline__ int tile_kv(const AttnArgs& a, const Request& r, int 
 struct UnitScale {
   float k, log_v, inv_v;
 };
-__device__ __forceinline__ float clamp_scale(float s) {
-  constexpr float kLo = 8.67361737988403547205962240695953369140625e-19f;  // 2^-60
-  return fminf(fmaxf(s, kLo), 1.f / kLo);  // NaN: kLo
-}
 __device__ __forceinline__ UnitScale unit_scale(const AttnArgs& a, int block, int head) {
   UnitScale r = {1.f, 0.f, 1.f};
   if (block < a.outer) {

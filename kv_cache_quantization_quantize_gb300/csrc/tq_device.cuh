@@ -85,6 +85,12 @@ __device__ __forceinline__ uint8_t* page_addr(const LayerView& lv, int slot, int
   return lv.pages + ((size_t)blk * lv.Hkv + h) * lv.page_bytes;
 }
 
+// A scale of a cache of 8 bits as every kernel takes it: the nearest in [2^-60, 2^60], none (NaN, 0, negative) as the least.
+__device__ __forceinline__ float clamp_scale(float s) {
+  constexpr float kLo = 8.67361737988403547205962240695953369140625e-19f;  // 2^-60
+  return fminf(fmaxf(s, kLo), 1.f / kLo);
+}
+
 // Barrier `id` (1..15) over the first `threads` threads that reach it (a multiple of 32).
 __device__ __forceinline__ void named_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");

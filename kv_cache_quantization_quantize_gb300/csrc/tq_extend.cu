@@ -411,10 +411,10 @@ __device__ __forceinline__ float scale_of(float top) {
   const int e = (int)(u >> 23) - 127 - ((u & 0x7fffffu) <= 0x600000u ? 8 : 7);
   return __uint_as_float((uint32_t)(min(max(e, kLeast), kMost) + 127) << 23);
 }
-// The scale that a block has already; what is none counts as the least.
-__device__ __forceinline__ float held_scale(float s) {
-  constexpr float kLo = 8.67361737988403547205962240695953369140625e-19f;  // 2^-60
-  return s >= kLo && s <= 1.f / kLo ? s : kLo;
+// The smallest power of two that is at least s, a positive normal number (or 0, which stays).
+__device__ __forceinline__ float power_up(float s) {
+  const uint32_t u = __float_as_uint(s);
+  return __uint_as_float(u & 0x7fffffu ? (u & 0x7f800000u) + 0x800000u : u);
 }
 
 template <int N>
@@ -555,8 +555,8 @@ __device__ void pages_part(const PagesArgs& p) {
           top = largest<2 * CH>(x[k], top);
         }
       }
-      const float held = at0 ? held_scale(*scale_at(w, h)) : 0.f;
-      const float scale = fmaxf(held, scale_of(warp_max(top))), by = 1.f / scale;
+      const float held = at0 ? clamp_scale(*scale_at(w, h)) : 0.f;  // a caller's need not be a power of two
+      const float scale = fmaxf(power_up(held), scale_of(warp_max(top))), by = 1.f / scale;
       if (at0 && scale > held) rescale<D>(to, a.o_row[1 + w], at0, held / scale, lane, 32);
 #pragma unroll
       for (int k = 0; k < kWarpPasses; ++k) {
@@ -641,10 +641,10 @@ __device__ void pages_part(const PagesArgs& p) {
       buf ^= 1;
       return top;
     };
-    const float held = at0 ? held_scale(*scale_at(w, h)) : 0.f;
+    const float held = at0 ? clamp_scale(*scale_at(w, h)) : 0.f;
     float top = top_of([](const float (&x)[2 * CH], float t) { return largest_any<2 * CH>(x, t); }, true);
     if (top == INFINITY) top = top_of([](const float (&x)[2 * CH], float t) { return largest<2 * CH>(x, t); }, false);
-    const float scale = fmaxf(held, scale_of(top)), by = 1.f / scale;
+    const float scale = fmaxf(power_up(held), scale_of(top)), by = 1.f / scale;
     if (at0 && scale > held) rescale<D>(to, a.o_row[1 + w], at0, held / scale, threadIdx.x, kThreads);
 #pragma unroll
     for (int k = 0; k < kPasses; ++k) {

@@ -120,3 +120,30 @@ def test_a_page_of_large_values_and_no_weight(d, n, batch):
     want = 3.0 * 2.0 ** -60 + 3.0 * 2.0 ** (60 - below) / 199
     # beside both roundings: scores up to 87 from fp32 sums of d products, off by (d + 8) 2^-24 of that, and fp32 sums of 1600 steps
     assert bool(((out.double() / want - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * 87 + 2.0 ** -12).all())
+
+
+# ---- appends ----
+
+@pytest.mark.parametrize("stored", [1.25 * 2.0 ** -3, 1.75 * 2.0 ** 9, 3.0 * 2.0 ** -61, 2.0 ** 70, math.inf, math.nan, 0.0, -1.0, 2.0 ** -70, 1.5 * 2.0 ** 60])
+@pytest.mark.parametrize("had,new", [(5, 3), (100, 60)])
+def test_extend_keeps_what_a_callers_scale_stands_for(stored, had, new):
+    """A partly filled page with a scale that extend did not write: its numbers stand for what attention takes them for (a
+    scale outside [2^-60, 2^60] counts as the nearest of the two, none as the least), also behind the step."""
+    d, gen = 64, torch.Generator().manual_seed(3)
+    k = torch.randn((new, 2, d), generator=gen).to(torch.bfloat16).to(DEV)
+    held = torch.randn((3, 128, 2, d), generator=gen)
+    pools, scales = [codes(held) for _ in range(2)], [torch.full((3, 2), stored, device=DEV) for _ in range(2)]
+    before = pools[0][1, :had].float().double()
+    word = i32([0])
+    paged.extend(k, k, *pools, i32([[1, 2]]), None, i32([0, new]), i32([had + new]), k_scale=scales[0], v_scale=scales[1], status=word)
+    was = 2.0 ** -60 if not stored > 2.0 ** -60 else min(float(torch.tensor(stored)), 2.0 ** 60)
+    rounded = 2.0 ** math.ceil(math.log2(was))
+    assert word.item() == 0
+    for pool, scale in zip(pools, scales):
+        for h in range(2):
+            now = max(rounded, ref.scale_of(k[:min(new, 128 - had), h].abs().max().item()))
+            assert scale[1, h].item() == now
+            old = before[:, h] * (was / now)
+            assert bool(((pool[1, :had, h].float().double() - old).abs() <= ref.half_step8(old) * (1 + 2.0 ** -20)).all())
+            y = k[:min(new, 128 - had), h].double() / now
+            assert bool(((pool[1, had:min(had + new, 128), h].float().double() - y).abs() <= ref.half_step8(y)).all())
