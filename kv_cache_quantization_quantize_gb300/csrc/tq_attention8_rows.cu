@@ -57,13 +57,6 @@ __device__ __forceinline__ bool any_of(bool x) {
       : "memory");
   return r != 0;
 }
-// The product of k_attn_rows, kept in its place: a ring entry is given back behind it, so what it was read from has arrived.
-__device__ __forceinline__ void mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 // Token that column (or row) x of a group of 8 stands for: with rows of 128 bytes, neighbours are four apart, so that the loads of K,
 // of two tokens by eight lanes, meet no bank conflict.
 template <int D>
@@ -322,8 +315,8 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
                 const uint32_t b0 = e4m3_lo(w), b1 = e4m3_hi(w);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                  if constexpr (kChains == 2) mma8(x & 1 ? s2[t][n] : s[t][n], af[t], b0, b1);
-                  else mma8(s[t][n], af[t], b0, b1);
+                  if constexpr (kChains == 2) mma16816<false>(x & 1 ? s2[t][n] : s[t][n], af[t], b0, b1);
+                  else mma16816<false>(s[t][n], af[t], b0, b1);
                 }
               }
             }
@@ -337,8 +330,6 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
                 for (int i = 0; i < 4; ++i) s[t][n][i] += s2[t][n][i];
           }
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&empty[st]);
       }
       // masked scores are selected away, not added to: what stands behind a sequence can be NaN
       bool need = false;
@@ -432,6 +423,7 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
         need = false;  // no weight is above 1 now
       }
       if (left) break;
+      if (lane == 0) mbar_arrive(&empty[e % ST]);  // K: the weights that were made of it were stored before the barrier
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         l[t][0] += sum[t][0] * us.inv_v;
@@ -490,14 +482,17 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
                 const uint32_t x0 = e4m3_lo(x), y0 = e4m3_lo(y), x1 = e4m3_hi(x), y1 = e4m3_hi(y);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                  mma8(o[t][2 * c], ap[j][t], x0, y0);
-                  mma8(o[t][2 * c + 1], ap[j][t], x1, y1);
+                  mma16816<false>(o[t][2 * c], ap[j][t], x0, y0);
+                  mma16816<false>(o[t][2 * c + 1], ap[j][t], x1, y1);
                 }
               }
           }
         }
+        uint32_t used = 0;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) used |= bits_of(o[t]);
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&empty[st]);
+        if (ok && lane == 0) give_back(&empty[st], used, a.batch);
       }
     }
     if (left) break;

@@ -261,8 +261,6 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
                 for (int i = 0; i < 4; ++i) s[t][n][i] += s2[t][n][i];
           }
         }
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&empty[st]);
       }
       // masked scores are selected away, not added to: what stands behind a sequence can be NaN
       bool need = false;
@@ -341,6 +339,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
         need = false;  // no weight is above 1 now
       }
       if (left) break;
+      if (lane == 0) mbar_arrive(&empty[e % ST]);  // K: the weights that were made of it were stored before the barrier
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         l[t][0] += sum[t][0];
@@ -391,8 +390,11 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
                 }
           }
         }
+        uint32_t used = 0;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) used |= bits_of(o[t]);
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&empty[st]);
+        if (ok && lane == 0) give_back(&empty[st], used, a.batch);
       }
     }
     if (left) break;

@@ -6,6 +6,7 @@ import torch
 
 from kv_cache_quantization_quantize_gb300 import paged
 from tests import extend_reference as ref
+from tests import paged_reference
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -120,6 +121,35 @@ def test_a_page_of_large_values_and_no_weight(d, n, batch):
     want = 3.0 * 2.0 ** -60 + 3.0 * 2.0 ** (60 - below) / 199
     # beside both roundings: scores up to 87 from fp32 sums of d products, off by (d + 8) 2^-24 of that, and fp32 sums of 1600 steps
     assert bool(((out.double() / want - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * 87 + 2.0 ** -12).all())
+
+
+# ---- rings of tiles ----
+
+@pytest.mark.parametrize("dtype", HALVES + [E4M3])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [1, 8])
+def test_few_rows_read_their_own_tiles_every_time(dtype, d, n):
+    """Steady rings on every SM, over and over: an entry that TMA fills again before its last load has returned would show as another
+    result in some run."""
+    gen = torch.Generator(device=DEV).manual_seed(d + n)
+    batch, blocks = 96, 30
+    k, v = (torch.randn((blocks, 128, 2, d), generator=gen, device=DEV).to(dtype) for _ in range(2))
+    q = torch.randn((batch * n, 8, d), generator=gen, device=DEV).to(torch.bfloat16 if dtype is E4M3 else dtype)
+    table = torch.stack([torch.randperm(blocks, generator=gen, device=DEV) for _ in range(batch)]).to(torch.int32)
+    lens = torch.randint(2500, 128 * blocks + 1, (batch,), generator=gen, device=DEV).to(torch.int32)
+    starts = torch.arange(0, (batch + 1) * n, n, dtype=torch.int32, device=DEV)
+    one = {"k_scale": torch.ones(blocks, 2, device=DEV), "v_scale": torch.ones(blocks, 2, device=DEV)} if dtype is E4M3 else {}
+    outs = [paged.attention(q, k, v, table, None, starts, lens, max_q=n, **one) for _ in range(200)]
+    assert bool(outs[0].isfinite().all()) and sum(not torch.equal(outs[0], x) for x in outs) == 0
+    for b in (0, batch - 1):  # and they are right
+        m = int(lens[b])
+        kk, vv = (x.view(torch.uint8)[table[b].long()].view(x.dtype).float().flatten(0, 1)[:m] for x in (k, v))
+        vis = [m - n + i + 1 for i in range(n)]
+        if dtype is E4M3:
+            want, bound = ref.attention8(q[b * n:(b + 1) * n], kk, torch.ones(m, 2, device=DEV), vv, torch.ones(m, 2, device=DEV), vis, d ** -0.5)
+        else:
+            want, bound = paged_reference.attention(q[b * n:(b + 1) * n], kk, vv, vis, d ** -0.5)
+        assert bool(((outs[0][b * n:(b + 1) * n].double() - want).abs() <= bound).all())
 
 
 # ---- appends ----
