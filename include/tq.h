@@ -567,7 +567,8 @@ typedef struct tq_new_rows {
  *     that, NaN stays NaN. A block's scale is that of the tokens in it, so two requests must not extend one block.
  *     Base and strides of the pool: multiples of 16. One launch, or two where there are many queries.
  *   - Not served, with a status bit: ids outside [0, max_seqs) (TQ_DEV_ERR_SEQ_ID); starts that fall or pass n_rows, a
- *     total below the number of new rows or past max_pages pages (TQ_DEV_ERR_LENGTH); pages without a block in the
+ *     total below the number of new rows or past max_pages pages (TQ_DEV_ERR_LENGTH: where starts fall, other requests'
+ *     rows may go unserved too); pages without a block in the
  *     pool (TQ_DEV_ERR_BLOCK: the page's tokens alone).
  * batch in [0, 65535], at most 2^31 - 256 rows. The host reads no array; calls can be captured. */
 tq_status tq_paged_extend(const tq_kv* pool, const tq_scales* scales, const tq_new_rows* rows, const tq_rotary* rot,

@@ -237,6 +237,16 @@ __device__ __forceinline__ StepRequest step_request(const StepMap& m, int b, uin
   }
   return r;
 }
+// What is wrong with the requests is told apart from serving them: where starts fall or pass the rows, no row may lead to
+// the request that does so. The n-th of `ctas` CTAs takes its part, its last warps first (the first ones look for tokens).
+__device__ __forceinline__ void report_requests(const StepMap& m, uint32_t* status, int n, int ctas, int threads) {
+  if (!status || (int64_t)n * threads >= m.batch) return;
+  for (int64_t b = (int64_t)n * threads + threads - 1 - threadIdx.x; b < m.batch; b += (int64_t)ctas * threads) {
+    uint32_t err = 0;
+    step_request(m, (int)b, err);
+    report(status, err);
+  }
+}
 
 // =============================================================================================
 // Rows of queries, keys and values, rotated or copied: a CTA takes `per` tokens with all their heads, a thread 2 CH
@@ -265,7 +275,7 @@ constexpr int kRowsThreads = 256;
 constexpr int kMostPer = 32;
 
 template <typename T, int CH, bool VEC>
-__device__ void rows_part(const RowsArgs& a, int cta) {
+__device__ void rows_part(const RowsArgs& a, int cta, int ctas) {
   struct Token {
     int position, block, place;  // block: -1: no place; -2: the row is not served
   };
@@ -280,8 +290,8 @@ __device__ void rows_part(const RowsArgs& a, int cta) {
         t = {a.positions[row], -1, 0};
       } else if (a.map.batch > 0) {
         const int b = find_last(a.map.batch, row, [&](int at) { return a.map.starts[at]; });
-        uint32_t err = 0;
-        const StepRequest r = step_request(a.map, b, err);
+        uint32_t err = 0, bad = 0;  // of the request: report_requests
+        const StepRequest r = step_request(a.map, b, bad);
         if (r.n > 0 && row >= r.row0 && row < r.row0 + r.n) {
           const int at = r.first + (row - r.row0);
           t.position = a.positions ? a.positions[row] : at;
@@ -300,6 +310,7 @@ __device__ void rows_part(const RowsArgs& a, int cta) {
     }
     if (lane == 0) tokens[i] = t;
   }
+  if (ctas > 0) report_requests(a.map, a.status, cta, ctas, kRowsThreads);
   named_barrier(1, kRowsThreads);
   const int threads = a.d / (2 * CH);  // of one head
   const int groups = kRowsThreads / threads, g = threadIdx.x / threads, j = threadIdx.x - g * threads;
@@ -356,7 +367,7 @@ __device__ void rows_part(const RowsArgs& a, int cta) {
 template <typename T, int CH, bool VEC>
 __global__ void __launch_bounds__(kRowsThreads, 3) k_rotate_rows(const __grid_constant__ RowsArgs a) {
   pdl_wait();
-  rows_part<T, CH, VEC>(a, blockIdx.x);
+  rows_part<T, CH, VEC>(a, blockIdx.x, a.step ? gridDim.x : 0);
 }
 
 int rows_ctas(RowsArgs& a, int ch, int sms) {
@@ -505,21 +516,17 @@ __device__ void pages_part(const PagesArgs& p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int number = blockIdx.x / p.y, y = blockIdx.x - number * p.y;
   const int b = find_last(a.map.batch, number, [&](int i) { return (int64_t)(max(a.map.starts[i], 0) / kPage) + 2 * i; });
-  uint32_t err = 0;
-  const StepRequest r = step_request(a.map, b, err);
+  uint32_t bad = 0;  // report_requests
+  const StepRequest r = step_request(a.map, b, bad);
   const int nth = number - (max(a.map.starts[b], 0) / kPage + 2 * b);
-  const bool tells = threadIdx.x == 0 && y == 0;
-  if (r.n == 0 || nth < 0) {
-    if (tells && nth == 0) report(a.status, err);
-    return;
-  }
+  if (r.n == 0 || nth < 0) return;
   const int page = r.first / kPage + nth, total = r.first + r.n;
   if (page > (total - 1) / kPage) return;
   const int lo = max(r.first, page * kPage), n = min(total, (page + 1) * kPage) - lo, at0 = lo - page * kPage;
   const int row0 = r.row0 + lo - r.first;
   const int block = a.map.table[(int64_t)r.table_row * a.map.stride + page];
   if (block < 0 || block >= a.n_blocks) {
-    if (tells) report(a.status, TQ_DEV_ERR_BLOCK);
+    if (threadIdx.x == 0 && y == 0) report(a.status, TQ_DEV_ERR_BLOCK);
     return;
   }
   const int hkv = a.heads[1], items = 2 * hkv;
@@ -663,8 +670,13 @@ template <typename T, int D, int CH, bool VEC>
 __global__ void __launch_bounds__(PagesShape<D, CH, sizeof(T)>::kThreads, D == 256 ? 1 : 2) k_extend_pages(const __grid_constant__ PagesArgs p) {
   pdl_wait();
   const int queries = p.pages * p.y;
-  if ((int)blockIdx.x < queries) pages_part<T, D, CH, VEC>(p);
-  else if (threadIdx.x < kRowsThreads) rows_part<T, CH, VEC>(p.rows, blockIdx.x - queries);
+  if ((int)blockIdx.x < queries) {
+    pages_part<T, D, CH, VEC>(p);
+    // first by the CTAs of page number 1, which a step of single tokens leaves idle
+    report_requests(p.rows.map, p.rows.status, ((int)blockIdx.x < p.y ? (int)blockIdx.x + queries : (int)blockIdx.x) - p.y, queries, blockDim.x);
+  } else if (threadIdx.x < kRowsThreads) {
+    rows_part<T, CH, VEC>(p.rows, blockIdx.x - queries, 0);
+  }
 }
 
 template <typename T, int D, int CH, bool VEC>

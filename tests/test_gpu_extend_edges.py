@@ -154,6 +154,26 @@ def test_few_rows_read_their_own_tiles_every_time(dtype, d, n):
 
 # ---- appends ----
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, E4M3])
+@pytest.mark.parametrize("rows,starts,totals", [
+    (100, [500, 600], [100]), (100, [0, 100, 700], [100, 600]), (1000, [0, 1000, 10, 20], [1000, 0, 10]), (1000, [0, 1000, 10, 20], [1000, 700, 10]),
+    (300, [0, 300, 2, 300], [300, 3, 298]), (6, [0, 2, -5, 6], [2, 4, 6]), (6, [-3, 2, 6], [5, 4]), (40, [0] + [40] * 700 + [39, 40], [40] + [1] * 701),
+])
+def test_starts_that_fall_or_pass_the_rows_are_reported(dtype, rows, starts, totals):
+    batch, d = len(totals), 64
+    k = torch.randn(rows, 1, d, device=DEV).to(torch.bfloat16)
+    pools = [torch.zeros(16, 128, 1, d, dtype=torch.uint8 if dtype is E4M3 else dtype, device=DEV) for _ in range(2)]
+    if dtype is E4M3:
+        pools = [p.view(E4M3) for p in pools]
+    scales = {"k_scale": torch.ones(16, 1, device=DEV), "v_scale": torch.ones(16, 1, device=DEV)} if dtype is E4M3 else {}
+    table = torch.full((batch, 8), -1, dtype=torch.int32)
+    table[0], table[-1, :3] = torch.arange(8), torch.arange(8, 11)
+    table[1:-1] = 15
+    word = i32([0])
+    paged.extend(k, k, *pools, table.to(DEV), None, i32(starts), i32(totals), status=word, **scales)
+    assert word.item() == paged.TQ_DEV_ERR_LENGTH
+
+
 @pytest.mark.parametrize("stored", [1.25 * 2.0 ** -3, 1.75 * 2.0 ** 9, 3.0 * 2.0 ** -61, 2.0 ** 70, math.inf, math.nan, 0.0, -1.0, 2.0 ** -70, 1.5 * 2.0 ** 60])
 @pytest.mark.parametrize("had,new", [(5, 3), (100, 60)])
 def test_extend_keeps_what_a_callers_scale_stands_for(stored, had, new):
