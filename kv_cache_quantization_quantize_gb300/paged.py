@@ -275,7 +275,11 @@ class Rotary:
 def rotate(x, positions, rotary, out=None, inverse=False, stream=None):
     """x [tokens, heads, head_dim] (bf16, f16 or f32, any strides with contiguous channels) rotated to `positions` [tokens]
     (int32) by a Rotary (tq_rotate). inverse: the transposed rotation, which takes a gradient of the result to that of x. out: the
-    tensor to write, which may be x. Returns out."""
+    tensor to write, which may be x. Returns out. Where x requires a gradient the rotation is recorded; it takes no out then."""
+    if x.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise ValueError("out: a recorded rotation makes its result itself (torch.no_grad() records nothing)")
+        return _Recorded.apply(x, positions, rotary, inverse, stream)
     shape, dtype, index = x.shape, x.dtype, x.get_device()
     if len(shape) != 3 or dtype not in _DTYPES or index < 0:
         raise ValueError("x: expected a bf16, f16 or f32 CUDA tensor [tokens, heads, head_dim]")
@@ -286,6 +290,20 @@ def rotate(x, positions, rotary, out=None, inverse=False, stream=None):
         with on:
             return _rotate(x, shape, dtype, index, place, rot, out, inverse, raw)
     return _rotate(x, shape, dtype, index, place, rot, out, inverse, raw)
+
+
+class _Recorded(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, positions, rotary, inverse, stream):
+        ctx.save_for_backward(positions)
+        ctx.rotary, ctx.inverse = rotary, inverse
+        return rotate(x, positions, rotary, inverse=inverse, stream=stream)
+
+    @staticmethod
+    def backward(ctx, grad):
+        if grad.stride(2) != 1:
+            grad = grad.contiguous()
+        return rotate(grad, *ctx.saved_tensors, ctx.rotary, inverse=not ctx.inverse), None, None, None, None
 
 
 def _rotate(x, shape, dtype, index, place, rot, out, inverse, raw):
@@ -310,7 +328,7 @@ def extend(k, v, k_pool, v_pool, table, seq_ids, starts, totals, rotary=None, po
     map_blocks gives them. rotary: a Rotary (None: K is written as it is); positions: int32 [rows] to rotate by instead of
     the tokens' places. q: [rows, n_q_heads, head_dim] of k's type, rotated into q_out (which may be q; None: a new
     tensor, whose rows of no request are not written). k_scale, v_scale: float32 [n_blocks, n_kv_heads] of pools of
-    torch.float8_e4m3fn, which are kept up with the tokens. Returns q_out."""
+    torch.float8_e4m3fn, which are kept up with the tokens. Returns q_out. No gradient is recorded: for training, rotate()."""
     scaled = k_scale is not None or v_scale is not None
     index, pool, d, heads, _ = _pools(k_pool, v_pool, scaled)
     scales = _scales(k_scale, v_scale, index, k_pool.shape[0], heads)

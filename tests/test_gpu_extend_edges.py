@@ -197,3 +197,46 @@ def test_extend_keeps_what_a_callers_scale_stands_for(stored, had, new):
             assert bool(((pool[1, :had, h].float().double() - old).abs() <= ref.half_step8(old) * (1 + 2.0 ** -20)).all())
             y = k[:min(new, 128 - had), h].double() / now
             assert bool(((pool[1, had:min(had + new, 128), h].float().double() - y).abs() <= ref.half_step8(y)).all())
+
+
+# ---- gradients of a rotation ----
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_a_rotation_records_its_gradient(dtype, interleaved):
+    gen = torch.Generator().manual_seed(5)
+    x, g = (torch.randn((7, 5, 64), generator=gen).to(dtype).to(DEV) for _ in range(2))
+    at, r = i32([0, 5, 900, 31, 7, 131071, 2]), paged.Rotary(32, interleaved=interleaved, scaling="ramp", factor=4.0, first=1024)
+    for inverse in (False, True):
+        leaf = x.clone().requires_grad_()
+        y = paged.rotate(leaf, at, r, inverse=inverse)
+        assert torch.equal(y, paged.rotate(x, at, r, inverse=inverse)) and y.requires_grad
+        y.backward(g)
+        assert torch.equal(leaf.grad, paged.rotate(g, at, r, inverse=not inverse))
+        # a part of a wider projection, and a gradient without strides of its own
+        wide = torch.cat([x, x], 2).requires_grad_()
+        paged.rotate(wide[..., 64:], at, r, inverse=inverse).sum().backward()
+        assert torch.equal(wide.grad[..., 64:], paged.rotate(torch.ones_like(x), at, r, inverse=not inverse)) and not wide.grad[..., :64].any()
+    leaf = x.clone().requires_grad_()
+    twice = g.clone().requires_grad_()
+    grad, = torch.autograd.grad(paged.rotate(leaf, at, r), leaf, twice, create_graph=True)
+    grad.backward(x)
+    assert torch.equal(twice.grad, paged.rotate(x, at, r))
+    with torch.no_grad():
+        assert not paged.rotate(leaf, at, r).requires_grad
+        assert paged.rotate(leaf, at, r, out=torch.empty_like(x)).dtype is dtype
+    with pytest.raises(ValueError):
+        paged.rotate(leaf, at, r, out=torch.empty_like(x))
+
+
+def test_a_rotations_gradient_by_differences():
+    gen = torch.Generator().manual_seed(6)
+    x, g = (torch.randn((3, 2, 16), generator=gen, dtype=torch.float32).to(DEV) for _ in range(2))
+    at, r = i32([3, 77, 4000]), paged.Rotary(8, times=1.5)
+    leaf = x.clone().requires_grad_()
+    (paged.rotate(leaf, at, r) * g).sum().backward()
+    for element in [(0, 0, 0), (1, 1, 5), (2, 0, 12)]:
+        moved = x.clone()
+        moved[element] += 8.0  # the map is linear
+        slope = ((paged.rotate(moved, at, r).double() - paged.rotate(x, at, r).double()) * g.double()).sum() / 8.0
+        assert abs(slope.item() - leaf.grad[element].item()) <= 16 * 2.0 ** -22 * 12 * g.abs().max().item()
