@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
       const int lim_all = seen(a, r, a.div_g(min(g.f0 + t * 128, g.rows - 1)));
       const int u0 = g.u0;
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
-      float m = mine ? -INFINITY : kFar, l = 0.f;  // a row past the last never outgrows its maximum (or does so for nothing)
+      float m = mine ? -INFINITY : kFarLifted, l = 0.f;  // a row past the last never outgrows its maximum (or does so for nothing)
       float mv = 0.f;            // m's part of the values' scale: weights are 2^(s - m + log2 vs - mv)
       float ml = m, mlv = 0.f;   // what l is relative to (kPair; else m)
       for (int k = kPair ? (made ^ wg) & 1 : 0; k < n; k += kPair ? 2 : 1) {
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
         }
         const bool grew = (more || lower > 0.f) && m != -INFINITY;  // or its scale was lowered
         const float mu = mn == -INFINITY ? 0.f : mn, above = (us.log_v - mvn) + kLift;
-        const bool far = fabsf(mu) > kFar;
+        const bool far = fabsf(mu) > kFarLifted;
         const bool special = __any_sync(0xffffffffu, grew || far);
         // O_t is whole before it is rescaled, and P_t has been used before it is written again
         const int last = special ? j - 1 : Sh::kOwnP ? j - Sh::kBufs : -1;
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
             }
           }
         }
-        // s * scale - mu in one rounding is off by what mu was rounded by, the same for all tokens of the row. Past kFar it would
+        // s * scale - mu in one rounding is off by what mu was rounded by, the same for all tokens of the row. Past kFarLifted it would
         // leave the weights' range: there the scores are rounded as mu was, and then taken from it.
         const bool by_steps = special && __any_sync(0xffffffffu, far);
         if (by_steps) {

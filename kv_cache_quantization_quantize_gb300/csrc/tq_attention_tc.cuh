@@ -10,6 +10,9 @@ namespace {
 // Scores (times log2 e) past this are 2 and more apart in fp32 and take steps of their own: 8192 queries on as many tokens
 // took 253.2 us without them at D = 64 and take 254.1 (causal 142.8 and 144.7), 619 and 623 at D = 128, 204 at D = 256.
 constexpr float kFar = 16777216.f;
+// The same with weights in f16, 2^kLift times as large: a constant of the exponent, the maximum and some whole numbers, is off by
+// half at most up to here, so that a weight stays below 2^15.75; another power of two on, one of 2^15 could become infinite.
+constexpr float kFarLifted = 8388608.f;
 
 // Registers per thread from here on (executed by every warp of a warpgroup).
 template <int N>

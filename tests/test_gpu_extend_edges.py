@@ -123,6 +123,26 @@ def test_a_page_of_large_values_and_no_weight(d, n, batch):
     assert bool(((out.double() / want - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * 87 + 2.0 ** -12).all())
 
 
+FAR = [2.0 ** 23 - 3, 2.0 ** 24 - 14, 2.0 ** 24 - 9, 2.0 ** 24 - 6, 2.0 ** 24 - 4, 2.0 ** 24 - 2, 2.0 ** 24, 2.0 ** 24 + 4]
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 640), (40, 320)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_weights_stay_in_f16_at_far_scores_over_8_bits(dtype, d, n, batch, sign):
+    """Scores of +-2^23 to 2^24 (log2) where fp32 has steps of 1 and 2, of which later pages' are 6 to 8 above the first's, just below what moves
+    the reference: weights are at their largest. Steps of 2 leave the later pages 2^4 of the first's weight at least."""
+    k, v = torch.ones(6, 128, 1, d), torch.full((6, 128, 1, d), 2.0)
+    v[0] = 1.0
+    for far in FAR:
+        for above in (6.0, 7.0, 8.0):
+            ks, vs = torch.full((6, 1), 1.0 + sign * above / far, device=DEV), torch.ones(6, 1, device=DEV)
+            ks[0] = 1.0
+            out = attend_shared(torch.full((n, 4, d), float(sign), dtype=dtype, device=DEV), codes(k), codes(v), ks, vs, batch, 768, far * math.log(2.0) / d)
+            assert bool((out >= 1.9).all()) and bool((out <= 2.0).all())
+
+
 # ---- rings of tiles ----
 
 @pytest.mark.parametrize("dtype", HALVES + [E4M3])
