@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
             float w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              w[i] = exp2_fast(s[t][n][i] - mu[i >> 1]);
+              w[i] = BF16 ? exp2_fast(s[t][n][i] - mu[i >> 1]) : exp2_fast((s[t][n][i] - mu[i >> 1]) + kLift);
               sum[t][i >> 1] += w[i];
             }
 #pragma unroll

@@ -353,6 +353,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
     set_regs_inc<216>();
     // ---- softmax of tile t: a thread per row (kPair: of every other unit) ----
     constexpr bool kPair = Sh::kPair;
+    constexpr float kPast = BF16 ? kFar : kFarLifted;
     const int wg = warp >> 2, t = kPair ? 0 : wg, row_t = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 TMEM lanes
     const uint32_t ts = tmem + t * 128 + lanes, tp = tmem + Sh::kP + t * Sh::kPStep + lanes;
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
       const int lim_all = seen(a, r, a.div_g(min(g.f0 + t * 128, g.rows - 1)));
       const int u0 = g.u0;
       const int both = Sh::kTurns ? min(g.n_of[0], g.n_of[NT - 1]) : 0;
-      float m = mine ? -INFINITY : kFar, l = 0.f;  // a row past the last never outgrows its maximum (or does so for nothing)
+      float m = mine ? -INFINITY : kPast, l = 0.f;  // a row past the last never outgrows its maximum (or does so for nothing)
       float ml = m;  // what l is relative to (kPair; else m)
       for (int k = kPair ? (made ^ wg) & 1 : 0; k < n; k += kPair ? 2 : 1) {
         const int j = made + k, bi = t * Sh::kBufs + buf_of(j);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
         }
         const bool grew = mn != m && m != -INFINITY;
         float mu = mn == -INFINITY ? 0.f : mn;
-        const bool far = fabsf(mu) > kFar;
+        const bool far = fabsf(mu) > kPast;
         const bool special = __any_sync(0xffffffffu, grew || far);
         // O_t is whole before it is rescaled, and P_t has been used before it is written again
         const int last = special ? j - 1 : Sh::kOwnP ? j - Sh::kBufs : -1;
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
               tmem_st32(to + c, o);
             }
           }
-          // s * scale - mu in one rounding is off by what mu was rounded by, the same for all tokens of the row. Past kFar
+          // s * scale - mu in one rounding is off by what mu was rounded by, the same for all tokens of the row. Past kPast
           // it would leave the weights' range: there the scores are rounded as mu was, and then taken from it.
           if (__any_sync(0xffffffffu, far)) {
             const float back = 1.f / a.scale_log2;
@@ -529,7 +530,8 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           }
         }
         m = mn;
-        const float2 sc = make_float2(a.scale_log2, a.scale_log2), off = make_float2(-mu, -mu);
+        const float from = (BF16 ? 0.f : kLift) - mu;
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2), off = make_float2(from, from);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // the product with the first half of V starts while the second is made

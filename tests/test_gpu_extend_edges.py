@@ -72,6 +72,19 @@ def test_small_weights_beside_a_sink_are_kept_over_8_bits(dtype, d, n, batch):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 640), (6, 640), (40, 320)])
+def test_small_weights_beside_a_sink_are_kept_over_f16(d, n, batch):
+    """The same over the exact cache in f16, whose weights are f16 too."""
+    m, below = 32768, 25.5
+    k, v, scale = sink(m, d, 1, below)
+    out = attend_shared(torch.ones(n, 4, d, dtype=torch.float16, device=DEV), k.half().to(DEV), v.half().to(DEV), None, None, batch, m, scale)
+    w, total = 2.0 ** -below, 1.0 + (m - 1) * 2.0 ** -below
+    mass = v.double().sum((0, 1, 2)).to(DEV) / total
+    bound = w * mass * (2.0 ** -11 + 2.0 ** -11 + 2.0 ** -12) + 2.0 ** -32 * mass + 2.0 ** -25
+    assert bool(((out.double() - w * mass).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("n", [1, 6, 40])
 @pytest.mark.parametrize("m", [70, 9000])
 def test_results_past_f16_are_infinite(d, n, m):
@@ -140,6 +153,24 @@ def test_weights_stay_in_f16_at_far_scores_over_8_bits(dtype, d, n, batch, sign)
             ks, vs = torch.full((6, 1), 1.0 + sign * above / far, device=DEV), torch.ones(6, 1, device=DEV)
             ks[0] = 1.0
             out = attend_shared(torch.full((n, 4, d), float(sign), dtype=dtype, device=DEV), codes(k), codes(v), ks, vs, batch, 768, far * math.log(2.0) / d)
+            assert bool((out >= 1.9).all()) and bool((out <= 2.0).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 640), (40, 320)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_weights_stay_in_f16_at_far_scores_over_f16(d, n, batch, sign):
+    """The same over the exact cache in f16."""
+    v = torch.full((6, 128, 1, d), 2.0)
+    v[0] = 1.0
+    for far in FAR:
+        for above in (6.0, 7.0, 8.0):
+            k = torch.zeros(6, 128, 1, d)
+            k[..., 0], k[..., 1] = sign * 4096.0, sign * (far - 4096.0 * 4096.0) / 1024.0
+            k[1:, ..., 2] = above
+            q = torch.zeros(n, 4, d)
+            q[..., 0], q[..., 1], q[..., 2] = 4096.0, 1024.0, 1.0
+            out = attend_shared(q.half().to(DEV), k.half().to(DEV), v.half().to(DEV), None, None, batch, 768, math.log(2.0))
             assert bool((out >= 1.9).all()) and bool((out <= 2.0).all())
 
 
