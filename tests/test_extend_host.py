@@ -162,3 +162,23 @@ def test_python_refuses_tensors_of_the_host():
     with pytest.raises(ValueError):
         paged.extend(x, x, p, p, torch.zeros(1, 2, dtype=torch.int32), None, torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), k_scale=torch.ones(2, 1),
                      v_scale=torch.ones(2, 1))
+
+
+@pytest.mark.parametrize("dim,base,args,steps", [
+    # pairs that turn 32 times and once over 4096 tokens: 20.9 and 45.03, so 20 and 46; pair 32 is 0.01 (7 / 13 + 6 / 13 / 16)
+    (128, 10000.0, {"scaling": "ramp", "factor": 16.0, "first": 4096},
+     {0: 1.0, 19: 0.064938163157621132, 20: 0.056234132519034908, 21: 0.046940859997959401, 26: 0.018583361251098548, 32: 0.0056730769230769231,
+      40: 0.00088178896293156731, 45: 0.00015177160473182493, 46: 8.3345089510207752e-5, 47: 7.2173874043091136e-5, 63: 7.2173874043091136e-6}),
+    (64, 500000.0, {"scaling": "ramp", "factor": 4.0, "first": 8192},
+     {0: 1.0, 8: 0.037606030930863936, 9: 0.024955408670558693, 12: 0.0054694985529128318, 15: 0.0010655597684559827, 17: 0.00031282462345246008,
+      18: 0.00015569310547864899, 19: 0.00010331813749637912, 31: 7.5346453803479279e-7}),
+    # base 10000 * 8^(128 / 126); pair 32 is its -1/2-th power
+    (128, 10000.0, {"scaling": "base", "factor": 8.0},
+     {0: 1.0, 1: 0.83784800191880243, 17: 0.049409339820143031, 32: 0.0034776640481145739, 50: 0.00014396665531557265, 63: 1.4434774808618227e-5}),
+    (64, 500000.0, {"scaling": "base", "factor": 2.0},
+     {0: 1.0, 1: 0.64892804304100951, 11: 0.0085933394173298561, 16: 0.00098888246841342714, 25: 2.0179646705774344e-5, 31: 1.5069290760695856e-6}),
+])
+def test_angles_of_middle_pairs(dim, base, args, steps):
+    """Against numbers of the rules' definitions, in 60 digits."""
+    r = paged.Rotary(dim, base=base, device="cpu", **args)
+    assert {i: r.steps[i] for i in steps} == pytest.approx(steps, rel=1e-13)

@@ -7,6 +7,7 @@ import torch
 from kv_cache_quantization_quantize_gb300 import paged
 from tests import extend_reference as ref
 from tests import paged_reference
+from tests.test_gpu_extend import normal, place_requests, run_extend8, same, starts_of
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -248,6 +249,39 @@ def test_extend_keeps_what_a_callers_scale_stands_for(stored, had, new):
             assert bool(((pool[1, :had, h].float().double() - old).abs() <= ref.half_step8(old) * (1 + 2.0 ** -20)).all())
             y = k[:min(new, 128 - had), h].double() / now
             assert bool(((pool[1, had:min(had + new, 128), h].float().double() - y).abs() <= ref.half_step8(y)).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rd,layout", [(24, "plain"), (8, "fused"), (64, "odd"), (24, "odd")])
+@pytest.mark.parametrize("nq,kv", [([3, 1, 8], [130, 128, 300]), ([9, 40], [135, 140]), ([300], [500]), ([5, 700, 1], [5, 701, 400])])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_extend_of_8_bits_by_four_pairs_at_head_dim_64(dtype, rd, layout, nq, kv, heads_first):
+    """Pairs or addresses that do not allow eight pairs in 16 bytes, in short and long runs across pages."""
+    run_extend8(((nq, kv), 4, 3, 64, rd, layout, heads_first), dtype, 31)
+
+
+@pytest.mark.parametrize("d,hq", [(64, 20), (128, 8)])
+def test_queries_at_odd_addresses_beside_aligned_keys(d, hq):
+    """Queries of a launch of their own take another width than keys and values: the call's results are those of rotation and of a
+    call without queries."""
+    nq = [(9 << 20) // (hq * d) - 200, 150]
+    kv = [nq[0], 400]
+    gen = torch.Generator().manual_seed(d)
+    rows = sum(nq)
+    q = normal(gen, (rows, hq, d), torch.bfloat16, "odd")
+    k, v = (normal(gen, (rows, 2, d), torch.bfloat16) for _ in range(2))
+    table, slot, blocks = place_requests(nq, kv, 1)
+    args = (table, i32(slot), i32(starts_of(nq)), i32(kv))
+    r, at = paged.Rotary(d), torch.cat([torch.arange(m - n, m) for n, m in zip(nq, kv)]).to(torch.int32).to(DEV)
+    results = []
+    for queries in (q, None):
+        pools = [torch.zeros(blocks, 128, 2, d, dtype=torch.uint8, device=DEV).view(E4M3) for _ in range(2)]
+        scales = [torch.ones(blocks, 2, device=DEV) for _ in range(2)]
+        out = paged.extend(k, v, *pools, *args, rotary=r, q=queries, k_scale=scales[0], v_scale=scales[1])
+        if queries is not None:
+            assert torch.equal(out, paged.rotate(q, at, r))
+        results.append(pools + scales)
+    assert all(same(a, b) for a, b in zip(*results))
 
 
 # ---- gradients of a rotation ----
