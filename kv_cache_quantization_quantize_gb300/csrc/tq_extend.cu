@@ -734,7 +734,9 @@ cudaError_t launch_rows(RowsArgs& a, Width w, int sms, cudaStream_t s) {
   // heads of 128 53.8 and 49.4), and in fp32, whose vectors are 16 bytes all the same (rows into bf16 50.7 and 53.3)
   if (w == kEight && (sizeof(T) == 4 || a.all <= 4)) w = kFour;
   const int ctas = rows_ctas(a, w == kEight ? 8 : 4, sms);
-  if (w == kEight) return launch_pdl(k_rotate_rows<T, 8, true>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
+  if constexpr (sizeof(T) == 2) {
+    if (w == kEight) return launch_pdl(k_rotate_rows<T, 8, true>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
+  }
   if (w == kFour) return launch_pdl(k_rotate_rows<T, 4, true>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
   return launch_pdl(k_rotate_rows<T, 4, false>, dim3(ctas), dim3(kRowsThreads), 0, s, a);
 }
