@@ -17,7 +17,9 @@ namespace {
 // multiplied with, however far apart the scales of pages are.
 // Measured: 32 single tokens over 4096 to 8192, 32 heads on 8 of 128, 71.0 us, 5.4 TB/s (79 % of a copy: a unit's chain of
 // products, maximum and products is not all hidden by two CTAs); one over 32768 21.9 us, of which some 8 are the way to the
-// first load and the join; 16 requests of 8 drafts, tiles of 32 rows, 64 us (42 %, the chain).
+// first load and the join; 16 requests of 8 drafts, tiles of 32 rows, 65 us (42 %, the chain). At head_dim 64 a unit has half the bytes
+// and the same chain, exponentials and barrier: 64 single tokens over 4096 to 8192, 16 heads on 4, 52 us (57 %). 64 short
+// requests of 100 to 1000 tokens, 32 heads on 8 of 128, 28 us (35 %).
 // =============================================================================================
 constexpr int k8TileCost = 64;   // start and end of a tile, as one unit
 constexpr int k8MinPart = 64;    // no CTA gets less than that (2 requests of 100 to 1000 tokens: 15.2 us with 128, 10.9 so)

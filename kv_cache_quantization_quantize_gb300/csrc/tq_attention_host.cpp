@@ -216,7 +216,9 @@ tq_status check_queries(const tq_queries* q, const tq_kv* kv) {
 // small parts spread better: where the tensor cores' tiles would be few (kRowsEach rows for each SM; 32 heads on 8 of 128, 16 queries
 // over 1000 tokens 12.5 against 18.8 us, over 16000 32.6 against 38.9; 16 heads on 4 of 256 12.3 against 26.9 and 30.2 against
 // 43.9; but 8 requests of 128 34.8 against 19.5) and each CTA gets kUnitsEach units at most (120 queries over 4000 tokens, 13 units:
-// 46.8 against 40.3).
+// 46.8 against 40.3). The rule counts padded rows, so near its edge it loses some: two prompts of 100 tokens, 32 heads on 8 of 128, 18.5 us
+// so and 15.0 with the other kernel, 4 requests of 16 after 2000 27.4 and 24.7, one of 200 after 30 22.1 and 20.8; two
+// of 64 after 1000 at 64 channels 5 %.
 constexpr int kRowsEach = 32, kUnitsEach = 8;
 tq::AttnPlan plan_of(const tq_queries& q, const tq_kv& kv, int sms) {
   tq::AttnPlan p;

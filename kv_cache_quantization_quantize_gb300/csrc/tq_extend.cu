@@ -251,9 +251,11 @@ __device__ __forceinline__ void report_requests(const StepMap& m, uint32_t* stat
 // =============================================================================================
 // Rows of queries, keys and values, rotated or copied: a CTA takes `per` tokens with all their heads, a thread 2 CH
 // channels of one token, whose cosines and sines it makes once for all heads that it meets. Everything is read and written
-// once, and DRAM bounds it: 16384 rows of 32 heads of 128, a quarter of each turned, 49.7 us, 5.4 TB/s (80 % of a copy); 8 prompts
-// of 1024 to 3000 tokens into a pool of 16 bits with 32 query heads 71.3 us, 5.7 TB/s. A step of 128 tokens takes 3.7 us, a launch and
-// four dependent loads (request, table, rows, results).
+// once, and with many heads DRAM bounds it: 16384 rows of 32 heads of 128, a quarter of each turned, 49.8 us, 5.4 TB/s (80 % of a copy);
+// 8 prompts of 1024 to 3000 tokens into a pool of 16 bits with 32 query heads 71.8 us, 5.7 TB/s. With few heads angles are made for few
+// elements: the same bytes in 65536 rows of 8 heads of 128 66.9 us (59 %), 65536 rows of 2 heads of 256 43 us (46 %: issue slots 63 %
+// used, the stalls are waits for loads and for results). A step of 128 tokens takes 3.6 us, a launch and four dependent
+// loads (request, table, rows, results).
 // =============================================================================================
 struct RowsArgs {
   Rotation rot;
@@ -385,8 +387,9 @@ int rows_ctas(RowsArgs& a, int ch, int sms) {
 // of a head). Runs of up to kShort new tokens take a warp per item, longer ones the CTA. The rows stay in registers, as they
 // came, between the largest of them and their rounding, so that everything is read once; K is rotated twice for that, with
 // cosines and sines that a thread makes once for all heads and keeps in shared memory of its own (4 x 8 pairs: registers
-// would leave one CTA to an SM). Instructions bound it: 65536 tokens of 8 heads of 128 in bf16 81.6 us, 4.8 TB/s (70 % of a copy);
-// at head_dim 256, with one CTA to an SM, 68 %. A step of 128 tokens takes 6.3 us.
+// would leave one CTA to an SM). The 14 warps that fit an SM beside that memory bound it: 65536 tokens of 8 heads of 128 in bf16
+// 82 us, 4.8 TB/s (70 % of a copy) with issue slots half used; at head_dim 256, with one CTA to an SM, 66 %; at 64 58 %, with
+// queries 51 %. A step of 128 tokens takes 6.4 us.
 // Page j of request b has number starts[b] / 128 + 2 b + j: n new tokens touch at most n / 128 + 2 pages, so numbers
 // never meet, and a CTA finds its request from starts alone.
 // =============================================================================================

@@ -210,13 +210,14 @@ class Rotary:
     """Angles of rotary positions: pair i of the first rotary_dim channels of a head turns by steps[i] radians per position.
 
     The pairs are channels (i, i + rotary_dim / 2), or with `interleaved` (2 i, 2 i + 1). Without scaling, steps[i] =
-    base^(-2 i / rotary_dim). Scalings to contexts that are `factor` times longer than the `first` tokens of training:
-      "linear"  every step divided by factor
-      "base"    base * factor^(rotary_dim / (rotary_dim - 2)): the fastest pair stays, the slowest is divided by factor
+    base^(-2 i / rotary_dim). Scalings to contexts that are `factor` times longer than the `first` tokens of training (without one
+    of these, factor and first change nothing):
+      "linear"  every step divided by factor (position interpolation, Chen et al. 2023)
+      "base"    base * factor^(rotary_dim / (rotary_dim - 2)): the fastest pair stays, the slowest is divided by factor (NTK-aware scaling)
       "bands"   by how often a pair turns over `first` tokens: `high` times and more stays, `low` times and less is
-                divided by factor, between them in proportion
+                divided by factor, between them in proportion (model configurations publish it as rope type "llama3")
       "ramp"    in proportion over the pairs between those that turn `fast` and `slow` times over `first` tokens; cosines and sines
-                are multiplied by `times`, by default 0.1 ln(factor) + 1
+                are multiplied by `times`, by default 0.1 ln(factor) + 1 (YaRN, Peng et al. 2023; its ramp over whole pairs, fast 32 and slow 1)
     `times` multiplies cosines and sines with any scaling. Angles of other rules: Rotary.of(steps)."""
 
     def __init__(self, rotary_dim, base=10000.0, interleaved=False, scaling=None, factor=1.0, first=0, low=1.0, high=4.0, fast=32.0, slow=1.0,
