@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kRowsThreads, RowsShape<D, MT>::kCtas)
             if (base + U > lim_all) x = t0 + n * 8 + c2 + (i & 1) < lim[t][i >> 1] ? x : -INFINITY;
             top[t][i >> 1] = fmaxf(top[t][i >> 1], x);
           }
-        need |= top[t][0] > m[t][0] + kLazy || top[t][1] > m[t][1] + kLazy;
+        need |= top[t][0] - m[t][0] > kLazy || top[t][1] - m[t][1] > kLazy;  // a sum m + kLazy could round to more
       }
       float sum[MT][2];
       for (;;) {  // twice where a maximum outgrew its range: the code is not doubled, since a cold path costs its fetches

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(TcShape<D>::kThreads, 1)
           m = *m_other;
         }
         float mn = m;
-        if (mx > m + kLazy || m == -INFINITY) mn = fmaxf(m, mx);
+        if (mx - m > kLazy || m == -INFINITY) mn = fmaxf(m, mx);  // a sum m + kLazy could round to more
         if constexpr (kPair) {
           *m_own = mn;
           __syncwarp();

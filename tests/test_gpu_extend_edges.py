@@ -175,6 +175,28 @@ def test_weights_stay_in_f16_at_far_scores_over_f16(d, n, batch, sign):
             assert bool((out >= 1.9).all()) and bool((out <= 2.0).all())
 
 
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,batch", [(1, 640), (40, 320)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_scores_a_step_of_fp32_apart(dtype, d, n, batch, sign):
+    """Scores of 2^25 to 2^30 (log2) over the exact cache, later pages' one step of fp32 (2 to 64) above the first's: the values of the later
+    pages, with 1/6 of the first's weight for 5 pages at most."""
+    v = torch.full((6, 128, 1, d), 2.0)
+    v[0] = 1.0
+    for power in range(25, 31):
+        step = 2.0 ** (power - 23)
+        for odd in (0, 1):  # the parity of the last bit
+            k, q = torch.zeros(6, 128, 1, d), torch.zeros(n, 4, d)
+            k[..., 0], k[..., 1], k[1:, ..., 2] = sign * 1.25 * 2.0 ** 12, sign * odd * step, step
+            q[..., 0], q[..., 1], q[..., 2] = 2.0 ** (power - 12), 1.0, 1.0
+            if q.max() > 65504.0:
+                k[..., 0] *= 8.0
+                q[..., 0] /= 8.0
+            out = attend_shared(q.to(dtype).to(DEV), k.to(dtype).to(DEV), v.to(dtype).to(DEV), None, None, batch, 768, math.log(2.0))
+            assert bool((out >= 2.0 - 1.0 / 6).all()) and bool((out <= 2.0).all()), (power, odd)
+
+
 # ---- rings of tiles ----
 
 @pytest.mark.parametrize("dtype", HALVES + [E4M3])
