@@ -350,14 +350,14 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
           }
         // (apart: far scores have no room for the logarithm)
         need |= (top[t][0] - m[t][0]) + (us.log_v - mv[t][0]) > kLazy || (top[t][1] - m[t][1]) + (us.log_v - mv[t][1]) > kLazy;
-        need |= fmaxf(mv[t][0], mv[t][1]) - us.log_v > kApart;
+        need |= us.log_v - fmaxf(mv[t][0], mv[t][1]) < kThin;
       }
       float sum[MT][2];
       for (;;) {  // twice where a maximum or a scale left its range: the code is not doubled, since a cold path costs its fetches
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           const float mu[2] = {m[t][0] == -INFINITY ? 0.f : m[t][0], m[t][1] == -INFINITY ? 0.f : m[t][1]};
-          const float above[2] = {(us.log_v - mv[t][0]) + kLift, (us.log_v - mv[t][1]) + kLift};
+          float above[2] = {(us.log_v - mv[t][0]) + kLift, (us.log_v - mv[t][1]) + kLift};
           sum[t][0] = sum[t][1] = 0.f;
 #pragma unroll
           for (int n = 0; n < NS; ++n) {
@@ -400,16 +400,12 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
 #pragma unroll
             for (int i = 1; i < NW; ++i) mx = fmaxf(mx, sx[i][row]);
             alpha[x] = 1.f;
-            const float by = (m[t][x] - mx) + (mv[t][x] - us.log_v), lower = fmaxf((mv[t][x] - us.log_v) - kApart, 0.f);
-            if (by < lower) {
+            const float by = (m[t][x] - mx) + (mv[t][x] - us.log_v);
+            if (by < 0.f) {
               alpha[x] = exp2_fast(by);
               m[t][x] = mx;
               mv[t][x] = us.log_v;
-              l[t][x] *= alpha[x];
-            } else if (lower > 0.f) {
-              alpha[x] = exp2_fast(lower);
-              mv[t][x] -= lower;
-              l[t][x] *= alpha[x];
+              l[t][x] = rescaled(l[t][x], by);
             }
           }
           if (k > 0) {
@@ -421,6 +417,21 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
               o[t][i][3] *= alpha[1];
             }
           }
+        }
+        bool thin = false;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) thin |= us.log_v - fmaxf(mv[t][0], mv[t][1]) < kThin;
+        if (thin) {  // the unit's part of the statistic by exponentials of its own
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int n = 0; n < NS; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float mu = m[t][i >> 1];
+                l[t][i >> 1] += exp2_fast((s[t][n][i] - (mu == -INFINITY ? 0.f : mu)) + (kLift - mv[t][i >> 1]));
+              }
+          us.inv_v = 0.f;  // and nothing from the weights
         }
         need = false;  // no weight is above 1 now
       }
@@ -524,7 +535,7 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
         float sum = sx[0][row];
 #pragma unroll
         for (int i = 1; i < NW; ++i) sum += sx[i][row];
-        const float part = exp2_fast(mv[t][x]);  // parts of a tile go to the join relative to m alone
+        const float2 part = part_reference(m[t][x], mv[t][x], sum);
         const int ch = warp * (D / NW) + j4 * 4;  // channels 4 j .. 4 j + 3 of each chunk: even, odd, even, odd
         if (g.direct) {
           const float inv = sum > 0.f ? 1.f / sum : 0.f;
@@ -540,9 +551,9 @@ __global__ void __launch_bounds__(Rows8Shape<D, MT>::kThreads, Rows8Shape<D, MT>
 #pragma unroll
           for (int c = 0; c < NC; ++c)
             *reinterpret_cast<float4*>(po + c * 16) =
-                make_float4(o[t][2 * c][2 * x] * part, o[t][2 * c + 1][2 * x] * part, o[t][2 * c][2 * x + 1] * part, o[t][2 * c + 1][2 * x + 1] * part);
+                make_float4(o[t][2 * c][2 * x] * part.y, o[t][2 * c + 1][2 * x] * part.y, o[t][2 * c][2 * x + 1] * part.y, o[t][2 * c + 1][2 * x + 1] * part.y);
           if (warp == 0 && (lane & 3) == 0)
-            cut_ml<R>(a, gridDim.x, blockIdx.x, g.slot)[row] = make_float2(m[t][x], sum * part);
+            cut_ml<R>(a, gridDim.x, blockIdx.x, g.slot)[row] = make_float2(part.x, sum * part.y);
         }
       }
   }

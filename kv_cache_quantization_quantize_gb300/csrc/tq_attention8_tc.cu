@@ -507,19 +507,19 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           mv = m_other->y;
         }
         // the sum of both maxima's parts may outgrow theirs; far scores have no room for the logarithm, so it stays apart
-        const float lower = fmaxf((mv - us.log_v) - kApart, 0.f);
-        const bool more = (mx - m) + (us.log_v - mv) > (lower > 0.f ? -lower : kLazy);  // also where m is -inf and mx is not
-        const float mn = more ? mx : m, mvn = more ? us.log_v : mv - lower;
+        const bool more = (mx - m) + (us.log_v - mv) > kLazy;  // also where m is -inf and mx is not
+        const float mn = more ? mx : m, mvn = more ? us.log_v : mv;
         if constexpr (kPair) {
           *m_own = make_float2(mn, mvn);
           __syncwarp();
           if (lane == 0) mbar_arrive(&m_full[mine8]);
-          if (mn != ml || mvn != mlv) l *= exp2_fast((ml - mn) + (mlv - mvn));
+          if (mn != ml || mvn != mlv) l = rescaled(l, (ml - mn) + (mlv - mvn));
           ml = mn;
           mlv = mvn;
         }
-        const bool grew = (more || lower > 0.f) && m != -INFINITY;  // or its scale was lowered
-        const float mu = mn == -INFINITY ? 0.f : mn, above = (us.log_v - mvn) + kLift;
+        const bool grew = more && m != -INFINITY;
+        const float mu = mn == -INFINITY ? 0.f : mn, own = us.log_v - mvn, held = least_above(own, mx - mn), above = held + kLift;
+        const float inv_v = held == own ? us.inv_v : exp2_fast(-(held + mvn));
         const bool far = fabsf(mu) > kFarLifted;
         const bool special = __any_sync(0xffffffffu, grew || far);
         // O_t is whole before it is rescaled, and P_t has been used before it is written again
@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
         }
         if (special) {
           if (__any_sync(0xffffffffu, grew)) {
-            const float alpha = grew ? exp2_fast((m - mn) + (mv - mvn)) : 1.f;
-            if constexpr (!kPair) l *= alpha;
+            const float by = grew ? (m - mn) + (mv - mvn) : 0.f, alpha = exp2_fast(by);
+            if constexpr (!kPair) l = rescaled(l, by);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           ++turns;
         }
         const float2 all = add2(sum[0], sum[1]);
-        l += (all.x + all.y) * us.inv_v;
+        l += (all.x + all.y) * inv_v;
       }
       if (!ok) break;
       made += n;
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
           tc_fence_after();
           m = m_other->x;
           mv = m_other->y;
-          if (m != ml || mv != mlv) l *= exp2_fast((ml - m) + (mlv - mv));
+          if (m != ml || mv != mlv) l = rescaled(l, (ml - m) + (mlv - mv));
         }
         l_all[wg * 128] = l;
         __syncwarp();
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
       // where this part's result goes; then the next tile's queries, so that its scores are made under the end of
       // this one
       const bool direct = g.direct;
-      // a part of a tile goes to the join relative to m alone
-      const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : exp2_fast(mv);
+      const float2 part = part_reference(m, mv, l);
+      const float inv = direct ? (l > 0.f ? 1.f / l : 0.f) : part.y;
       // the rows of the warp's 32 that go out by this lane: 16 bytes of each piece of row (i 32 + lane) / kLanes
       constexpr int kLanes = Sh::kOutRow / 16;
       int64_t to_row[kLanes];
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(Tc8Shape<D>::kThreads, 1)
                            : (int64_t)(t * 128 + row) * D;
       }
       float* po = cut_o<T, D>(a, gridDim.x, blockIdx.x, g.slot);
-      if (!direct && (!kPair || wg == 0)) cut_ml<T>(a, gridDim.x, blockIdx.x, g.slot)[t * 128 + row_t] = make_float2(m, l * inv);
+      if (!direct && (!kPair || wg == 0)) cut_ml<T>(a, gridDim.x, blockIdx.x, g.slot)[t * 128 + row_t] = make_float2(part.x, l * inv);
       have = take(g);
       if (!ok) break;
       if (have) load_q();

@@ -396,10 +396,30 @@ constexpr float kLazy = 8.0f;
 // f16 has nothing below 2^-25, so without it a weight of 2^-25 of the row's largest would be lost, which 2^15 tokens
 // behind a first one that takes nearly all of the weight have; so it is 2^-32.
 constexpr float kLift = 7.0f;
-// Over 8 bits: the reference's scale is no more than 2^kApart above that of the unit at hand, or it is lowered, sums and statistic with it. Scales can be
-// 2^120 apart, and a weight below fp32's range (2^-126) would be lost to the statistic, which divides it by a scale that
-// small; and the statistic relative to a maximum's score alone, as the join takes it, could leave the range above.
-constexpr float kApart = 80.0f;
+// Over 8 bits a row's reference is the largest of s + log2 vs, and scales can be 2^120 apart. Three things keep the statistic, which
+// divides by the scale, inside fp32's range then:
+//   - Where a unit's scale over the reference's, `above` in powers of two, is below kThin, its part of the statistic is not made
+//     of its weights, which can be below fp32's range. The rows kernel takes exponentials of its own for it, behind its rare path. The tensor
+//     cores' kernel makes the weights with a larger `above`, no larger than makes the largest of them 2^-66 (x: its score over
+//     the reference's): so small they are 0 in f16 either way, and their sum is divided by what they were made with.
+//   - The statistic is rescaled in two steps.
+//   - A part of a tile goes to the join relative to m + mv and a power of two of its sum (below).
+constexpr float kThin = -80.0f;
+__device__ __forceinline__ float least_above(float above, float x) {
+  return above < kThin ? fmaxf(above, fminf(0.f, -66.f - x)) : above;
+}
+__device__ __forceinline__ float rescaled(float l, float by) {
+  const float half = exp2_fast(0.5f * by);
+  return l * half * half;
+}
+// Of a part with the reference m + mv and the statistic l: what it is relative to in the join, in one float, and the factor of its
+// sums. The rounding of that float, which far scores make large, goes into the factor.
+__device__ __forceinline__ float2 part_reference(float m, float mv, float l) {
+  if (m == -INFINITY) return make_float2(m, 1.f);  // it saw no token
+  const int e = min(max((int)(__float_as_uint(l) >> 23) - 127, 0), 60);
+  const float t = mv + (float)e, to = m + t;
+  return make_float2(to, exp2_fast(((m - to) + t) - (float)e));
+}
 
 }  // namespace
 }  // namespace tq

@@ -7,7 +7,7 @@ import torch
 from kv_cache_quantization_quantize_gb300 import paged
 from tests import extend_reference as ref
 from tests import paged_reference
-from tests.test_gpu_extend import normal, place_requests, run_extend8, same, starts_of
+from tests.test_gpu_extend import attend_inputs, check_attended, normal, place_requests, run_extend8, same, starts_of
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -135,6 +135,21 @@ def test_a_page_of_large_values_and_no_weight(d, n, batch):
     want = 3.0 * 2.0 ** -60 + 3.0 * 2.0 ** (60 - below) / 199
     # beside both roundings: scores up to 87 from fp32 sums of d products, off by (d + 8) 2^-24 of that, and fp32 sums of 1600 steps
     assert bool(((out.double() / want - 1.0).abs() <= 2.0 ** -8 + 2.0 ** -11 + 2 * (d + 8) * 2.0 ** -24 * 87 + 2.0 ** -12).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n,m", [(1, 700), (3, 9000), (8, 700), (60, 900), (200, 5000)])
+@pytest.mark.parametrize("loud", [1.0, 40.0])
+def test_scales_over_their_whole_range(d, n, m, loud):
+    """Each page's scale of values anywhere from 2^-60 to 2^60; with loud queries scores up to some 2^8 beside them."""
+    q, k, ks, v, vs, table, slot = attend_inputs([n, n], [m, m - 129], 8, 2, d, torch.bfloat16, False, 50 + n)
+    for seed in range(4):
+        gen = torch.Generator().manual_seed(seed)
+        vs = torch.exp2(torch.randint(-60, 61, vs.shape, generator=gen).float()).to(DEV)
+        if seed == 3:  # the two ends alone
+            vs = torch.where(torch.rand(vs.shape, generator=gen).to(DEV) < 0.5, 2.0 ** 60, 2.0 ** -60)
+        out = paged.attention(q * loud, k, v, table, i32(slot), i32([0, n, 2 * n]), i32([m, m - 129]), max_q=n, k_scale=ks, v_scale=vs)
+        check_attended(out, q * loud, k, ks, v, vs, table, slot, [n, n], [m, m - 129])
 
 
 FAR = [2.0 ** 23 - 3, 2.0 ** 24 - 14, 2.0 ** 24 - 9, 2.0 ** 24 - 6, 2.0 ** 24 - 4, 2.0 ** 24 - 2, 2.0 ** 24, 2.0 ** 24 + 4]
